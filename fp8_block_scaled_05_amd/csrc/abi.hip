@@ -31,12 +31,23 @@ bool ld_ok(int64_t ld, int64_t row) { return ld >= row && ld % 16 == 0; }
 constexpr int64_t kMaxOperandLd = int64_t(1) << 24;
 bool operand_ld_ok(int64_t ld, int64_t row) { return ld_ok(ld, row) && ld <= kMaxOperandLd; }
 
+// the head's calls: 256 rows of bf16 within 32-bit byte offsets
+constexpr int64_t kMaxHeadLd = int64_t(1) << 22;
+bool head_ld_ok(int64_t ld, int64_t row) { return ld_ok(ld, row) && ld <= kMaxHeadLd; }
+
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 int hip_status(hipError_t e) {
   if (e == hipSuccess) return FP8BS_OK;
   g_last_hip_error = static_cast<int>(e);
   return FP8BS_ERR_HIP;
+}
+
+// Rows of x, vocabulary and hidden size of the head's calls: row and
+// vocabulary numbers are kept in 32 bits.
+bool head_sizes_ok(int64_t M, int64_t V, int64_t K) {
+  return M >= 0 && M <= INT32_MAX && V > 0 && V <= INT32_MAX && K > 0 && K % kTile == 0 &&
+         K <= kMaxHeadLd;
 }
 
 size_t fused_q_bytes(int64_t M, int64_t K) { return round256(size_t(M) * size_t(K)); }
@@ -408,13 +419,52 @@ int fp8_block_gemm_bf16_noalloc(const uint16_t* a, int64_t lda, float* sa, int64
                          nullptr, 0, M, N, K, ws, FP8BS_NOALLOC_SCRATCH_BYTES, stream);
 }
 
+int bf16_linear_xent(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw,
+                     const int64_t* target, int64_t ignore_index, float* loss, float* lse,
+                     int64_t M, int64_t V, int64_t K, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+  if (!head_sizes_ok(M, V, K)) return FP8BS_ERR_SHAPE;
+  if (M == 0) return FP8BS_OK;
+  if (!x || !w || !target || !loss || !lse) return FP8BS_ERR_NULL;
+  if (!head_ld_ok(ldx, K) || !head_ld_ok(ldw, K) || !aligned(x, 16) || !aligned(w, 16) ||
+      !aligned(target, 8) || !aligned(loss, 4) || !aligned(lse, 4))
+    return FP8BS_ERR_LAYOUT;
+  if (!workspace || workspace_bytes < fp8bs::xent_workspace(M, V, K)) return FP8BS_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return FP8BS_ERR_LAYOUT;
+  return hip_status(fp8bs::launch_xent(x, ldx, w, ldw, target, ignore_index, loss, lse, M, V, K,
+                                       workspace, static_cast<hipStream_t>(stream)));
+}
+
+int bf16_linear_xent_backward(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw,
+                              const int64_t* target, int64_t ignore_index, const float* lse,
+                              const float* dloss, uint16_t* dx, int64_t lddx, uint16_t* dw,
+                              int64_t lddw, int64_t M, int64_t V, int64_t K, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  if (!head_sizes_ok(M, V, K)) return FP8BS_ERR_SHAPE;
+  if (!w || !dw || (M > 0 && (!x || !target || !lse || !dloss || !dx))) return FP8BS_ERR_NULL;
+  if (!head_ld_ok(ldw, K) || !ld_ok(lddw, K) || !aligned(w, 16) || !aligned(dw, 16))
+    return FP8BS_ERR_LAYOUT;
+  if (M > 0 && (!head_ld_ok(ldx, K) || !ld_ok(lddx, K) || !aligned(x, 16) || !aligned(dx, 16) ||
+                !aligned(target, 8) || !aligned(lse, 4) || !aligned(dloss, 4)))
+    return FP8BS_ERR_LAYOUT;
+  if (!workspace || workspace_bytes < fp8bs::xent_grad_workspace(M, V, K))
+    return FP8BS_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return FP8BS_ERR_LAYOUT;
+  return hip_status(fp8bs::launch_xent_backward(x, ldx, w, ldw, target, ignore_index, lse, dloss,
+                                                dx, lddx, dw, lddw, M, V, K, workspace,
+                                                static_cast<hipStream_t>(stream)));
+}
+
 size_t fp8bs_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int64_t G) {
-  (void)N;
   (void)G;
+  if (op == FP8BS_OP_XENT_BACKWARD && head_sizes_ok(M, N, K))
+    return fp8bs::xent_grad_workspace(M, N, K);
   if (M <= 0 || K <= 0) return 0;
   switch (op) {
     case FP8BS_OP_GEMM_BF16:
       return fused_q_bytes(M, K) + fused_s_bytes(M, K);
+    case FP8BS_OP_XENT:
+      return head_sizes_ok(M, N, K) ? fp8bs::xent_workspace(M, N, K) : 0;
     default:
       return 0;
   }

@@ -101,4 +101,17 @@ hipError_t launch_few_rows_gemm(const void* a, int64_t lda, float* sa, int64_t l
                                 int64_t ldc, bool out_bf16, int64_t M, int64_t N, int64_t K,
                                 hipStream_t stream);
 
+// Cross entropy of the bf16 head's logits (workspace: xent_workspace bytes),
+// and its gradients (xent_grad_workspace bytes; M may be 0).
+size_t xent_workspace(int64_t M, int64_t V, int64_t K);
+hipError_t launch_xent(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw,
+                       const int64_t* target, int64_t ignore, float* loss, float* lse, int64_t M,
+                       int64_t V, int64_t K, void* workspace, hipStream_t stream);
+size_t xent_grad_workspace(int64_t M, int64_t V, int64_t K);
+hipError_t launch_xent_backward(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw,
+                                const int64_t* target, int64_t ignore, const float* lse,
+                                const float* dloss, uint16_t* dx, int64_t lddx, uint16_t* dw,
+                                int64_t lddw, int64_t M, int64_t V, int64_t K, void* workspace,
+                                hipStream_t stream);
+
 }  // namespace fp8bs

@@ -1,0 +1,653 @@
+// Softmax cross entropy of the head's logits, with its gradients, for gfx950.
+//
+// With logits l(m, v) = x(m) . w(v) (bf16 operands, FP32 sums), the loss of row
+// m with target t is lse(m) - l(m, t), lse(m) = log sum_v exp l(m, v).  The
+// logits never reach memory:
+// - forward: the tiles of the product reduce their logits in registers to one
+//   (maximum, sum of exp(l - maximum)) pair per row and 16-row-tile column
+//   block, and one wave per row joins the pairs.
+// - backward: with P = exp(l - lse) and G = P - onehot(t), the gradients are
+//   dx(m) = dloss(m) sum_v G(m, v) w(v) and dw(v) = sum_m G(m, v) dloss(m) x(m).
+//   The vocabulary is taken in pieces: a piece's logits are rebuilt and left
+//   as G in bf16 in the workspace, then one launch forms the piece's dw and
+//   its part of dx (FP32, added up over the pieces in the workspace).
+//
+// Roundings.  G is rounded to bf16 (it feeds MFMAs) and carries no dloss, so
+// the target's entry, which dominates both gradients, keeps its value near
+// -1.  dx takes dloss in FP32 at the end.  dw takes it through x: with
+// c = max |dloss| its operand is bf16(x dloss / c), which is x itself where
+// dloss is one value for all rows (a mean or a sum), and c in FP32 at the end.
+//
+// Rows whose target is ignore_index (or outside [0, V)) carry no loss: they
+// are left out of all products (the rows that remain are packed together), so
+// they cost nothing and whatever they hold, NaN and infinities too, reaches
+// no output.
+
+#include "gemm_bf16.hpp"
+
+namespace fp8bs {
+
+namespace {
+
+using gemm16::kCol;
+using gemm16::kRow;
+using gemm16::kStep;
+using gemm16::Operand;
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Large tiles, and the tile of few rows.  q are the rows of x, p the
+// vocabulary.
+using LogitsCfg = gemm16::Cfg<256, 256, 2, 4, 2, kRow, kRow>;
+using LogitsFewCfg = gemm16::Cfg<128, 64, 4, 1, 4, kRow, kRow>;
+// dx: q rows, p hidden, k vocabulary.  dw: q vocabulary, p hidden, k rows.
+using DxCfg = gemm16::Cfg<256, 256, 2, 4, 2, kCol, kRow>;
+using DwCfg = gemm16::Cfg<256, 256, 2, 4, 2, kCol, kCol>;
+
+constexpr int64_t kTile = 256;
+constexpr int64_t kFewXentRows = 64;
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// What the row pass leaves for the others.
+struct Header {
+  int32_t rows;     // rows with a loss
+  int32_t uniform;  // dloss is one value over those rows (backward)
+  float c;          // max |dloss| (1 where that is 0 or not finite)
+};
+
+struct Rows {
+  Header* h;
+  int32_t* index;  // packed row -> row
+  int32_t* place;  // row -> packed row, or -1
+  int32_t* target; // of the packed rows
+  float* lse;      // of the packed rows (backward)
+  float* dloss;    // of the packed rows (backward)
+};
+
+// One workgroup: packs the rows with a loss, in order.
+__global__ __launch_bounds__(1024) void xent_rows_kernel(const int64_t* target, int64_t M,
+                                                         int64_t V, int64_t ignore, Rows r,
+                                                         const float* lse, const float* dloss,
+                                                         float* loss_out, float* lse_out) {
+  __shared__ int32_t count[16];
+  __shared__ float red[2][16];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  int32_t base = 0;
+  float top = 0.0f, low = INFINITY, high = -INFINITY;
+  bool nan = false;
+  for (int64_t m0 = 0; m0 < M; m0 += 1024) {
+    const int64_t m = m0 + threadIdx.x;
+    const int64_t t = m < M ? target[m] : ignore;
+    const bool valid = m < M && t != ignore && t >= 0 && t < V;
+    const unsigned long long mask = __ballot(valid);
+    __syncthreads();
+    if (lane == 0) count[wave] = __popcll(mask);
+    __syncthreads();
+    int32_t at = base, all = 0;
+    for (int w = 0; w < 16; ++w) {
+      at += w < wave ? count[w] : 0;
+      all += count[w];
+    }
+    base += all;
+    at += __popcll(mask & ((1ull << lane) - 1ull));
+    if (valid) {
+      r.index[at] = (int32_t)m;
+      r.target[at] = (int32_t)t;
+      if (dloss) {
+        const float d = dloss[m];
+        r.lse[at] = lse[m];
+        r.dloss[at] = d;
+        top = fmaxf(top, fabsf(d));
+        low = fminf(low, d);
+        high = fmaxf(high, d);
+        nan = nan || d != d;
+      }
+    }
+    if (m < M) {
+      r.place[m] = valid ? at : -1;
+      if (loss_out && !valid) loss_out[m] = lse_out[m] = 0.0f;
+    }
+  }
+  if (dloss) {
+    top = max_wave64(top);
+    high = max_wave64(high);
+    low = -max_wave64(-low);
+    nan = __any(nan);
+    __syncthreads();
+    if (lane == 0) {
+      red[0][wave] = top;
+      red[1][wave] = !nan && (low == high || low > high) ? low : NAN;  // low > high: no rows
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      bool same = true;
+      float v = INFINITY;
+      top = 0.0f;
+      for (int w = 0; w < 16; ++w) {
+        top = fmaxf(top, red[0][w]);
+        const float x = red[1][w];
+        if (x == INFINITY) continue;  // a wave without rows
+        same = same && x == x && (v == INFINITY || v == x);
+        v = x;
+      }
+      r.h->c = top > 0.0f && top < INFINITY ? top : 1.0f;
+      r.h->uniform = same && fabsf(v) == top && v > 0.0f ? 1 : 0;
+    }
+  }
+  if (threadIdx.x == 0) r.h->rows = base;
+}
+
+// Packs the rows of x, one wave per packed row, zeros up to a multiple of 64
+// rows (the last k-step of dw's product); xs (backward, dloss not uniform):
+// the rows times dloss / c.
+__global__ __launch_bounds__(256) void xent_pack_kernel(const uint16_t* x, int64_t ldx, int64_t M,
+                                                        int64_t K, Rows r, uint16_t* xc,
+                                                        uint16_t* xs) {
+  const int64_t q = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  const int64_t rows = r.h->rows, upto = (rows + kStep - 1) / kStep * kStep;
+  const bool scaled = xs != nullptr && !r.h->uniform;
+  // all rows, as they are: used in place
+  if (q >= upto || (rows == M && (xs == nullptr || (rows == upto && !scaled)))) return;
+  const bool real = q < rows;
+  const uint16_t* src = x + (real ? (int64_t)r.index[q] : 0) * ldx;
+  const float f = scaled && real ? r.dloss[q] / r.h->c : 1.0f;
+  for (int64_t k = lane * 8; k < K; k += 512) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (real) v = *reinterpret_cast<const u32x4*>(src + k);
+    *reinterpret_cast<u32x4*>(xc + q * K + k) = v;
+    if (scaled) {
+      u32x4 w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = bf16x2_rne(bf16_lo(v[e]) * f, bf16_hi(v[e]) * f);
+      *reinterpret_cast<u32x4*>(xs + q * K + k) = w;
+    }
+  }
+}
+
+// Tile (pt, qt) number i of a raster of PT x QT tiles: 8 p-tiles x all
+// q-tiles, in blocks of 8 x 4, before the next 8 p-tiles.
+__device__ __forceinline__ void raster(int64_t i, int64_t PT, int64_t QT, int64_t& pt,
+                                       int64_t& qt) {
+  constexpr int64_t GP = 8, GQ = 4;
+  const int64_t p0 = i / (GP * QT) * GP, r = i % (GP * QT);
+  const int64_t gp = PT - p0 < GP ? PT - p0 : GP;
+  const int64_t q0 = r / (GQ * gp) * GQ, rr = r % (GQ * gp);
+  const int64_t gq = QT - q0 < GQ ? QT - q0 : GQ;
+  qt = q0 + rr % gq;
+  pt = p0 + rr / gq;
+}
+
+template <class C>
+__device__ __forceinline__ void clear(gemm16::Acc<C>& acc) {
+#pragma unroll
+  for (int i = 0; i < C::FP; ++i)
+#pragma unroll
+    for (int j = 0; j < C::FQ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+}
+
+struct LossArgs {
+  const uint16_t* x;
+  int64_t ldx;
+  const uint16_t* xc;  // packed rows, row stride K (null: few rows, not packed)
+  const uint16_t* w;
+  int64_t ldw;
+  int64_t M, V, K;
+  Rows r;
+  const int64_t* target;  // few rows: of the rows themselves
+  float2* part;           // [rows][blocks]: maximum, sum
+  int64_t blocks;         // pairs per row
+  float* at;              // logit of each row's target
+};
+
+// Forward: one tile of logits -> the rows' pairs over each wave's TP columns.
+template <class C, bool FEW>
+__global__ __launch_bounds__(C::THREADS) void xent_loss_kernel(LossArgs a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  FP8BS_GEMM16_STAGES(C);
+  const int64_t rows = FEW ? a.M : a.r.h->rows;
+  const int64_t PT = (a.V + C::BP - 1) / C::BP, QT = (rows + C::BQ - 1) / C::BQ;
+  if ((int64_t)blockIdx.x >= PT * QT) return;  // whole workgroup
+  int64_t pt, qt;
+  raster(gemm::xcd_remap(blockIdx.x, PT * QT), PT, QT, pt, qt);
+  const int64_t p0 = pt * C::BP, q0 = qt * C::BQ;
+  const bool direct = FEW || rows == a.M;
+  const uint16_t* x = direct ? a.x : a.xc;
+  const int64_t ldx = direct ? a.ldx : a.K;
+  const Operand op{a.w + p0 * a.ldw, a.ldw, (int)(a.V - p0 < C::BP ? a.V - p0 : C::BP), 0};
+  const Operand oq{x + q0 * ldx, ldx, (int)(rows - q0 < C::BQ ? rows - q0 : C::BQ), 0};
+  gemm16::Acc<C> acc;
+  clear<C>(acc);
+  gemm16::product<C>(op, oq, a.K / kStep, stages, acc);
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  const int wp = wave / C::WQ, wq = wave % C::WQ;
+  const int64_t pw = p0 + wp * C::TP;  // the wave's first column
+  if (pw >= a.V) return;
+  const int64_t left = a.V - pw;
+  const int n = left < C::TP ? (int)left : C::TP;  // its valid columns
+#pragma unroll
+  for (int j = 0; j < C::FQ; ++j) {
+    const int64_t q = q0 + wq * C::TQ + 16 * j + l16;
+    const bool real = q < rows;
+    float m = -INFINITY;
+    if (n == C::TP) {
+#pragma unroll
+      for (int i = 0; i < C::FP; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) m = fmaxf(m, acc[i][j][r]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < C::FP; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if (gemm16::p_of<C>(i, g) + r >= n) acc[i][j][r] = -INFINITY;
+          m = fmaxf(m, acc[i][j][r]);
+        }
+    }
+    m = fmaxf(m, __shfl_xor(m, 16, 64));
+    m = fmaxf(m, __shfl_xor(m, 32, 64));
+    // a block of -inf logits alone has no sum
+    const float b = m == -INFINITY ? 0.0f : -m * kLog2e;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < C::FP; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, b));
+    s += __shfl_xor(s, 16, 64);
+    s += __shfl_xor(s, 32, 64);
+    if (real && g == 0) a.part[q * a.blocks + pw / C::TP] = make_float2(m, s);
+    // the target's logit, on the one lane that holds it
+    int64_t t = -1;
+    if (real) t = FEW ? a.target[q] : (int64_t)a.r.target[q];
+    const int64_t d = t - pw;
+    if (__any(d >= 0 && d < n)) {
+#pragma unroll
+      for (int i = 0; i < C::FP; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (d == gemm16::p_of<C>(i, g) + r) a.at[q] = acc[i][j][r];
+    }
+  }
+#endif
+}
+
+// One wave per (packed) row: joins its pairs.
+template <bool FEW>
+__global__ __launch_bounds__(256) void xent_join_kernel(LossArgs a, int64_t ignore, float* loss,
+                                                        float* lse) {
+  const int64_t q = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  const int64_t rows = FEW ? a.M : a.r.h->rows;
+  if (q >= rows) return;
+  const float2* p = a.part + q * a.blocks;
+  float m = -INFINITY, s = 0.0f;
+  for (int64_t b = lane; b < a.blocks; b += 64) {
+    const float2 v = p[b];
+    const float top = fmaxf(m, v.x);
+    // -inf - -inf: a pair without a sum adds nothing
+    s = (m == -INFINITY ? 0.0f : s * __builtin_amdgcn_exp2f((m - top) * kLog2e)) +
+        (v.x == -INFINITY ? v.y : v.y * __builtin_amdgcn_exp2f((v.x - top) * kLog2e));
+    m = top;
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const float m2 = __shfl_xor(m, d, 64), s2 = __shfl_xor(s, d, 64);
+    const float top = fmaxf(m, m2);
+    s = (m == -INFINITY ? s : s * __builtin_amdgcn_exp2f((m - top) * kLog2e)) +
+        (m2 == -INFINITY ? s2 : s2 * __builtin_amdgcn_exp2f((m2 - top) * kLog2e));
+    m = top;
+  }
+  if (lane != 0) return;
+  if constexpr (FEW) {
+    const int64_t t = a.target[q];
+    if (t == ignore || t < 0 || t >= a.V) {
+      loss[q] = lse[q] = 0.0f;
+      return;
+    }
+  }
+  const float l = m + logf(s);
+  const int64_t row = FEW ? q : (int64_t)a.r.index[q];
+  lse[row] = l;
+  loss[row] = l - a.at[q];
+}
+
+struct GradArgs {
+  const uint16_t* x;
+  int64_t ldx;
+  const uint16_t *xc, *xs;  // packed rows, and those times dloss / c
+  const uint16_t* w;
+  int64_t ldw;
+  int64_t M, V, K;
+  Rows r;
+  uint16_t* g;      // [rows, whole tiles][ldg] of the piece
+  int64_t ldg;      // columns of a piece, a multiple of 256
+  int64_t v0, nv;   // the piece's vocabulary [v0, v0 + nv)
+  float* dxp;       // FP32 parts of dx, [splits][M][K]
+  int64_t splits;
+  uint16_t* dw;
+  int64_t lddw;
+};
+
+// Backward, first launch of a piece: logits rebuilt, G stored.  Rows past the
+// last and columns past the vocabulary are zeros up to whole tiles.
+template <class C>
+__global__ __launch_bounds__(C::THREADS) void xent_grad_logits_kernel(GradArgs a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  FP8BS_GEMM16_STAGES(C);
+  const int64_t rows = a.r.h->rows;
+  const int64_t PT = (a.nv + C::BP - 1) / C::BP, QT = (rows + C::BQ - 1) / C::BQ;
+  if ((int64_t)blockIdx.x >= PT * QT) return;  // whole workgroup
+  int64_t pt, qt;
+  raster(gemm::xcd_remap(blockIdx.x, PT * QT), PT, QT, pt, qt);
+  const int64_t p0 = pt * C::BP, q0 = qt * C::BQ;
+  const uint16_t* x = rows == a.M ? a.x : a.xc;
+  const int64_t ldx = rows == a.M ? a.ldx : a.K;
+  const Operand op{a.w + (a.v0 + p0) * a.ldw, a.ldw,
+                   (int)(a.nv - p0 < C::BP ? a.nv - p0 : C::BP), 0};
+  const Operand oq{x + q0 * ldx, ldx, (int)(rows - q0 < C::BQ ? rows - q0 : C::BQ), 0};
+  gemm16::Acc<C> acc;
+  clear<C>(acc);
+  gemm16::product<C>(op, oq, a.K / kStep, stages, acc);
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  const int wp = wave / C::WQ, wq = wave % C::WQ;
+  const int64_t pw = p0 + wp * C::TP;
+  const int64_t n = a.nv - pw;  // columns from pw on (<= 0: none)
+  static_assert(C::NI == 4, "runs of 16 columns per lane");
+#pragma unroll
+  for (int j = 0; j < C::FQ; ++j) {
+    const int64_t q = q0 + wq * C::TQ + 16 * j + l16;
+    const bool real = q < rows;
+    const float b = real ? -a.r.lse[q] * kLog2e : 0.0f;
+    const int64_t t = real ? (int64_t)a.r.target[q] - (a.v0 + pw) : -1;
+    uint16_t* dst = a.g + q * a.ldg + pw;
+#pragma unroll
+    for (int i4 = 0; i4 < C::FP; i4 += 4) {
+      uint32_t o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float f[2];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const int i = i4 + e / 2, r = 2 * (e & 1) + z;
+          const int p = gemm16::p_of<C>(i, g) + r;
+          float v = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, b));
+          v = t == p ? v - 1.0f : v;
+          f[z] = real && p < n ? v : 0.0f;
+        }
+        o[e] = bf16x2_rne(f[0], f[1]);
+      }
+      uint16_t* d = dst + gemm16::p_of<C>(i4, g);
+      *reinterpret_cast<u32x4*>(d) = u32x4{o[0], o[1], o[2], o[3]};
+      *reinterpret_cast<u32x4*>(d + 8) = u32x4{o[4], o[5], o[6], o[7]};
+    }
+  }
+#endif
+}
+
+// Backward, second launch of a piece: tiles of its part of dx (first, they are
+// the longer ones), then of its dw.
+template <class CX, class CW>
+__global__ __launch_bounds__(CX::THREADS) void xent_grad_kernel(GradArgs a, int first) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  static_assert(CX::STAGE_BYTES == CW::STAGE_BYTES && CX::STAGES == CW::STAGES &&
+                    CX::THREADS == CW::THREADS, "one workgroup shape");
+  FP8BS_GEMM16_STAGES(CX);
+  const int64_t rows = a.r.h->rows;
+  const int64_t PT = (a.K + CX::BP - 1) / CX::BP, QX = (rows + CX::BQ - 1) / CX::BQ;
+  const int64_t NX = PT * QX * a.splits, QW = (a.nv + CW::BQ - 1) / CW::BQ, NW = PT * QW;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  const int64_t bid = blockIdx.x;
+  if (bid < NX) {
+    using C = CX;
+    const int64_t i = gemm::xcd_remap(bid, NX);
+    const int64_t split = i / (PT * QX);
+    int64_t pt, qt;
+    raster(i % (PT * QX), PT, QX, pt, qt);
+    const int64_t p0 = pt * C::BP, q0 = qt * C::BQ;
+    const int64_t steps = (a.nv + kStep - 1) / kStep;
+    const int64_t s0 = steps * split / a.splits, s1 = steps * (split + 1) / a.splits;
+    const int64_t k0 = s0 * kStep;
+    const Operand op{a.w + (a.v0 + k0) * a.ldw + p0, a.ldw,
+                     (int)(a.K - p0 < C::BP ? a.K - p0 : C::BP), a.nv - k0};
+    // G holds whole tiles of rows
+    const Operand oq{a.g + q0 * a.ldg + k0, a.ldg, C::BQ, 0};
+    gemm16::Acc<C> acc;
+    clear<C>(acc);
+    gemm16::product<C>(op, oq, s1 - s0, stages, acc);
+    const int wp = wave / C::WQ, wq = wave % C::WQ;
+    float* out = a.dxp + split * a.M * a.K;
+#pragma unroll
+    for (int j = 0; j < C::FQ; ++j) {
+      const int64_t q = q0 + wq * C::TQ + 16 * j + l16;
+      if (q >= rows) continue;
+#pragma unroll
+      for (int i2 = 0; i2 < C::FP; ++i2) {
+        const int64_t p = p0 + wp * C::TP + gemm16::p_of<C>(i2, g);
+        if (p >= a.K) continue;
+        v4f* d = reinterpret_cast<v4f*>(out + q * a.K + p);
+        *d = first ? acc[i2][j] : *d + acc[i2][j];
+      }
+    }
+  } else if (bid - NX < NW) {
+    using C = CW;
+    int64_t pt, qt;
+    raster(gemm::xcd_remap(bid - NX, NW), PT, QW, pt, qt);
+    const int64_t p0 = pt * C::BP, q0 = qt * C::BQ;
+    const int64_t steps = (rows + kStep - 1) / kStep;
+    const bool direct = a.r.h->uniform && rows == a.M && rows % kStep == 0;
+    const uint16_t* x = direct ? a.x : a.r.h->uniform ? a.xc : a.xs;
+    const int64_t ldx = direct ? a.ldx : a.K;
+    const int64_t kr = steps * kStep;
+    const Operand op{x + p0, ldx, (int)(a.K - p0 < C::BP ? a.K - p0 : C::BP), kr};
+    const Operand oq{a.g + q0, a.ldg, C::BQ, kr};
+    gemm16::Acc<C> acc;
+    clear<C>(acc);
+    gemm16::product<C>(op, oq, steps, stages, acc);
+    const int wp = wave / C::WQ, wq = wave % C::WQ;
+    const float c = a.r.h->c;
+#pragma unroll
+    for (int j = 0; j < C::FQ; ++j) {
+      const int64_t q = q0 + wq * C::TQ + 16 * j + l16;
+      if (q >= a.nv) continue;
+#pragma unroll
+      for (int i = 0; i < C::FP; ++i) {
+        const int64_t p = p0 + wp * C::TP + gemm16::p_of<C>(i, g);
+        if (p >= a.K) continue;
+        const v4f v = acc[i][j] * c;
+        *reinterpret_cast<u32x2*>(a.dw + (a.v0 + q) * a.lddw + p) =
+            u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+      }
+    }
+  }
+#endif
+}
+
+// One wave per row of x: adds up its parts of dx (zeros for a row without a
+// loss).
+__global__ __launch_bounds__(256) void xent_dx_kernel(GradArgs a, uint16_t* dx, int64_t lddx) {
+  const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (m >= a.M) return;
+  const int64_t q = a.r.place[m];
+  const float d = q >= 0 ? a.r.dloss[q] : 0.0f;
+  for (int64_t k = lane * 4; k < a.K; k += 256) {
+    u32x2 o = {0u, 0u};
+    if (q >= 0) {
+      v4f s = *reinterpret_cast<const v4f*>(a.dxp + q * a.K + k);
+      for (int64_t z = 1; z < a.splits; ++z)
+        s += *reinterpret_cast<const v4f*>(a.dxp + (z * a.M + q) * a.K + k);
+      s = s * d;
+      o = u32x2{bf16x2_rne(s[0], s[1]), bf16x2_rne(s[2], s[3])};
+    }
+    *reinterpret_cast<u32x2*>(dx + m * lddx + k) = o;
+  }
+}
+
+// Workspace, in order; every part starts at a multiple of 256 bytes.
+struct Carver {
+  uint8_t* base;
+  size_t used = 0;
+  template <class T>
+  T* take(size_t n) {
+    T* p = reinterpret_cast<T*>(base + used);
+    used += (n * sizeof(T) + 255) & ~size_t(255);
+    return p;
+  }
+};
+
+Rows take_rows(Carver& c, int64_t M, bool grad) {
+  Rows r{};
+  r.h = c.take<Header>(1);
+  r.index = c.take<int32_t>(M);
+  r.place = c.take<int32_t>(M);
+  r.target = c.take<int32_t>(M);
+  if (grad) {
+    r.lse = c.take<float>(M);
+    r.dloss = c.take<float>(M);
+  }
+  return r;
+}
+
+struct LossPlan {
+  Rows r;
+  uint16_t* xc;
+  float2* part;
+  int64_t blocks;
+  float* at;
+  size_t bytes;
+};
+
+LossPlan loss_plan(void* ws, int64_t M, int64_t V, int64_t K) {
+  Carver c{static_cast<uint8_t*>(ws)};
+  LossPlan p{};
+  const bool few = M <= kFewXentRows;
+  p.blocks = few ? cdiv(V, LogitsFewCfg::TP) : cdiv(V, LogitsCfg::TP);
+  p.part = c.take<float2>(M * p.blocks);
+  p.at = c.take<float>(M);
+  if (!few) {
+    p.r = take_rows(c, M, false);
+    p.xc = c.take<uint16_t>(cdiv(M, kStep) * kStep * K);
+  }
+  p.bytes = c.used;
+  return p;
+}
+
+// The vocabulary is cut into equal pieces, whole tiles each, whose G takes at
+// most kPieceBytes, the size of the last-level cache, so that G is read back
+// from there.
+constexpr int64_t kPieceBytes = int64_t(256) << 20;
+
+struct GradPlan {
+  Rows r;
+  uint16_t *xc, *xs, *g;
+  int64_t ldg, pieces;
+  float* dxp;
+  int64_t splits;
+  size_t bytes;
+};
+
+GradPlan grad_plan(void* ws, int64_t M, int64_t V, int64_t K) {
+  Carver c{static_cast<uint8_t*>(ws)};
+  GradPlan p{};
+  const int64_t Mt = cdiv(M > 0 ? M : 1, kTile) * kTile;
+  int64_t most = kPieceBytes / (2 * Mt) / kTile * kTile;
+  most = most < kTile ? kTile : most;
+  p.pieces = cdiv(V, most);
+  p.ldg = cdiv(cdiv(V, p.pieces), kTile) * kTile;
+  p.pieces = cdiv(V, p.ldg);
+  // dx's tiles contract over the whole piece: cut that axis until a tile takes
+  // at most half of a compute unit's share of the launch
+  const int64_t tx = cdiv(M, kTile) * cdiv(K, kTile), sx = p.ldg / kStep;
+  const int64_t tw = p.ldg / kTile * cdiv(K, kTile), sw = cdiv(M, kStep) + 4;
+  p.splits = 1;
+  while (p.splits < 32 && sx / p.splits > 8 && 2 * 256 * (sx / p.splits) > tx * sx + tw * sw)
+    p.splits *= 2;
+  p.r = take_rows(c, M, true);
+  p.xc = c.take<uint16_t>(cdiv(M, kStep) * kStep * K);
+  p.xs = c.take<uint16_t>(cdiv(M, kStep) * kStep * K);
+  p.g = c.take<uint16_t>(Mt * p.ldg);
+  p.dxp = c.take<float>(p.splits * M * K);
+  p.bytes = c.used;
+  return p;
+}
+
+}  // namespace
+
+size_t xent_workspace(int64_t M, int64_t V, int64_t K) { return loss_plan(nullptr, M, V, K).bytes; }
+size_t xent_grad_workspace(int64_t M, int64_t V, int64_t K) {
+  return grad_plan(nullptr, M, V, K).bytes;
+}
+
+hipError_t launch_xent(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw,
+                       const int64_t* target, int64_t ignore, float* loss, float* lse, int64_t M,
+                       int64_t V, int64_t K, void* workspace, hipStream_t stream) {
+  const LossPlan p = loss_plan(workspace, M, V, K);
+  const LossArgs a{x, ldx, p.xc, w, ldw, M, V, K, p.r, target, p.part, p.blocks, p.at};
+  hipError_t e;
+  if (M <= kFewXentRows) {
+    using C = LogitsFewCfg;
+    e = launch_kernel(xent_loss_kernel<C, true>, dim3((unsigned)cdiv(V, C::BP)), dim3(C::THREADS),
+                      stream, a);
+    if (e != hipSuccess) return e;
+    return launch_kernel(xent_join_kernel<true>, dim3((unsigned)cdiv(M, 4)), dim3(256), stream, a,
+                         ignore, loss, lse);
+  }
+  using C = LogitsCfg;
+  const int64_t tiles = cdiv(V, C::BP) * cdiv(M, C::BQ);
+  if (tiles > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  e = launch_kernel(xent_rows_kernel, dim3(1), dim3(1024), stream, target, M, V, ignore, p.r,
+                    static_cast<const float*>(nullptr), static_cast<const float*>(nullptr), loss,
+                    lse);
+  if (e != hipSuccess) return e;
+  e = launch_kernel(xent_pack_kernel, dim3((unsigned)cdiv(cdiv(M, kStep) * kStep, 4)), dim3(256),
+                    stream, x, ldx, M, K, p.r, p.xc, static_cast<uint16_t*>(nullptr));
+  if (e != hipSuccess) return e;
+  e = launch_kernel(xent_loss_kernel<C, false>, dim3((unsigned)tiles), dim3(C::THREADS), stream, a);
+  if (e != hipSuccess) return e;
+  return launch_kernel(xent_join_kernel<false>, dim3((unsigned)cdiv(M, 4)), dim3(256), stream, a,
+                       ignore, loss, lse);
+}
+
+hipError_t launch_xent_backward(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw,
+                                const int64_t* target, int64_t ignore, const float* lse,
+                                const float* dloss, uint16_t* dx, int64_t lddx, uint16_t* dw,
+                                int64_t lddw, int64_t M, int64_t V, int64_t K, void* workspace,
+                                hipStream_t stream) {
+  const GradPlan p = grad_plan(workspace, M, V, K);
+  GradArgs a{x, ldx, p.xc, p.xs, w, ldw, M, V, K, p.r, p.g, p.ldg, 0, 0, p.dxp, p.splits, dw, lddw};
+  const int64_t MT = cdiv(M, kTile), KT = cdiv(K, kTile);
+  const int64_t t1 = MT * (p.ldg / kTile), t2 = KT * (MT * p.splits + p.ldg / kTile);
+  if (t1 > 0x7FFFFFFF || t2 > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  hipError_t e = launch_kernel(xent_rows_kernel, dim3(1), dim3(1024), stream, target, M, V, ignore,
+                               p.r, lse, dloss, static_cast<float*>(nullptr),
+                               static_cast<float*>(nullptr));
+  if (e != hipSuccess) return e;
+  if (M > 0) {
+    e = launch_kernel(xent_pack_kernel, dim3((unsigned)cdiv(cdiv(M, kStep) * kStep, 4)), dim3(256),
+                      stream, x, ldx, M, K, p.r, p.xc, p.xs);
+    if (e != hipSuccess) return e;
+  }
+  for (int64_t i = 0; i < p.pieces; ++i) {
+    a.v0 = i * p.ldg;
+    a.nv = V - a.v0 < p.ldg ? V - a.v0 : p.ldg;
+    if (M > 0) {
+      e = launch_kernel(xent_grad_logits_kernel<LogitsCfg>, dim3((unsigned)t1),
+                        dim3(LogitsCfg::THREADS), stream, a);
+      if (e != hipSuccess) return e;
+    }
+    e = launch_kernel(xent_grad_kernel<DxCfg, DwCfg>, dim3((unsigned)t2), dim3(DxCfg::THREADS),
+                      stream, a, i == 0 ? 1 : 0);
+    if (e != hipSuccess) return e;
+  }
+  if (M == 0) return hipSuccess;
+  return launch_kernel(xent_dx_kernel, dim3((unsigned)cdiv(M, 4)), dim3(256), stream, a, dx, lddx);
+}
+
+}  // namespace fp8bs

@@ -18,7 +18,8 @@ LIB_PATH = os.path.join(_PKG, "libfp8bs.so")
 OK, ERR_NULL, ERR_SHAPE, ERR_LAYOUT, ERR_DTYPE, ERR_WORKSPACE, ERR_HIP = range(7)
 OUT_F32, OUT_BF16 = 0, 1
 A_E4M3, A_BF16 = 0, 1
-OP_QUANT_ACT, OP_QUANT_W, OP_GEMM_E4M3, OP_GEMM_BF16, OP_GROUPED_GEMM = range(5)
+OP_QUANT_ACT, OP_QUANT_W, OP_GEMM_E4M3, OP_GEMM_BF16, OP_GROUPED_GEMM, OP_XENT, \
+    OP_XENT_BACKWARD = range(7)
 NOALLOC_SCRATCH_BYTES = 8 * 1024 * 1024  # FP8BS_NOALLOC_SCRATCH_BYTES
 DELAY_TILE, DELAY_TENSOR = 0, 1
 
@@ -36,6 +37,8 @@ EXPORTS = (
     "fp8_block_grouped_gemm_e4m3_out",
     "fp8_block_gemm_rowscaled",
     "fp8_block_kgrouped_gemm_rowscaled",
+    "bf16_linear_xent",
+    "bf16_linear_xent_backward",
     "fp8bs_workspace_bytes",
     "fp8bs_status_string",
     "fp8bs_last_hip_error",
@@ -69,6 +72,10 @@ _SIGNATURES = {
                                  _i64, _i64, _i64, _p, _sz, _p], _int),
     "fp8_block_grouped_gemm_e4m3_out": ([_p, _i64, _p, _i64, _p, _i64, _i64, _p, _p, _i64, _p,
                                          _i64, _p, _i64, _i64, _i64, _i64, _p, _sz, _p], _int),
+    "bf16_linear_xent": ([_p, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _i64, _i64, _p, _sz, _p],
+                         _int),
+    "bf16_linear_xent_backward": ([_p, _i64, _p, _i64, _p, _i64, _p, _p, _p, _i64, _p, _i64, _i64,
+                                   _i64, _i64, _p, _sz, _p], _int),
     "fp8bs_workspace_bytes": ([_int, _i64, _i64, _i64, _i64], _sz),
     "fp8bs_status_string": ([_int], ctypes.c_char_p),
     "fp8bs_last_hip_error": ([], _int),
@@ -592,3 +599,83 @@ def fp8_block_grouped_gemm_e4m3_out(a, sa, b, sb, group_offsets, qc=None, sc=Non
                                                    _stream(a)),
                "fp8_block_grouped_gemm_e4m3_out")
     return qc, sc
+
+
+def _vec(t, name, n, dtype):
+    """Check that ``t`` (if given) is a contiguous vector of at least ``n``."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 1 or t.shape[0] < n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of at least {n} entries, "
+                         f"got {list(t.shape)}")
+
+
+def _head_operands(where, x, w, target):
+    """Sizes of a call of the head after checking its operand tensors."""
+    _mat(x, "x", 0, 0, torch.bfloat16)
+    M, K = x.shape
+    _k_of(K, where)
+    V = w.shape[0] if w.dim() == 2 else -1
+    if V == 0:
+        raise ValueError("w must have at least one row")
+    _mat(w, "w", V, K, torch.bfloat16)
+    _vec(target, "target", M, torch.int64)
+    return M, V, K
+
+
+def _head_workspace(op, M, V, K, workspace, device):
+    if workspace is None:
+        workspace = torch.empty(workspace_bytes(op, M, V, K), dtype=torch.uint8, device=device)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def bf16_linear_xent(x, w, target, ignore_index=-100, loss=None, lse=None, workspace=None):
+    """Softmax cross entropy of the head's logits x . w^T, which are never
+    stored: bf16 x [M][K], w [V][K], int64 target [M] -> ``(loss, lse)``, fp32
+    [M] each, unreduced.
+
+    A row whose target is ``ignore_index`` or outside [0, V) has loss and lse
+    0, whatever its x holds.
+    """
+    M, V, K = _head_operands("bf16_linear_xent", x, w, target)
+    _vec(loss, "loss", M, torch.float32)
+    _vec(lse, "lse", M, torch.float32)
+    _need_device(x, w, target, loss, lse, workspace)
+    if loss is None:
+        loss = torch.empty(M, dtype=torch.float32, device=x.device)
+    if lse is None:
+        lse = torch.empty(M, dtype=torch.float32, device=x.device)
+    workspace, ws_bytes = _head_workspace(OP_XENT, M, V, K, workspace, x.device)
+    ldx = _rowmajor(x, "x") if M else K
+    with _on(x.device):
+        _check(lib.bf16_linear_xent(_ptr(x), ldx, _ptr(w), _ld(w), _ptr(target), ignore_index,
+                                    _ptr(loss), _ptr(lse), M, V, K, _ptr(workspace), ws_bytes,
+                                    _stream(x)), "bf16_linear_xent")
+    return loss, lse
+
+
+def bf16_linear_xent_backward(x, w, target, lse, dloss, ignore_index=-100, dx=None, dw=None,
+                              workspace=None):
+    """Gradients of ``bf16_linear_xent``: fp32 ``lse`` [M] of the forward call
+    and ``dloss`` [M] (the gradient of each row's loss) -> ``(dx, dw)``, bf16
+    [M][K] and [V][K].  The logits are rebuilt in pieces of the vocabulary."""
+    M, V, K = _head_operands("bf16_linear_xent_backward", x, w, target)
+    _vec(lse, "lse", M, torch.float32)
+    _vec(dloss, "dloss", M, torch.float32)
+    _mat(dx, "dx", M, K, torch.bfloat16)
+    _mat(dw, "dw", V, K, torch.bfloat16)
+    _need_device(x, w, target, lse, dloss, dx, dw, workspace)
+    if dx is None:
+        dx = torch.empty(M, K, dtype=torch.bfloat16, device=x.device)
+    if dw is None:
+        dw = torch.empty(V, K, dtype=torch.bfloat16, device=x.device)
+    workspace, ws_bytes = _head_workspace(OP_XENT_BACKWARD, M, V, K, workspace, x.device)
+    ldx = _rowmajor(x, "x") if M else K
+    with _on(x.device):
+        _check(lib.bf16_linear_xent_backward(
+            _ptr(x), ldx, _ptr(w), _ld(w), _ptr(target), ignore_index, _ptr(lse), _ptr(dloss),
+            _ptr(dx), _ld(dx), _ptr(dw), _ld(dw), M, V, K, _ptr(workspace), ws_bytes,
+            _stream(x)), "bf16_linear_xent_backward")
+    return dx, dw

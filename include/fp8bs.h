@@ -84,7 +84,9 @@ enum {
   FP8BS_OP_QUANT_W = 1,
   FP8BS_OP_GEMM_E4M3 = 2,
   FP8BS_OP_GEMM_BF16 = 3,
-  FP8BS_OP_GROUPED_GEMM = 4
+  FP8BS_OP_GROUPED_GEMM = 4,
+  FP8BS_OP_XENT = 5,
+  FP8BS_OP_XENT_BACKWARD = 6
 };
 
 /*
@@ -424,6 +426,58 @@ int fp8_block_grouped_gemm_e4m3_out(const uint8_t* a, int64_t lda,
                                     int64_t G, int64_t M_total, int64_t N,
                                     int64_t K, void* workspace,
                                     size_t workspace_bytes, void* stream);
+/*
+ * Softmax cross entropy of a bf16 head, without its logits: with
+ * l(m, v) = sum_k x(m, k) w(v, k) (FP32 sums of bf16 products),
+ *   lse[m] = log sum_v exp l(m, v),  loss[m] = lse[m] - l(m, target[m]).
+ * The head of FP8 mixed-precision training stays in bf16; the logits are
+ * reduced inside the product and never written.
+ *
+ *   x       [in]  bf16 [M][ldx], the last hidden states.
+ *   w       [in]  bf16 [V][ldw], the head's weight (V any size >= 1).
+ *   target  [in]  int64 [M].  A row whose target is ignore_index, or lies
+ *                 outside [0, V), carries no loss: loss and lse are 0 there
+ *                 and its x may hold anything, NaN and infinities too.
+ *   loss, lse [out] fp32 [M].  Non-finite logits give what the formulas give.
+ *   workspace  fp8bs_workspace_bytes(FP8BS_OP_XENT, M, V, K, 0) bytes,
+ *              256-byte aligned; free again when the call's work is done.
+ * The result does not depend on timing (no atomics).
+ * Errors: M < 0, V < 1, either above 2^31 - 1, K not a positive multiple of
+ *         128 or above 2^22 -> ERR_SHAPE; NULL -> ERR_NULL; ldx/ldw < K, not
+ *         a multiple of 16 or above 2^22, misaligned pointer -> ERR_LAYOUT;
+ *         workspace -> ERR_WORKSPACE.  M == 0 launches nothing.
+ */
+int bf16_linear_xent(const uint16_t* x, int64_t ldx, const uint16_t* w,
+                     int64_t ldw, const int64_t* target, int64_t ignore_index,
+                     float* loss, float* lse, int64_t M, int64_t V, int64_t K,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of bf16_linear_xent: with G(m, v) = exp(l(m, v) - lse[m]) -
+ * [v == target[m]] over the rows that carry a loss,
+ *   dx(m) = dloss[m] sum_v G(m, v) w(v),  dw(v) = sum_m dloss[m] G(m, v) x(m).
+ * The logits are rebuilt in pieces of the vocabulary; of a piece only G is
+ * kept, in bf16 (rounded to nearest even) in the workspace.
+ *
+ *   x, w, target, ignore_index  as bf16_linear_xent.
+ *   lse     [in]  fp32 [M], as the forward call left it.
+ *   dloss   [in]  fp32 [M], gradient of each row's loss.  It multiplies the
+ *                 finished sums of dx in FP32; dw takes bf16(x dloss / c) with
+ *                 c = max |dloss|, exact where dloss is one value.
+ *   dx      [out] bf16 [M][lddx]; zeros for a row without a loss.
+ *   dw      [out] bf16 [V][lddw], overwritten (all zeros for M == 0).
+ *   workspace  fp8bs_workspace_bytes(FP8BS_OP_XENT_BACKWARD, M, V, K, 0).
+ * Errors: as bf16_linear_xent; lddx/lddw < K or not a multiple of 16 ->
+ *         ERR_LAYOUT.
+ */
+int bf16_linear_xent_backward(const uint16_t* x, int64_t ldx,
+                              const uint16_t* w, int64_t ldw,
+                              const int64_t* target, int64_t ignore_index,
+                              const float* lse, const float* dloss,
+                              uint16_t* dx, int64_t lddx, uint16_t* dw,
+                              int64_t lddw, int64_t M, int64_t V, int64_t K,
+                              void* workspace, size_t workspace_bytes,
+                              void* stream);
 /* Workspace bytes an entry point needs for the given sizes (0 if none). */
 size_t fp8bs_workspace_bytes(int op, int64_t M, int64_t N, int64_t K,
                              int64_t G);
