@@ -150,7 +150,8 @@ namespace {
 int block_gemm_impl(int a_kind, const void* a, int64_t lda, float* sa, int64_t ldsa,
                     const uint8_t* b, int64_t ldb, const float* sb, void* c, int64_t ldc,
                     fp8bs::OutKind out, float* sc, int64_t ldsc, int64_t M, int64_t N,
-                    int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+                    int64_t K, void* workspace, size_t workspace_bytes, void* stream,
+                    const fp8bs::Epilogue* ep = nullptr) {
   if (a_kind != FP8BS_A_E4M3 && a_kind != FP8BS_A_BF16) return FP8BS_ERR_DTYPE;
   if (M < 0 || N < 0 || K <= 0 || K % kTile != 0) return FP8BS_ERR_SHAPE;
   if (out == fp8bs::kOutE4M3 && N % kTile != 0) return FP8BS_ERR_SHAPE;
@@ -178,7 +179,7 @@ int block_gemm_impl(int a_kind, const void* a, int64_t lda, float* sa, int64_t l
   if (bf16_a && M <= fp8bs::kFewRowsFused && out != fp8bs::kOutE4M3) {
     // very few rows: the weight-stream kernel quantizes A itself
     return hip_status(fp8bs::launch_few_rows_gemm(a, lda, sa, ldsa, true, b, ldb, sb, c, ldc,
-                                                  out == fp8bs::kOutBF16, M, N, K, st));
+                                                  out == fp8bs::kOutBF16, M, N, K, st, ep));
   }
 
   fp8bs::GemmArgs g{};
@@ -213,8 +214,32 @@ int block_gemm_impl(int a_kind, const void* a, int64_t lda, float* sa, int64_t l
   if (M <= fp8bs::kFewRows && out != fp8bs::kOutE4M3)
     return hip_status(fp8bs::launch_few_rows_gemm(g.a, g.lda, const_cast<float*>(g.sa), g.ldsa,
                                                   false, b, ldb, sb, c, ldc,
-                                                  out == fp8bs::kOutBF16, M, N, K, st));
+                                                  out == fp8bs::kOutBF16, M, N, K, st, ep));
+  if (ep) return hip_status(fp8bs::launch_block_gemm_epilogue(g, *ep, out, st));
   return hip_status(fp8bs::launch_block_gemm(g, out, st));
+}
+
+// The caller's epilogue of an M x N output, checked.
+int epilogue_of(const fp8bs_epilogue* in, int64_t M, int64_t N, fp8bs::Epilogue& e) {
+  if (!in) return FP8BS_ERR_NULL;
+  switch (in->act) {
+    case FP8BS_ACT_NONE: e.act = fp8bs::kActNone; break;
+    case FP8BS_ACT_RELU: e.act = fp8bs::kActRelu; break;
+    case FP8BS_ACT_SILU: e.act = fp8bs::kActSilu; break;
+    case FP8BS_ACT_GELU: e.act = fp8bs::kActGelu; break;
+    default: return FP8BS_ERR_DTYPE;
+  }
+  if (M > 0 && N > 0 &&
+      ((in->bias && !aligned(in->bias, 4)) ||
+       (in->residual && (in->ldr < N || !aligned(in->residual, 2))) ||
+       (in->z && (in->ldz < N || !aligned(in->z, 2)))))
+    return FP8BS_ERR_LAYOUT;
+  e.bias = in->bias;
+  e.residual = in->residual;
+  e.ldr = in->ldr;
+  e.z = in->z;
+  e.ldz = in->ldz;
+  return FP8BS_OK;
 }
 
 // Shared body of the grouped entry points.
@@ -304,6 +329,58 @@ int fp8_block_gemm_e4m3_out(int a_kind, const void* a, int64_t lda, float* sa, i
                             int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
   return block_gemm_impl(a_kind, a, lda, sa, ldsa, b, ldb, sb, qc, ldqc, fp8bs::kOutE4M3, sc,
                          ldsc, M, N, K, workspace, workspace_bytes, stream);
+}
+
+int fp8_block_gemm_epilogue(int a_kind, const void* a, int64_t lda, float* sa, int64_t ldsa,
+                            const uint8_t* b, int64_t ldb, const float* sb,
+                            const fp8bs_epilogue* epilogue, uint16_t* c, int64_t ldc, int64_t M,
+                            int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  fp8bs::Epilogue e{};
+  const int status = epilogue_of(epilogue, M, N, e);
+  if (status != FP8BS_OK) return status;
+  return block_gemm_impl(a_kind, a, lda, sa, ldsa, b, ldb, sb, c, ldc, fp8bs::kOutBF16, nullptr, 0,
+                         M, N, K, workspace, workspace_bytes, stream, &e);
+}
+
+int fp8_block_gemm_epilogue_e4m3_out(int a_kind, const void* a, int64_t lda, float* sa,
+                                     int64_t ldsa, const uint8_t* b, int64_t ldb, const float* sb,
+                                     const fp8bs_epilogue* epilogue, uint8_t* qc, int64_t ldqc,
+                                     float* sc, int64_t ldsc, int64_t M, int64_t N, int64_t K,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+  fp8bs::Epilogue e{};
+  const int status = epilogue_of(epilogue, M, N, e);
+  if (status != FP8BS_OK) return status;
+  return block_gemm_impl(a_kind, a, lda, sa, ldsa, b, ldb, sb, qc, ldqc, fp8bs::kOutE4M3, sc, ldsc,
+                         M, N, K, workspace, workspace_bytes, stream, &e);
+}
+
+int fp8_quant_epilogue_backward(const uint16_t* dy, int64_t lddy, const uint16_t* z, int64_t ldz,
+                                int act, int64_t M, int64_t N, uint8_t* q, int64_t ldq, float* s,
+                                int64_t lds, uint8_t* qt, int64_t ldqt, float* st, int64_t ldst,
+                                float* dbias, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  fp8bs::Epilogue e{};
+  const fp8bs_epilogue in{nullptr, nullptr, 0, nullptr, 0, act};
+  const int status = epilogue_of(&in, 0, 0, e);
+  if (status != FP8BS_OK) return status;
+  if (M < 0 || N < 0 || N % kTile != 0) return FP8BS_ERR_SHAPE;
+  if (M == 0 || N == 0) return FP8BS_OK;
+  const bool reads_z = e.act != fp8bs::kActNone;
+  if (!dy || (reads_z && !z) || !q || !s || !qt || !st || !dbias) return FP8BS_ERR_NULL;
+  const int64_t Mp = (M + kTile - 1) / kTile * kTile;
+  if (!ld_ok(lddy, N) || (reads_z && !ld_ok(ldz, N)) || !ld_ok(ldq, N) || lds < M ||
+      !ld_ok(ldqt, Mp) || ldst < N)
+    return FP8BS_ERR_LAYOUT;
+  if (!aligned(dy, 16) || (reads_z && !aligned(z, 16)) || !aligned(q, 16) || !aligned(s, 4) ||
+      !aligned(qt, 16) || !aligned(st, 4) || !aligned(dbias, 4))
+    return FP8BS_ERR_LAYOUT;
+  if (!workspace || workspace_bytes < fp8bs::epilogue_backward_workspace(M, N))
+    return FP8BS_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return FP8BS_ERR_LAYOUT;
+  return hip_status(fp8bs::launch_epilogue_backward(dy, lddy, z, ldz, e.act, M, N, q, ldq, s, lds,
+                                                    qt, ldqt, st, ldst, dbias, workspace,
+                                                    static_cast<hipStream_t>(stream)));
 }
 
 int fp8_block_gemm_rowscaled(const uint8_t* a, int64_t lda, const float* sa, int64_t ldsa,
@@ -459,6 +536,8 @@ size_t fp8bs_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int64_t G)
   (void)G;
   if (op == FP8BS_OP_XENT_BACKWARD && head_sizes_ok(M, N, K))
     return fp8bs::xent_grad_workspace(M, N, K);
+  if (op == FP8BS_OP_EPILOGUE_BACKWARD)
+    return M > 0 && N > 0 ? fp8bs::epilogue_backward_workspace(M, N) : 0;
   if (M <= 0 || K <= 0) return 0;
   switch (op) {
     case FP8BS_OP_GEMM_BF16:
@@ -476,7 +555,7 @@ const char* fp8bs_status_string(int status) {
     case FP8BS_ERR_NULL: return "a required pointer is NULL";
     case FP8BS_ERR_SHAPE: return "unsupported shape (negative size, K not a positive multiple of 128, or bad group count)";
     case FP8BS_ERR_LAYOUT: return "unsupported layout (leading dimension or pointer alignment)";
-    case FP8BS_ERR_DTYPE: return "unknown a_kind, out_kind or mode";
+    case FP8BS_ERR_DTYPE: return "unknown a_kind, out_kind, mode or act";
     case FP8BS_ERR_WORKSPACE: return "workspace missing or too small";
     case FP8BS_ERR_HIP: return "HIP launch failed";
     default: return "unknown status";

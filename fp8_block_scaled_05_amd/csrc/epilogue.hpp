@@ -1,0 +1,76 @@
+// Activations of the linear layer's epilogue, and their derivatives.
+//
+//   relu  max(z, 0)
+//   silu  z sigma(z)
+//   gelu  z sigma(2 u), u = c (z + 0.044715 z^3), c = sqrt(2 / pi): the tanh
+//         form 0.5 z (1 + tanh u), since 1 + tanh u = 2 sigma(2 u)
+// with sigma(x) = 1 / (1 + e^-x).  Derivatives (0 at z = 0 for relu):
+//   silu  s + z s (1 - s), s = sigma(z)
+//   gelu  s + z s (1 - s) 2 u', s = sigma(2 u), u' = c (1 + 3 * 0.044715 z^2)
+#pragma once
+
+#include "device.hpp"
+#include "internal.hpp"
+
+namespace fp8bs {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
+constexpr float kGeluA = 0.044715f;
+// |z| past which sigma(2 u) is 0 or 1 in FP32: z is clamped to it inside u, so
+// that z^3 stays finite
+constexpr float kGeluTop = 20.0f;
+
+// sigma(x) by the hardware exponential and reciprocal (each within 1 ulp; the
+// argument's rounding to |x| 2^-24 is what e^-x loses most): below bf16's
+// rounding by far for the epilogue's outputs.
+__device__ __forceinline__ float sigmoid_fast(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -kLog2e));
+}
+
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+  if constexpr (ACT == kActRelu) {
+    return z > 0.0f || z != z ? z : 0.0f;
+  } else if constexpr (ACT == kActSilu) {
+    return z * sigmoid_fast(z);
+  } else if constexpr (ACT == kActGelu) {
+    const float c = __builtin_amdgcn_fmed3f(z, -kGeluTop, kGeluTop);
+    return z * sigmoid_fast(2.0f * kGeluC * c * __builtin_fmaf(kGeluA * c, c, 1.0f));
+  } else {
+    return z;
+  }
+}
+
+// The derivative, with the correctly rounded-to-an-ulp exponential: its
+// results are quantized, and an error here moves values over a code's edge.
+template <int ACT>
+__device__ __forceinline__ float activate_grad(float z) {
+  if constexpr (ACT == kActRelu) {
+    return z > 0.0f ? 1.0f : 0.0f;
+  } else if constexpr (ACT == kActSilu) {
+    const float s = __builtin_amdgcn_rcpf(1.0f + expf(-z));
+    return __builtin_fmaf(z * s, 1.0f - s, s);
+  } else if constexpr (ACT == kActGelu) {
+    const float c = __builtin_amdgcn_fmed3f(z, -kGeluTop, kGeluTop);
+    const float u2 = 2.0f * kGeluC * c * __builtin_fmaf(kGeluA * c, c, 1.0f);
+    const float du2 = 2.0f * kGeluC * __builtin_fmaf(3.0f * kGeluA * c, c, 1.0f);
+    const float s = __builtin_amdgcn_rcpf(1.0f + expf(-u2));
+    return __builtin_fmaf(c * s * (1.0f - s), du2, s);
+  } else {
+    return 1.0f;
+  }
+}
+
+// f(std::integral_constant<int, act>) for the runtime act (wave-uniform).
+template <class F>
+__device__ __forceinline__ void with_activation(int act, F&& f) {
+  switch (act) {
+    case kActRelu: f(std::integral_constant<int, kActRelu>{}); break;
+    case kActSilu: f(std::integral_constant<int, kActSilu>{}); break;
+    case kActGelu: f(std::integral_constant<int, kActGelu>{}); break;
+    default: break;
+  }
+}
+
+}  // namespace fp8bs

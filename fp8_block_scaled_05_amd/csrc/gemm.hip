@@ -25,35 +25,12 @@
 namespace fp8bs {
 
 namespace {
-// BM, BN, waves along M, waves along N, LDS stages, tile-rows per L2 group
-using LargeCfg = gemm::Cfg<256, 256, 2, 4, 2, 4>;
-// half-height tiles: a last partial round of the dense raster, and groups'
-// last tile-rows of at most 128 rows
-using LargeTail = gemm::Cfg<128, 256, 2, 4, 2, 4>;
-using Rows32Cfg = gemm::Cfg<32, 32, 1, 2, 4, 1>;
-using Rows64Cfg = gemm::Cfg<64, 128, 1, 4, 4, 1>;
-
-// Tile shape for M > 64: the least estimated time, counted in rounds of
-// workgroups (one workgroup per compute unit), a round of 256x256, 128x256
-// and 64x128 (four-stage) tiles taking 100, 77 and 40 (relative times per
-// round at equal K, measured on MI355X with one or two rounds); the 256x256
-// launch runs a last partial round of at most half the compute units as
-// 128x256 tiles, half a round.
-enum class Tiles { kLarge, kHalf, kSmall };
-Tiles pick_tiles(const GemmArgs& a) {
-  const int64_t cus = gemm::device_cus();
-  if (cus <= 0) return Tiles::kLarge;
-  const int64_t tl = ((a.M + 255) / 256) * ((a.N + 255) / 256);
-  const int64_t th = ((a.M + 127) / 128) * ((a.N + 255) / 256);
-  const int64_t ts = ((a.M + 63) / 64) * ((a.N + 127) / 128);
-  const int64_t tail = tl % cus;
-  const int64_t cost_l =
-      100 * (tl / cus) + (tail == 0 ? 0 : (tl > cus && 2 * tail <= cus) ? 50 : 100);
-  const int64_t cost_h = 77 * ((th + cus - 1) / cus);
-  const int64_t cost_s = 40 * ((ts + cus - 1) / cus);
-  if (cost_l <= cost_h && cost_l <= cost_s) return Tiles::kLarge;
-  return cost_h <= cost_s ? Tiles::kHalf : Tiles::kSmall;
-}
+using gemm::LargeCfg;
+using gemm::LargeTail;
+using gemm::Rows32Cfg;
+using gemm::Rows64Cfg;
+using gemm::Tiles;
+using gemm::pick_tiles;
 }  // namespace
 
 hipError_t launch_block_gemm(const GemmArgs& args, OutKind out, hipStream_t stream) {

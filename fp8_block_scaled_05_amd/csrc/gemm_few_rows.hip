@@ -38,6 +38,7 @@
 // result to accumulation registers that each promotion must copy out first
 // (four extra VALU instructions per MFMA).
 
+#include "epilogue.hpp"
 #include "gemm_kernel.hpp"
 
 namespace fp8bs {
@@ -159,8 +160,35 @@ struct FewArgs {
   int out_bf16;
 };
 
-template <int RC, int MT, bool FUSED>
-__global__ __launch_bounds__(kWaves * 64) void few_rows_kteam_kernel(FewArgs p) {
+// Finishes and stores the lane's 4 consecutive outputs (m, n .. n + 3), of
+// which the first `left` exist (bf16 output).
+__device__ __forceinline__ void store_finished(const FewArgs& p, const Epilogue& e, int64_t m,
+                                               int64_t n, int left, v4f v) {
+  const bool whole = left >= 4;
+  const int some = left < 4 ? left : 4;
+  if (e.bias)
+    for (int r = 0; r < some; ++r) v[r] += e.bias[n + r];
+  auto store = [&](uint16_t* base, int64_t ld) {
+    uint16_t* dst = base + m * ld + n;
+    if (whole && reinterpret_cast<uintptr_t>(dst) % 8 == 0) {
+      *reinterpret_cast<u32x2*>(dst) = u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+    } else {
+      for (int r = 0; r < some; ++r) dst[r] = f32_to_bf16_rne(v[r]);
+    }
+  };
+  if (e.z) store(e.z, e.ldz);
+  with_activation(e.act, [&](auto act) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = activate<decltype(act)::value>(v[r]);
+  });
+  if (e.residual)
+    for (int r = 0; r < some; ++r)
+      v[r] += __uint_as_float((uint32_t)e.residual[m * e.ldr + n + r] << 16);
+  store(static_cast<uint16_t*>(p.c), p.ldc);
+}
+
+template <int RC, int MT, bool FUSED, bool EPI>
+__global__ __launch_bounds__(kWaves * 64) void few_rows_kteam_kernel(FewArgs p, Epilogue ep) {
 #if defined(__HIP_DEVICE_COMPILE__)
   using C = FewCfg<RC, MT, FUSED>;
   constexpr int RT = C::RT;
@@ -389,6 +417,10 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_kteam_kernel(FewArgs p) 
       const int nl = 16 * i + 4 * g;  // first of the lane's 4 output columns
       if (m >= p.M || nl >= nrows) continue;
       const int64_t n = row0 + nl;
+      if constexpr (EPI) {
+        store_finished(p, ep, m, n, nrows - nl, sum);
+        continue;
+      }
       if (p.out_bf16) {
         uint16_t* dst = static_cast<uint16_t*>(p.c) + m * p.ldc + n;
         if (vec && nl + 4 <= nrows) {
@@ -439,8 +471,8 @@ struct SharedCfg {
   static_assert((S - 2) * CPW <= 63, "vmcnt range");
 };
 
-template <int RC>
-__global__ __launch_bounds__(kWaves * 64) void few_rows_shared_kernel(FewArgs p) {
+template <int RC, bool EPI>
+__global__ __launch_bounds__(kWaves * 64) void few_rows_shared_kernel(FewArgs p, Epilogue ep) {
 #if defined(__HIP_DEVICE_COMPILE__)
   using C = SharedCfg<RC>;
   constexpr int RT = C::RT, S = C::S;
@@ -589,6 +621,10 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_shared_kernel(FewArgs p)
       if (nl >= nrows) continue;
       const int64_t n = row0 + nl;
       const v4f sum = acc[i];
+      if constexpr (EPI) {
+        store_finished(p, ep, m, n, nrows - nl, sum);
+        continue;
+      }
       if (p.out_bf16) {
         uint16_t* dst = static_cast<uint16_t*>(p.c) + m * p.ldc + n;
         if (vec && nl + 4 <= nrows) {
@@ -614,28 +650,31 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_shared_kernel(FewArgs p)
 // Weight rows per workgroup (RC 8-row copies): the fewest that put the
 // whole N on at most one workgroup per compute unit, from a fixed set.
 template <int MT, bool FUSED>
-hipError_t launch_mt(const FewArgs& p, int cus, hipStream_t stream) {
+hipError_t launch_mt(const FewArgs& p, const Epilogue* e, int cus, hipStream_t stream) {
   const int64_t per = (p.N + cus - 1) / cus;
   auto go = [&](auto RC_) {
     constexpr int RC = decltype(RC_)::value;
     const int64_t blocks = (p.N + 8 * RC - 1) / (8 * RC);
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED>, dim3((unsigned)blocks),
-                         dim3(kWaves * 64), stream, p);
+    const dim3 grid((unsigned)blocks), block(kWaves * 64);
+    if (e) return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, true>, grid, block, stream, p, *e);
+    return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, false>, grid, block, stream, p,
+                         Epilogue{});
   };
   if (per <= 8) return go(std::integral_constant<int, 1>{});
   if (per <= 24) return go(std::integral_constant<int, 3>{});
   return go(std::integral_constant<int, 9>{});
 }
 
-hipError_t launch_shared(const FewArgs& p, int cus, hipStream_t stream) {
+hipError_t launch_shared(const FewArgs& p, const Epilogue* e, int cus, hipStream_t stream) {
   const int64_t per = (p.N + cus - 1) / cus;
   auto go = [&](auto RC_) {
     constexpr int RC = decltype(RC_)::value;
     const int64_t blocks = (p.N + 8 * RC - 1) / (8 * RC);
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    return launch_kernel(few_rows_shared_kernel<RC>, dim3((unsigned)blocks), dim3(kWaves * 64),
-                         stream, p);
+    const dim3 grid((unsigned)blocks), block(kWaves * 64);
+    if (e) return launch_kernel(few_rows_shared_kernel<RC, true>, grid, block, stream, p, *e);
+    return launch_kernel(few_rows_shared_kernel<RC, false>, grid, block, stream, p, Epilogue{});
   };
   if (per <= 8) return go(std::integral_constant<int, 1>{});
   if (per <= 24) return go(std::integral_constant<int, 3>{});
@@ -647,17 +686,18 @@ hipError_t launch_shared(const FewArgs& p, int cus, hipStream_t stream) {
 hipError_t launch_few_rows_gemm(const void* a, int64_t lda, float* sa, int64_t ldsa, bool fused,
                                 const uint8_t* b, int64_t ldb, const float* sb, void* c,
                                 int64_t ldc, bool out_bf16, int64_t M, int64_t N, int64_t K,
-                                hipStream_t stream) {
+                                hipStream_t stream, const Epilogue* epilogue) {
   const FewArgs p{a, lda, sa, ldsa, b, ldb, sb, c, ldc, M, N, K, out_bf16 ? 1 : 0};
   const int cus = gemm::device_cus();
   if (cus <= 0) return hipErrorInvalidDevice;
+  if (epilogue && !out_bf16) return hipErrorInvalidValue;
   if (fused) {
     if (M > kFewRowsFused) return hipErrorInvalidValue;
-    return launch_mt<1, true>(p, cus, stream);
+    return launch_mt<1, true>(p, epilogue, cus, stream);
   }
-  if (M <= 16) return launch_mt<1, false>(p, cus, stream);
-  if (M <= 32) return launch_mt<2, false>(p, cus, stream);
-  if (M <= kFewRows) return launch_shared(p, cus, stream);
+  if (M <= 16) return launch_mt<1, false>(p, epilogue, cus, stream);
+  if (M <= 32) return launch_mt<2, false>(p, epilogue, cus, stream);
+  if (M <= kFewRows) return launch_shared(p, epilogue, cus, stream);
   return hipErrorInvalidValue;
 }
 

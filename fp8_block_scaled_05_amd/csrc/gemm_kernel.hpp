@@ -728,9 +728,18 @@ __device__ __forceinline__ void store_tile_e4m3(const GemmArgs& p, const TileCoo
   }
 }
 
-template <class C, int OUT>
+// Epilogue of the plain product: the FP32 sums are stored as they are.
+struct NoEpilogue {
+  template <class C>
+  __device__ __forceinline__ void apply(const GemmArgs&, const TileCoords&,
+                                        v4f (&)[C::FM][C::FN], int, int, int) const {}
+};
+
+// ep.apply<C>(p, t, acc, wm, wn, lane) may change a wave's finished sums
+// before they are stored.
+template <class C, int OUT, class E = NoEpilogue>
 __device__ __forceinline__ void block_gemm_body(const GemmArgs& p, const TileCoords& t,
-                                                const LdsSet& L) {
+                                                const LdsSet& L, const E& ep = E()) {
   // wave index in an SGPR so that per-wave values stay scalar
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
@@ -846,6 +855,7 @@ __device__ __forceinline__ void block_gemm_body(const GemmArgs& p, const TileCoo
     }
   }
 
+  ep.template apply<C>(p, t, acc, wm, wn, lane);
   if constexpr (OUT == kOutE4M3) {
     store_tile_e4m3<C>(p, t, acc, wm, wn, lane, L.red, L.rcp);
   } else {
@@ -876,8 +886,8 @@ __device__ __forceinline__ void store_zero_tile(const GemmArgs& p, const TileCoo
 // most TAIL::BM rows.  TAIL == C: no half tiles.
 // The buffer-resource type exists only for the device; the host pass sees an
 // empty kernel (it only needs the launch stub).
-template <class C, class TAIL, int SCHED, int OUT>
-__global__ __launch_bounds__(C::THREADS) void block_gemm_kernel(GemmArgs p, int64_t full) {
+template <class C, class TAIL, int SCHED, int OUT, class E>
+__device__ __forceinline__ void block_gemm_tile(const GemmArgs& p, int64_t full, const E& ep) {
 #if defined(__HIP_DEVICE_COMPILE__)
   static_assert((TAIL::THREADS == C::THREADS && TAIL::BN == C::BN && 2 * TAIL::BM == C::BM) ||
                     std::is_same<C, TAIL>::value, "tail tiles are half-height tiles");
@@ -910,11 +920,11 @@ __global__ __launch_bounds__(C::THREADS) void block_gemm_kernel(GemmArgs p, int6
     grouped_tile<C>(p, bid, MT, t);
     if constexpr (HALVES) {
       if (t.row_end - t.row0 <= TAIL::BM) {
-        block_gemm_body<TAIL, OUT>(p, t, L);
+        block_gemm_body<TAIL, OUT>(p, t, L, ep);
         return;
       }
     }
-    block_gemm_body<C, OUT>(p, t, L);
+    block_gemm_body<C, OUT>(p, t, L, ep);
   } else {
     constexpr int out_bytes = OUT == kOutF32 ? 4 : OUT == kOutBF16 ? 2 : 1;
     auto tile_of = [&](int64_t i) {
@@ -938,7 +948,7 @@ __global__ __launch_bounds__(C::THREADS) void block_gemm_kernel(GemmArgs p, int6
           return;
         }
       }
-      block_gemm_body<C, OUT>(p, t, L);
+      block_gemm_body<C, OUT>(p, t, L, ep);
     } else if constexpr (HALVES) {
       const int64_t j = order(bid - full, (int64_t)gridDim.x - full);
       tile_of(full + j / 2);
@@ -950,10 +960,22 @@ __global__ __launch_bounds__(C::THREADS) void block_gemm_kernel(GemmArgs p, int6
           return;
         }
       }
-      block_gemm_body<TAIL, OUT>(p, t, L);
+      block_gemm_body<TAIL, OUT>(p, t, L, ep);
     }
   }
 #endif
+}
+
+template <class C, class TAIL, int SCHED, int OUT>
+__global__ __launch_bounds__(C::THREADS) void block_gemm_kernel(GemmArgs p, int64_t full) {
+  block_gemm_tile<C, TAIL, SCHED, OUT>(p, full, NoEpilogue());
+}
+
+// The dense product with an epilogue (an object of kernel-argument type E).
+template <class C, class TAIL, int OUT, class E>
+__global__ __launch_bounds__(C::THREADS) void block_gemm_epilogue_kernel(GemmArgs p, int64_t full,
+                                                                         E ep) {
+  block_gemm_tile<C, TAIL, kDense, OUT>(p, full, ep);
 }
 
 // Compute units of the current device, cached per device.  Any thread may
@@ -972,8 +994,11 @@ inline int device_cus() {
   return n;
 }
 
-template <class C, int SCHED, class TAIL = C>
-hipError_t launch(const GemmArgs& args, OutKind out, hipStream_t stream) {
+// Workgroups of a launch, the first `full` of them on whole tiles (see
+// block_gemm_tile); 0 for an empty product, -1 where the grid would be too
+// large.
+template <class C, int SCHED, class TAIL>
+int64_t grid_size(const GemmArgs& args, int64_t& full) {
   const int64_t NT = (args.N + C::BN - 1) / C::BN;
   int64_t MT = (args.M + C::BM - 1) / C::BM;
   // grouped rows: every non-empty group adds at most one partial tile-row,
@@ -981,8 +1006,9 @@ hipError_t launch(const GemmArgs& args, OutKind out, hipStream_t stream) {
   if (SCHED == kGroupRows) MT = MT + args.G < args.M ? MT + args.G : args.M;
   // grouped K: the same tiles for every group
   const int64_t tiles = MT * NT * (SCHED == kGroupK ? args.G : 1);
-  if (tiles <= 0) return hipSuccess;
-  int64_t full = tiles, blocks = tiles;
+  if (tiles <= 0) return 0;
+  int64_t blocks = tiles;
+  full = tiles;
   if (SCHED != kGroupRows && !std::is_same<C, TAIL>::value) {
     // split the last partial round only when its halves fit in one round
     // (at most half the compute units' worth of tiles): a larger tail would
@@ -994,7 +1020,15 @@ hipError_t launch(const GemmArgs& args, OutKind out, hipStream_t stream) {
       blocks = full + 2 * tail;
     }
   }
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  return blocks > 0x7FFFFFFF ? -1 : blocks;
+}
+
+template <class C, int SCHED, class TAIL = C>
+hipError_t launch(const GemmArgs& args, OutKind out, hipStream_t stream) {
+  int64_t full = 0;
+  const int64_t blocks = grid_size<C, SCHED, TAIL>(args, full);
+  if (blocks == 0) return hipSuccess;
+  if (blocks < 0) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)blocks), block(C::THREADS);
   switch (out) {
     case kOutF32:
@@ -1013,6 +1047,37 @@ hipError_t launch(const GemmArgs& args, OutKind out, hipStream_t stream) {
         return hipErrorInvalidConfiguration;
       }
   }
+}
+
+// Tile shapes of the dense launches (see gemm.hip).
+// BM, BN, waves along M, waves along N, LDS stages, tile-rows per L2 group
+using LargeCfg = Cfg<256, 256, 2, 4, 2, 4>;
+// half-height tiles: a last partial round of the dense raster, and groups'
+// last tile-rows of at most 128 rows
+using LargeTail = Cfg<128, 256, 2, 4, 2, 4>;
+using Rows32Cfg = Cfg<32, 32, 1, 2, 4, 1>;
+using Rows64Cfg = Cfg<64, 128, 1, 4, 4, 1>;
+
+// Tile shape for M > 64: the least estimated time, counted in rounds of
+// workgroups (one workgroup per compute unit), a round of 256x256, 128x256
+// and 64x128 (four-stage) tiles taking 100, 77 and 40 (relative times per
+// round at equal K, measured on MI355X with one or two rounds); the 256x256
+// launch runs a last partial round of at most half the compute units as
+// 128x256 tiles, half a round.
+enum class Tiles { kLarge, kHalf, kSmall };
+inline Tiles pick_tiles(const GemmArgs& a) {
+  const int64_t cus = device_cus();
+  if (cus <= 0) return Tiles::kLarge;
+  const int64_t tl = ((a.M + 255) / 256) * ((a.N + 255) / 256);
+  const int64_t th = ((a.M + 127) / 128) * ((a.N + 255) / 256);
+  const int64_t ts = ((a.M + 63) / 64) * ((a.N + 127) / 128);
+  const int64_t tail = tl % cus;
+  const int64_t cost_l =
+      100 * (tl / cus) + (tail == 0 ? 0 : (tl > cus && 2 * tail <= cus) ? 50 : 100);
+  const int64_t cost_h = 77 * ((th + cus - 1) / cus);
+  const int64_t cost_s = 40 * ((ts + cus - 1) / cus);
+  if (cost_l <= cost_h && cost_l <= cost_s) return Tiles::kLarge;
+  return cost_h <= cost_s ? Tiles::kHalf : Tiles::kSmall;
 }
 
 }  // namespace gemm

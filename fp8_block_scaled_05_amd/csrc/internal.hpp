@@ -93,13 +93,42 @@ hipError_t launch_grouped_gemm(const GemmArgs& args, OutKind out, hipStream_t st
 // Few-row GEMM (M <= kFewRows), fp32 or bf16 output.  fused (M <=
 // kFewRowsFused): A is bf16 [M][lda], quantized per 1x128 tile inside the
 // kernel (sa: optional scale output); otherwise A is E4M3 codes with input
-// scales sa.
+// scales sa.  epilogue (bf16 output only): finishes the sums.
+struct Epilogue;
 constexpr int64_t kFewRows = 64;
 constexpr int64_t kFewRowsFused = 16;
 hipError_t launch_few_rows_gemm(const void* a, int64_t lda, float* sa, int64_t ldsa, bool fused,
                                 const uint8_t* b, int64_t ldb, const float* sb, void* c,
                                 int64_t ldc, bool out_bf16, int64_t M, int64_t N, int64_t K,
-                                hipStream_t stream);
+                                hipStream_t stream, const Epilogue* epilogue = nullptr);
+
+// Epilogue of a linear layer: z = product + bias (stored in bf16 if z), then
+// act(z) + residual.  bias, residual and z may be null.
+enum Activation { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3 };
+struct Epilogue {
+  const float* bias;         // [N]
+  const uint16_t* residual;  // bf16 [M][ldr]
+  int64_t ldr;
+  uint16_t* z;               // bf16 [M][ldz]
+  int64_t ldz;
+  int act;
+};
+
+// The dense product with an epilogue; bf16 or E4M3 output.
+hipError_t launch_block_gemm_epilogue(const GemmArgs& args, const Epilogue& e, OutKind out,
+                                      hipStream_t stream);
+
+// From the gradient dy of the epilogue's output and the kept z (not read for
+// kActNone): dz = dy act'(z) as E4M3 codes per 1x128 tile (q, s) and, with its
+// rows zero-padded to a multiple of 128, per 128 rows and transposed (qt, st);
+// dbias[n] = sum over the rows.  workspace: epilogue_backward_workspace bytes.
+// N is a multiple of 128.
+size_t epilogue_backward_workspace(int64_t M, int64_t N);
+hipError_t launch_epilogue_backward(const uint16_t* dy, int64_t lddy, const uint16_t* z,
+                                    int64_t ldz, int act, int64_t M, int64_t N, uint8_t* q,
+                                    int64_t ldq, float* s, int64_t lds, uint8_t* qt, int64_t ldqt,
+                                    float* st, int64_t ldst, float* dbias, void* workspace,
+                                    hipStream_t stream);
 
 // Cross entropy of the bf16 head's logits (workspace: xent_workspace bytes),
 // and its gradients (xent_grad_workspace bytes; M may be 0).

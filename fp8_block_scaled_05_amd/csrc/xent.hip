@@ -23,6 +23,7 @@
 // they cost nothing and whatever they hold, NaN and infinities too, reaches
 // no output.
 
+#include "epilogue.hpp"
 #include "gemm_bf16.hpp"
 
 namespace fp8bs {
@@ -34,7 +35,6 @@ using gemm16::kRow;
 using gemm16::kStep;
 using gemm16::Operand;
 
-constexpr float kLog2e = 1.4426950408889634f;
 
 // Large tiles, and the tile of few rows.  q are the rows of x, p the
 // vocabulary.

@@ -19,7 +19,8 @@ OK, ERR_NULL, ERR_SHAPE, ERR_LAYOUT, ERR_DTYPE, ERR_WORKSPACE, ERR_HIP = range(7
 OUT_F32, OUT_BF16 = 0, 1
 A_E4M3, A_BF16 = 0, 1
 OP_QUANT_ACT, OP_QUANT_W, OP_GEMM_E4M3, OP_GEMM_BF16, OP_GROUPED_GEMM, OP_XENT, \
-    OP_XENT_BACKWARD = range(7)
+    OP_XENT_BACKWARD, OP_EPILOGUE_BACKWARD = range(8)
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}  # FP8BS_ACT_*
 NOALLOC_SCRATCH_BYTES = 8 * 1024 * 1024  # FP8BS_NOALLOC_SCRATCH_BYTES
 DELAY_TILE, DELAY_TENSOR = 0, 1
 
@@ -35,6 +36,9 @@ EXPORTS = (
     "fp8_block_grouped_gemm",
     "fp8_block_gemm_e4m3_out",
     "fp8_block_grouped_gemm_e4m3_out",
+    "fp8_block_gemm_epilogue",
+    "fp8_block_gemm_epilogue_e4m3_out",
+    "fp8_quant_epilogue_backward",
     "fp8_block_gemm_rowscaled",
     "fp8_block_kgrouped_gemm_rowscaled",
     "bf16_linear_xent",
@@ -48,6 +52,16 @@ _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
 _sz = ctypes.c_size_t
+
+
+class _Epilogue(ctypes.Structure):
+    """fp8bs_epilogue"""
+
+    _fields_ = [("bias", _p), ("residual", _p), ("ldr", _i64), ("z", _p), ("ldz", _i64),
+                ("act", _int)]
+
+
+_ep = ctypes.POINTER(_Epilogue)
 
 _SIGNATURES = {
     "fp8_quant_act_1x128": ([_p, _i64, _i64, _i64, _p, _i64, _p, _i64, _p], _int),
@@ -72,6 +86,12 @@ _SIGNATURES = {
                                  _i64, _i64, _i64, _p, _sz, _p], _int),
     "fp8_block_grouped_gemm_e4m3_out": ([_p, _i64, _p, _i64, _p, _i64, _i64, _p, _p, _i64, _p,
                                          _i64, _p, _i64, _i64, _i64, _i64, _p, _sz, _p], _int),
+    "fp8_block_gemm_epilogue": ([_int, _p, _i64, _p, _i64, _p, _i64, _p, _ep, _p, _i64, _i64, _i64,
+                                 _i64, _p, _sz, _p], _int),
+    "fp8_block_gemm_epilogue_e4m3_out": ([_int, _p, _i64, _p, _i64, _p, _i64, _p, _ep, _p, _i64,
+                                          _p, _i64, _i64, _i64, _i64, _p, _sz, _p], _int),
+    "fp8_quant_epilogue_backward": ([_p, _i64, _p, _i64, _int, _i64, _i64, _p, _i64, _p, _i64, _p,
+                                     _i64, _p, _i64, _p, _p, _sz, _p], _int),
     "bf16_linear_xent": ([_p, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _i64, _i64, _p, _sz, _p],
                          _int),
     "bf16_linear_xent_backward": ([_p, _i64, _p, _i64, _p, _i64, _p, _p, _p, _i64, _p, _i64, _i64,
@@ -172,6 +192,17 @@ def _mat(t, name, rows, cols, dtype, ld=None):
         raise ValueError(f"{name} rows overlap (row stride {row} < {cols})")
     if ld is not None and rows > 1 and row != ld:
         raise ValueError(f"{name} must have row stride {ld}, got {row}")
+
+
+def _vec(t, name, n, dtype):
+    """Check that ``t`` (if given) is a contiguous vector of at least ``n``."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 1 or t.shape[0] < n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of at least {n} entries, "
+                         f"got {list(t.shape)}")
 
 
 def _rowmajor(t, name):
@@ -601,15 +632,107 @@ def fp8_block_grouped_gemm_e4m3_out(a, sa, b, sb, group_offsets, qc=None, sc=Non
     return qc, sc
 
 
-def _vec(t, name, n, dtype):
-    """Check that ``t`` (if given) is a contiguous vector of at least ``n``."""
-    if t is None:
-        return
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 1 or t.shape[0] < n or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous vector of at least {n} entries, "
-                         f"got {list(t.shape)}")
+def _act_id(act):
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {', '.join(ACTS)}, got {act!r}")
+    return ACTS[act]
+
+
+def _epilogue_operands(M, N, bias, act, residual, z):
+    act = _act_id(act)
+    _vec(bias, "bias", N, torch.float32)
+    _mat(residual, "residual", M, N, torch.bfloat16)
+    _mat(z, "z", M, N, torch.bfloat16)
+    return _Epilogue(_ptr(bias), _ptr(residual), residual.stride(0) if residual is not None else 0,
+                     _ptr(z), z.stride(0) if z is not None else 0, act)
+
+
+def fp8_block_gemm_epilogue(a, sa, b, sb, bias=None, act="none", residual=None, z=None, out=None,
+                            workspace=None):
+    """``fp8_block_gemm`` with a linear layer's epilogue: z = A . B^T + bias,
+    returns act(z) + residual in bf16 [M][N].
+
+    ``bias`` fp32 [N]; ``act`` "none", "relu", "silu" or "gelu" (tanh form);
+    ``residual`` bf16 [M][N]; ``z`` an optional bf16 [M][N] output that
+    receives what the backward pass needs (``fp8_quant_epilogue_backward``).
+    """
+    a_kind, M, N, K = _dense_operands("fp8_block_gemm_epilogue", a, sa, b, sb)
+    ep = _epilogue_operands(M, N, bias, act, residual, z)
+    _mat(out, "out", M, N, torch.bfloat16)
+    _need_device(a, sa, b, sb, bias, residual, z, out, workspace)
+    if out is None:
+        out = torch.empty(M, N, dtype=torch.bfloat16, device=a.device)
+    workspace, ws_bytes = _workspace(a_kind, M, N, K, workspace, a.device)
+    ldsa = sa.stride(0) if sa is not None else 0
+    with _on(a.device):
+        _check(lib.fp8_block_gemm_epilogue(a_kind, _ptr(a), _ld(a), _ptr(sa), ldsa, _ptr(b),
+                                           _ld(b), _ptr(sb), ep, _ptr(out), _ld(out), M, N, K,
+                                           _ptr(workspace), ws_bytes, _stream(a)),
+               "fp8_block_gemm_epilogue")
+    return out
+
+
+def fp8_block_gemm_epilogue_e4m3_out(a, sa, b, sb, bias=None, act="none", residual=None, z=None,
+                                     qc=None, sc=None, workspace=None):
+    """As ``fp8_block_gemm_epilogue``, with the result quantized per 1x128 tile
+    along N: returns ``(qc, sc)`` as ``fp8_block_gemm_e4m3_out``."""
+    a_kind, M, N, K = _dense_operands("fp8_block_gemm_epilogue_e4m3_out", a, sa, b, sb)
+    _e4m3_check(M, N, qc, sc)
+    ep = _epilogue_operands(M, N, bias, act, residual, z)
+    _need_device(a, sa, b, sb, bias, residual, z, qc, sc, workspace)
+    qc, sc = _e4m3_outputs(M, N, qc, sc, a.device)
+    workspace, ws_bytes = _workspace(a_kind, M, N, K, workspace, a.device)
+    ldsa = sa.stride(0) if sa is not None else 0
+    with _on(a.device):
+        _check(lib.fp8_block_gemm_epilogue_e4m3_out(
+            a_kind, _ptr(a), _ld(a), _ptr(sa), ldsa, _ptr(b), _ld(b), _ptr(sb), ep, _ptr(qc),
+            _ld(qc), _ptr(sc), sc.stride(0), M, N, K, _ptr(workspace), ws_bytes, _stream(a)),
+            "fp8_block_gemm_epilogue_e4m3_out")
+    return qc, sc
+
+
+def fp8_quant_epilogue_backward(dy, z, act="none", q=None, s=None, qt=None, st=None, dbias=None,
+                                workspace=None):
+    """Backward of the epilogue up to the backward GEMMs' operands: from bf16
+    ``dy`` [M][N] and the kept ``z`` (None for act "none"), dz = dy act'(z) as
+
+    ``(q, s)``: E4M3 codes [M][N], scales [N/128][M], the (a, sa) of the data
+    gradient; ``(qt, st)``: codes [N][Mp], scales [Mp/128][N], Mp = M rounded
+    up to 128 (zero padding), the (a, sa) of the weight gradient; ``dbias``
+    fp32 [N].  Returns ``(q, s, qt, st, dbias)``.
+    """
+    act_id = _act_id(act)
+    _mat(dy, "dy", 0, 0, torch.bfloat16)
+    M, N = dy.shape
+    if N % 128 != 0:
+        raise ValueError(f"fp8_quant_epilogue_backward: N = {N} must be a multiple of 128")
+    if z is None and act_id != ACTS["none"]:
+        raise ValueError(f"act {act!r} needs z")
+    Mp = (M + 127) // 128 * 128
+    _mat(z, "z", M, N, torch.bfloat16)
+    _mat(q, "q", M, N, torch.uint8)
+    _mat(s, "s", N // 128, M, torch.float32)
+    _mat(qt, "qt", N, Mp, torch.uint8)
+    _mat(st, "st", Mp // 128, N, torch.float32)
+    _vec(dbias, "dbias", N, torch.float32)
+    _need_device(dy, z, q, s, qt, st, dbias, workspace)
+    dev = dy.device
+    q = torch.empty(M, N, dtype=torch.uint8, device=dev) if q is None else q
+    s = torch.empty(N // 128, M, dtype=torch.float32, device=dev) if s is None else s
+    qt = torch.empty(N, Mp, dtype=torch.uint8, device=dev) if qt is None else qt
+    st = torch.empty(Mp // 128, N, dtype=torch.float32, device=dev) if st is None else st
+    dbias = torch.empty(N, dtype=torch.float32, device=dev) if dbias is None else dbias
+    if workspace is None:
+        workspace = torch.empty(workspace_bytes(OP_EPILOGUE_BACKWARD, M, N, 0), dtype=torch.uint8,
+                                device=dev)
+    with _on(dev):
+        _check(lib.fp8_quant_epilogue_backward(
+            _ptr(dy), _rowmajor(dy, "dy") if M else N, _ptr(z),
+            _rowmajor(z, "z") if z is not None and M else 0, act_id, M, N, _ptr(q), _ld(q),
+            _ptr(s), s.stride(0), _ptr(qt), _ld(qt), _ptr(st), st.stride(0), _ptr(dbias),
+            _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(dy)),
+            "fp8_quant_epilogue_backward")
+    return q, s, qt, st, dbias
 
 
 def _head_operands(where, x, w, target):
@@ -650,8 +773,8 @@ def bf16_linear_xent(x, w, target, ignore_index=-100, loss=None, lse=None, works
     workspace, ws_bytes = _head_workspace(OP_XENT, M, V, K, workspace, x.device)
     ldx = _rowmajor(x, "x") if M else K
     with _on(x.device):
-        _check(lib.bf16_linear_xent(_ptr(x), ldx, _ptr(w), _ld(w), _ptr(target), ignore_index,
-                                    _ptr(loss), _ptr(lse), M, V, K, _ptr(workspace), ws_bytes,
+        _check(lib.bf16_linear_xent(_ptr(x), ldx, _ptr(w), _rowmajor(w, "w"), _ptr(target),
+                                    ignore_index, _ptr(loss), _ptr(lse), M, V, K, _ptr(workspace), ws_bytes,
                                     _stream(x)), "bf16_linear_xent")
     return loss, lse
 
@@ -675,7 +798,8 @@ def bf16_linear_xent_backward(x, w, target, lse, dloss, ignore_index=-100, dx=No
     ldx = _rowmajor(x, "x") if M else K
     with _on(x.device):
         _check(lib.bf16_linear_xent_backward(
-            _ptr(x), ldx, _ptr(w), _ld(w), _ptr(target), ignore_index, _ptr(lse), _ptr(dloss),
+            _ptr(x), ldx, _ptr(w), _rowmajor(w, "w"), _ptr(target), ignore_index, _ptr(lse),
+            _ptr(dloss),
             _ptr(dx), _ld(dx), _ptr(dw), _ld(dw), M, V, K, _ptr(workspace), ws_bytes,
             _stream(x)), "bf16_linear_xent_backward")
     return dx, dw

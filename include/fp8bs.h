@@ -65,7 +65,7 @@ enum {
   FP8BS_ERR_NULL = 1,      /* a required pointer is NULL                     */
   FP8BS_ERR_SHAPE = 2,     /* negative size, K not a multiple of 128, ...    */
   FP8BS_ERR_LAYOUT = 3,    /* leading dimension or alignment not supported   */
-  FP8BS_ERR_DTYPE = 4,     /* unknown a_kind / out_kind                      */
+  FP8BS_ERR_DTYPE = 4,     /* unknown a_kind / out_kind / mode / act         */
   FP8BS_ERR_WORKSPACE = 5, /* workspace missing or smaller than required     */
   FP8BS_ERR_HIP = 6        /* a HIP launch failed (see fp8bs_last_hip_error) */
 };
@@ -86,8 +86,32 @@ enum {
   FP8BS_OP_GEMM_BF16 = 3,
   FP8BS_OP_GROUPED_GEMM = 4,
   FP8BS_OP_XENT = 5,
-  FP8BS_OP_XENT_BACKWARD = 6
+  FP8BS_OP_XENT_BACKWARD = 6,
+  FP8BS_OP_EPILOGUE_BACKWARD = 7
 };
+
+/* act of a linear layer's epilogue. */
+enum {
+  FP8BS_ACT_NONE = 0,
+  FP8BS_ACT_RELU = 1, /* max(z, 0)                                     */
+  FP8BS_ACT_SILU = 2, /* z / (1 + exp(-z))                             */
+  FP8BS_ACT_GELU = 3  /* 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+};
+
+/*
+ * Epilogue of a linear layer: z = product + bias, y = act(z) + residual.
+ * Every part may be left out (NULL, FP8BS_ACT_NONE).  The struct itself is
+ * read on the host during the call; its pointers are device memory.
+ */
+typedef struct fp8bs_epilogue {
+  const float* bias;        /* [in]  fp32 [N]                              */
+  const uint16_t* residual; /* [in]  bf16 [M][ldr], ldr >= N               */
+  int64_t ldr;
+  uint16_t* z;              /* [out] bf16 [M][ldz], ldz >= N: the value act
+                             *       is applied to, for the backward pass  */
+  int64_t ldz;
+  int act;                  /* FP8BS_ACT_*                                 */
+} fp8bs_epilogue;
 
 /*
  * Online activation quantization, one scale per 1x128 tile.
@@ -318,6 +342,69 @@ int fp8_block_gemm_e4m3_out(int a_kind, const void* a, int64_t lda, float* sa,
                             float* sc, int64_t ldsc, int64_t M, int64_t N,
                             int64_t K, void* workspace,
                             size_t workspace_bytes, void* stream);
+/*
+ * fp8_block_gemm with a linear layer's epilogue: z = A . B^T + bias,
+ * c = act(z) + residual, in bf16.  The FP32 sums are finished in registers:
+ * z and c are rounded once each (nearest even), and act is applied to the
+ * unrounded z.  Few rows (M <= 16 with a bf16 A) quantize A inside the
+ * product, as fp8_block_gemm does.
+ *
+ *   a_kind, a, sa, b, sb, workspace  as fp8_block_gemm.
+ *   epilogue  see fp8bs_epilogue; residual and c may be the same array
+ *             (each element is read before it is written, by one lane).
+ *   c         [out] bf16 [M][ldc], ldc >= N.
+ * Errors: as fp8_block_gemm; epilogue NULL -> ERR_NULL; unknown act ->
+ *         ERR_DTYPE; ldr/ldz < N or misaligned -> ERR_LAYOUT.
+ */
+int fp8_block_gemm_epilogue(int a_kind, const void* a, int64_t lda, float* sa,
+                            int64_t ldsa, const uint8_t* b, int64_t ldb,
+                            const float* sb, const fp8bs_epilogue* epilogue,
+                            uint16_t* c, int64_t ldc, int64_t M, int64_t N,
+                            int64_t K, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
+ * fp8_block_gemm_epilogue with the output quantized for the next FP8 GEMM, as
+ * fp8_block_gemm_e4m3_out: c = act(z) + residual in FP32, quantized per 1x128
+ * tile along N by the online rule.
+ * Errors: as those two calls.
+ */
+int fp8_block_gemm_epilogue_e4m3_out(int a_kind, const void* a, int64_t lda,
+                                     float* sa, int64_t ldsa, const uint8_t* b,
+                                     int64_t ldb, const float* sb,
+                                     const fp8bs_epilogue* epilogue,
+                                     uint8_t* qc, int64_t ldqc, float* sc,
+                                     int64_t ldsc, int64_t M, int64_t N,
+                                     int64_t K, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/*
+ * Backward of the epilogue, up to the operands of the two backward GEMMs.
+ * With dy the gradient of c: dz = dy act'(z) (FP32, never stored; act'(0) = 0
+ * for relu), the gradient of the residual is dy itself, and
+ *   q, s    [out] dz as fp8_quant_act_1x128 would quantize it: codes
+ *                 [M][ldq], s(m, nb) at s[nb*lds + m], lds >= M -- the (a, sa)
+ *                 of the data gradient dX = dz . W;
+ *   qt, st  [out] dz as fp8_quant_act_128x1_t would, with the rows zero-padded
+ *                 to Mp = M rounded up to 128: codes [N][ldqt], ldqt >= Mp,
+ *                 st(n, mb) at st[mb*ldst + n], ldst >= N -- the (a, sa) of
+ *                 the weight gradient dW = dz^T . X (X padded alike);
+ *   dbias   [out] fp32 [N], sum of dz over the rows (in a fixed order).
+ *   dy      [in]  bf16 [M][lddy].
+ *   z       [in]  bf16 [M][ldz], as the forward call kept it (not read for
+ *                 FP8BS_ACT_NONE, may be NULL then).
+ *   workspace  fp8bs_workspace_bytes(FP8BS_OP_EPILOGUE_BACKWARD, M, N, 0, 0).
+ * M == 0 launches nothing (dbias is not written).
+ * Errors: N not a multiple of 128 -> ERR_SHAPE; unknown act -> ERR_DTYPE;
+ *         otherwise as the two quantizers; workspace -> ERR_WORKSPACE.
+ */
+int fp8_quant_epilogue_backward(const uint16_t* dy, int64_t lddy,
+                                const uint16_t* z, int64_t ldz, int act,
+                                int64_t M, int64_t N, uint8_t* q, int64_t ldq,
+                                float* s, int64_t lds, uint8_t* qt,
+                                int64_t ldqt, float* st, int64_t ldst,
+                                float* dbias, void* workspace,
+                                size_t workspace_bytes, void* stream);
 /*
  * Block-scaled FP8 GEMM with one scale per row and 128-K group on both
  * operands:  C[m][n] = sum_kb sa(m,kb) * sb(n,kb) * P(m,n,kb), P the FP8 x FP8
