@@ -88,75 +88,47 @@ __device__ __forceinline__ constexpr int p_of(int i, int g) {
 
 __device__ __forceinline__ int col_swizzle(int k) { return 2 * ((k & 3) | (((k >> 4) & 1) << 2)); }
 
-// Byte offset, from the operand's base at the step's first k, of the 16 bytes
-// that lane `lane` of 1-KB copy `c` moves.  k_lim: last valid k-row of the
-// step (kCol).
-template <class C, bool IS_P>
-__device__ __forceinline__ uint32_t copy_offset(const Operand& o, int c, int lane, int k_lim) {
-  constexpr int B = IS_P ? C::BP : C::BQ;
-  if constexpr ((IS_P ? C::LP : C::LQ) == kRow) {
-    const int r = c * 8 + (lane >> 3);
-    int row = IS_P ? p_row<C>(r) : r;
-    row = row < o.rows ? row : o.rows - 1;
-    return (uint32_t)row * (uint32_t)(o.ld * 2) + (uint32_t)(((lane & 7) ^ lds_swizzle(r)) * 16);
-  } else {
-    constexpr int CH = B / 8;          // 16-byte chunks of a k-row
-    constexpr int RPC = 64 / CH;       // k-rows per copy
-    const int k = c * RPC + lane / CH;
-    int chunk = (lane % CH) ^ col_swizzle(k);
-    const int last = (o.rows - 1) / 8;
-    chunk = chunk < last ? chunk : last;
-    const int kk = k < k_lim ? k : k_lim;
-    return (uint32_t)kk * (uint32_t)(o.ld * 2) + (uint32_t)(chunk * 16);
-  }
-}
-
 // Per-lane LDS byte offsets of a wave's fragments inside a stage, opaque to
-// the optimizer (see gemm::FragOffs).  kRow: [0], [1] are the 16-byte reads of
-// halves 0 and 1, tile i at + 2048 i.  kCol: [i] is tile i's transposing read,
-// half h and its k quad e at + (8 h + 4 e) k-rows.
-template <int L, int F>
+// the optimizer (see gemm::FragOffs).  kRow: o[h] is the 16-byte read of half
+// h, tile i at + 2048 i.  kCol: o[0] is tile 0's transposing read, tile i at
+// ^ 32 i (the swizzle leaves those bits to be XORed), half h and its k quad e at
+// + (8 h + 4 e) k-rows.
 struct FragOffs {
-  int o[L == kRow ? 2 : F];
+  int o[2];
 };
 
 template <class C, bool IS_P>
-__device__ __forceinline__ FragOffs<IS_P ? C::LP : C::LQ, IS_P ? C::FP : C::FQ> frag_offsets(
-    int w, int lane) {
-  constexpr int L = IS_P ? C::LP : C::LQ, F = IS_P ? C::FP : C::FQ;
+__device__ __forceinline__ FragOffs frag_offsets(int w, int lane) {
   constexpr int T = IS_P ? C::TP : C::TQ, B = IS_P ? C::BP : C::BQ;
   constexpr int OFF = IS_P ? 0 : C::Q_OFF;
   const int g = lane >> 4, l16 = lane & 15;
-  FragOffs<L, F> f;
-  if constexpr (L == kRow) {
+  FragOffs f;
+  if constexpr ((IS_P ? C::LP : C::LQ) == kRow) {
     const int slot = (2 * g) ^ lds_swizzle(l16);
     f.o[0] = OFF + (w * T + l16) * 128 + slot * 16;
     f.o[1] = OFF + (w * T + l16) * 128 + (slot ^ 1) * 16;
-    asm volatile("" : "+v"(f.o[0]), "+v"(f.o[1]));
   } else {
+    static_assert(OFF % 256 == 0 && 2 * B % 256 == 0 && T % 64 == 0, "bits 5 to 7 are the tile's");
     const int k = 16 * g + (l16 >> 2);
-#pragma unroll
-    for (int i = 0; i < F; ++i) {
-      const int chunk = (w * T + 16 * i) / 8 + ((l16 & 3) >> 1);
-      f.o[i] = OFF + k * (2 * B) + (chunk ^ col_swizzle(k)) * 16 + (l16 & 1) * 8;
-      asm volatile("" : "+v"(f.o[i]));
-    }
+    const int chunk = w * T / 8 + ((l16 & 3) >> 1);
+    f.o[0] = OFF + k * (2 * B) + (chunk ^ col_swizzle(k)) * 16 + (l16 & 1) * 8;
+    f.o[1] = 0;
   }
+  asm volatile("" : "+v"(f.o[0]), "+v"(f.o[1]));
   return f;
 }
 
 // MFMA operand of tile i and half h.
-template <class C, bool IS_P, class FO>
-__device__ __forceinline__ bf16x8 load_frag(uint8_t* st, const FO& f, int i, int h) {
+template <class C, bool IS_P>
+__device__ __forceinline__ bf16x8 load_frag(uint8_t* st, const FragOffs& f, int i, int h) {
   constexpr int L = IS_P ? C::LP : C::LQ;
   constexpr int B = IS_P ? C::BP : C::BQ;
   if constexpr (L == kRow) {
     return *reinterpret_cast<const bf16x8*>(st + f.o[h] + 2048 * i);
   } else {
-    const s16x4 a =
-        __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(st + f.o[i] + (8 * h) * 2 * B));
-    const s16x4 b =
-        __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(st + f.o[i] + (8 * h + 4) * 2 * B));
+    uint8_t* at = st + (f.o[0] ^ (32 * i)) + 8 * h * 2 * B;
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 4 * 2 * B));
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
   }
 }
@@ -164,82 +136,202 @@ __device__ __forceinline__ bf16x8 load_frag(uint8_t* st, const FO& f, int i, int
 template <class C>
 using Acc = v4f[C::FP][C::FQ];
 
-// acc += the product over `steps` k-steps (steps >= 0).
+// One operand's share of a wave's copies HBM->LDS: N 1-KB copies per k-step,
+// copy c of wave w being block c NWAVES + w.  Byte offsets are relative to the
+// operand's base at the step's first k.
+template <class C, bool IS_P>
+struct Copier {
+  static constexpr int B = IS_P ? C::BP : C::BQ, N = IS_P ? C::CP : C::CQ;
+  static constexpr bool COL = (IS_P ? C::LP : C::LQ) == kCol;
+  static constexpr int CH = B / 8;  // kCol: 16-byte chunks of a k-row
+  // kCol: copy c takes k-row k0 + c DK; its chunk goes by c mod 2
+  static constexpr int DK = 64 / CH * C::NWAVES;
+  static_assert(!COL || DK % 16 == 0, "swizzle by the copy's parity");
+
+  const uint8_t* base;
+  int64_t step, k_rows;    // step: bytes per k
+  uint32_t ld;             // bytes
+  uint32_t at[COL ? 3 : N];  // kRow: the copies' offsets; kCol: k0 and the two chunks' offsets
+  int lds;                 // of copy 0
+
+  __device__ __forceinline__ Copier(const Operand& o, int wave, int lane)
+      : base(reinterpret_cast<const uint8_t*>(o.base)), k_rows(o.k_rows), ld((uint32_t)(o.ld * 2)),
+        lds((IS_P ? 0 : C::Q_OFF) + wave * 1024) {
+    step = COL ? o.ld * 2 : 2;
+    if constexpr (COL) {
+      const int k0 = wave * (64 / CH) + lane / CH, last = (o.rows - 1) / 8;
+      at[0] = (uint32_t)k0;
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const int chunk = (lane % CH) ^ col_swizzle(k0 + z * DK);
+        at[1 + z] = (uint32_t)((chunk < last ? chunk : last) * 16);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        const int r = (c * C::NWAVES + wave) * 8 + (lane >> 3);
+        int row = IS_P ? p_row<C>(r) : r;
+        row = row < o.rows ? row : o.rows - 1;
+        at[c] = (uint32_t)row * ld + (uint32_t)(((lane & 7) ^ lds_swizzle(r)) * 16);
+      }
+    }
+  }
+
+  // copy c of k-step s into stage st
+  __device__ __forceinline__ void issue(int64_t s, uint8_t* st, int c) const {
+#if defined(__HIP_DEVICE_COMPILE__)
+    uint32_t v;
+    int64_t first = s * kStep;
+    if constexpr (COL) {
+      // k-rows past the last repeat it
+      first = first < k_rows ? first : k_rows - 1;
+      const int64_t left = k_rows - 1 - first;
+      const uint32_t lim = left < kStep - 1 ? (uint32_t)left : kStep - 1;
+      const uint32_t k = at[0] + (uint32_t)(c * DK);
+      v = (k < lim ? k : lim) * ld + at[1 + (c & 1)];
+    } else {
+      v = at[c];
+    }
+    const __amdgpu_buffer_rsrc_t rs = gemm::make_rsrc(base + first * step);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rs, (gemm::lds_void*)(st + lds + c * C::NWAVES * 1024), 16, v, 0, 0, 0);
+#endif
+  }
+};
+
+// Both operands' copies; copy c < CP is P's.
 template <class C>
-__device__ __forceinline__ void product(const Operand& op, const Operand& oq, int64_t steps,
-                                        uint8_t* const (&stages)[4], Acc<C>& acc) {
+struct Copiers {
+  Copier<C, true> p;
+  Copier<C, false> q;
+  __device__ __forceinline__ Copiers(const Operand& op, const Operand& oq, int wave, int lane)
+      : p(op, wave, lane), q(oq, wave, lane) {}
+  __device__ __forceinline__ void issue(int64_t s, uint8_t* st, int c) const {
+    if (c < C::CP) {
+      p.issue(s, st, c);
+    } else {
+      q.issue(s, st, c - C::CP);
+    }
+  }
+  __device__ __forceinline__ void issue_all(int64_t s, uint8_t* st) const {
+#pragma unroll
+    for (int c = 0; c < C::COPIES; ++c) issue(s, st, c);
+  }
+};
+
+// acc += the product over `steps` k-steps (steps >= 0), few MFMAs per step:
+// the stream of the operands bounds it, so STAGES - 1 steps are in flight.
+template <class C>
+__device__ __forceinline__ void product_deep(const Operand& op, const Operand& oq, int64_t steps,
+                                             uint8_t* const (&stages)[4], Acc<C>& acc) {
   if (steps <= 0) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
-  const int wp = wave / C::WQ, wq = wave % C::WQ;
-  const auto fp = frag_offsets<C, true>(wp, lane);
-  const auto fq = frag_offsets<C, false>(wq, lane);
-
-  const int64_t step_p = C::LP == kCol ? op.ld * (2 * kStep) : 2 * kStep;
-  const int64_t step_q = C::LQ == kCol ? oq.ld * (2 * kStep) : 2 * kStep;
-  uint32_t off[C::COPIES];
+  const auto fp = frag_offsets<C, true>(wave / C::WQ, lane);
+  const auto fq = frag_offsets<C, false>(wave % C::WQ, lane);
+  const Copiers<C> cp(op, oq, wave, lane);
+  // step s lives in stage s % STAGES; past the last step its copies are
+  // issued again, never read, so that the wait counts stay constants
+  auto last = [&](int64_t s) { return s < steps ? s : steps - 1; };
 #pragma unroll
-  for (int c = 0; c < C::COPIES; ++c)
-    off[c] = c < C::CP
-                 ? copy_offset<C, true>(op, c * C::NWAVES + wave, lane, kStep - 1)
-                 : copy_offset<C, false>(oq, (c - C::CP) * C::NWAVES + wave, lane, kStep - 1);
-
-  // copies of k-step s (past the last step: the last again, never read)
-  auto issue = [&](int64_t s, uint8_t* st) {
-    const int64_t sc = s < steps ? s : steps - 1;
-    const __amdgpu_buffer_rsrc_t rp =
-        gemm::make_rsrc(reinterpret_cast<const uint8_t*>(op.base) + sc * step_p);
-    const __amdgpu_buffer_rsrc_t rq =
-        gemm::make_rsrc(reinterpret_cast<const uint8_t*>(oq.base) + sc * step_q);
-    // k-rows that end inside this step: further ones repeat the last
-    const int64_t lp = op.k_rows - 1 - sc * kStep, lq = oq.k_rows - 1 - sc * kStep;
-    const bool cut_p = C::LP == kCol && lp < kStep - 1, cut_q = C::LQ == kCol && lq < kStep - 1;
-#pragma unroll
-    for (int c = 0; c < C::CP; ++c) {
-      const int b = c * C::NWAVES + wave;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rp, (gemm::lds_void*)(st + b * 1024), 16,
-          cut_p ? copy_offset<C, true>(op, b, lane, (int)lp) : off[c], 0, 0, 0);
-    }
-#pragma unroll
-    for (int c = 0; c < C::CQ; ++c) {
-      const int b = c * C::NWAVES + wave;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rq, (gemm::lds_void*)(st + C::Q_OFF + b * 1024), 16,
-          cut_q ? copy_offset<C, false>(oq, b, lane, (int)lq) : off[C::CP + c], 0, 0, 0);
-    }
-  };
-  auto compute = [&](uint8_t* st) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      bf16x8 q[C::FQ];
-#pragma unroll
-      for (int j = 0; j < C::FQ; ++j) q[j] = load_frag<C, false>(st, fq, j, h);
-#pragma unroll
-      for (int i = 0; i < C::FP; ++i) {
-        const bf16x8 p = load_frag<C, true>(st, fp, i, h);
-#pragma unroll
-        for (int j = 0; j < C::FQ; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p, q[j], acc[i][j], 0, 0, 0);
-      }
-    }
-  };
-
-  // step s lives in stage s % STAGES; STAGES - 1 steps are in flight ahead
-#pragma unroll
-  for (int s = 0; s < C::STAGES - 1; ++s) issue(s, stages[s]);
+  for (int s = 0; s < C::STAGES - 1; ++s) cp.issue_all(last(s), stages[s]);
   for (int64_t s = 0; s < steps; s += C::STAGES) {
 #pragma unroll
     for (int u = 0; u < C::STAGES; ++u) {
       if (s + u < steps) {
         gemm::barrier_after_vmcnt<(C::STAGES - 2) * C::COPIES>();
-        issue(s + u + C::STAGES - 1, stages[(u + C::STAGES - 1) % C::STAGES]);
-        compute(stages[u]);
+        cp.issue_all(last(s + u + C::STAGES - 1), stages[(u + C::STAGES - 1) % C::STAGES]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          bf16x8 q[C::FQ];
+#pragma unroll
+          for (int j = 0; j < C::FQ; ++j) q[j] = load_frag<C, false>(stages[u], fq, j, h);
+#pragma unroll
+          for (int i = 0; i < C::FP; ++i) {
+            const bf16x8 p = load_frag<C, true>(stages[u], fp, i, h);
+#pragma unroll
+            for (int j = 0; j < C::FQ; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p, q[j], acc[i][j], 0, 0, 0);
+          }
+        }
       }
     }
   }
   // every copy has landed and every wave has left the stages
   gemm::barrier_after_vmcnt<0>();
+}
+
+// acc += the product over `steps` k-steps (even, >= 0), MFMA-bound.
+//
+// Two stages.  A step is 2 FP rows of FQ MFMAs (half h = row / FP, tile i =
+// row mod FP).  Row r's P fragment is read from LDS at row r - D, so that the
+// read is D FQ MFMAs old when it is used; the Q fragments of the second half
+// are read over the first rows.  The step's one barrier stands D rows before
+// its end, when the last fragment of the stage has been read: behind it the
+// next stage has landed (its copies are most of a step old), so the last D
+// rows read the first fragments of the next step, and the copies of the step
+// after it refill the stage just left.  The matrix cores so have work through
+// the barrier and the step's change.  One loop with one exit, without a peeled
+// end: several exits have the compiler move the accumulators between copies of
+// the step, and spill.  So past the last step its copies are issued again and
+// the fragments of a successor that is not there are read, both unused.
+template <class C>
+__device__ __forceinline__ void product(const Operand& op, const Operand& oq, int64_t steps,
+                                        uint8_t* const (&stages)[4], Acc<C>& acc) {
+  static_assert(C::STAGES == 2, "two stages");
+  if (steps <= 0) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  const auto fp = frag_offsets<C, true>(wave / C::WQ, lane);
+  const auto fq = frag_offsets<C, false>(wave % C::WQ, lane);
+  const Copiers<C> cp(op, oq, wave, lane);
+  constexpr int D = 3, R = 2 * C::FP, RING = D + 1;
+  static_assert(R % RING == 0 && C::FP > D, "ring of P fragments");
+  bf16x8 p[RING], q[2][C::FQ];
+
+  // one step from stage `st`; next: its successor's stage
+  auto step = [&](int64_t s, uint8_t* st, uint8_t* next) {
+    const int64_t refill = s + 2 < steps ? s + 2 : steps - 1;
+    static_for<0, R>([&](auto r_) {
+      constexpr int r = decltype(r_)::value, h = r / C::FP, i = r % C::FP;
+      if constexpr (r == R - D) {
+        gemm::barrier_after_vmcnt<0>();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (r + D < R) {
+        p[(r + D) % RING] = load_frag<C, true>(st, fp, (r + D) % C::FP, (r + D) / C::FP);
+      } else {
+        p[(r + D) % RING] = load_frag<C, true>(next, fp, r + D - R, 0);
+      }
+      static_for<0, C::FQ>([&](auto j_) {
+        constexpr int j = decltype(j_)::value;
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p[r % RING], q[h][j], acc[i][j], 0, 0, 0);
+        // Q fragments: the second half's over the first FQ rows, the next
+        // step's over the last D rows
+        if constexpr (j == 0 && r < C::FQ) q[1][r] = load_frag<C, false>(st, fq, r, 1);
+        if constexpr (r >= R - D) {
+          constexpr int n = (r - (R - D)) * C::FQ + j;  // of D FQ
+          if constexpr (n < C::FQ) q[0][n] = load_frag<C, false>(next, fq, n, 0);
+          if constexpr (n < C::COPIES) cp.issue(refill, st, n);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
+  };
+
+  cp.issue_all(0, stages[0]);
+  cp.issue_all(1, stages[1]);
+  gemm::barrier_after_vmcnt<C::COPIES>();
+#pragma unroll
+  for (int j = 0; j < C::FQ; ++j) q[0][j] = load_frag<C, false>(stages[0], fq, j, 0);
+#pragma unroll
+  for (int r = 0; r < D; ++r) p[r] = load_frag<C, true>(stages[0], fp, r, 0);
+  for (int64_t s = 0; s < steps; s += 2) {
+    step(s, stages[0], stages[1]);
+    step(s + 1, stages[1], stages[0]);
+  }
+  // the copies past the last step have landed before the stages are left
+  gemm::wait_vmcnt<0>();
 }
 
 // The stage buffers: separate objects, so that the compiler can tell reads of

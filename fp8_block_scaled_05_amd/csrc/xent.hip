@@ -45,6 +45,7 @@ using DxCfg = gemm16::Cfg<256, 256, 2, 4, 2, kCol, kRow>;
 using DwCfg = gemm16::Cfg<256, 256, 2, 4, 2, kCol, kCol>;
 
 constexpr int64_t kTile = 256;
+constexpr int64_t kPad = 2 * kStep;  // k-steps come in pairs
 constexpr int64_t kFewXentRows = 64;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -138,15 +139,15 @@ __global__ __launch_bounds__(1024) void xent_rows_kernel(const int64_t* target, 
   if (threadIdx.x == 0) r.h->rows = base;
 }
 
-// Packs the rows of x, one wave per packed row, zeros up to a multiple of 64
-// rows (the last k-step of dw's product); xs (backward, dloss not uniform):
+// Packs the rows of x, one wave per packed row, zeros up to a multiple of kPad
+// rows (the last k-steps of dw's product); xs (backward, dloss not uniform):
 // the rows times dloss / c.
 __global__ __launch_bounds__(256) void xent_pack_kernel(const uint16_t* x, int64_t ldx, int64_t M,
                                                         int64_t K, Rows r, uint16_t* xc,
                                                         uint16_t* xs) {
   const int64_t q = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
-  const int64_t rows = r.h->rows, upto = (rows + kStep - 1) / kStep * kStep;
+  const int64_t rows = r.h->rows, upto = (rows + kPad - 1) / kPad * kPad;
   const bool scaled = xs != nullptr && !r.h->uniform;
   // all rows, as they are: used in place
   if (q >= upto || (rows == M && (xs == nullptr || (rows == upto && !scaled)))) return;
@@ -219,7 +220,11 @@ __global__ __launch_bounds__(C::THREADS) void xent_loss_kernel(LossArgs a) {
   const Operand oq{x + q0 * ldx, ldx, (int)(rows - q0 < C::BQ ? rows - q0 : C::BQ), 0};
   gemm16::Acc<C> acc;
   clear<C>(acc);
-  gemm16::product<C>(op, oq, a.K / kStep, stages, acc);
+  if constexpr (FEW) {
+    gemm16::product_deep<C>(op, oq, a.K / kStep, stages, acc);
+  } else {
+    gemm16::product<C>(op, oq, a.K / kStep, stages, acc);
+  }
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
@@ -411,8 +416,9 @@ __global__ __launch_bounds__(CX::THREADS) void xent_grad_kernel(GradArgs a, int 
     int64_t pt, qt;
     raster(i % (PT * QX), PT, QX, pt, qt);
     const int64_t p0 = pt * C::BP, q0 = qt * C::BQ;
-    const int64_t steps = (a.nv + kStep - 1) / kStep;
-    const int64_t s0 = steps * split / a.splits, s1 = steps * (split + 1) / a.splits;
+    // in pairs of k-steps; G is zero past the vocabulary, up to whole tiles
+    const int64_t pairs = (a.nv + 2 * kStep - 1) / (2 * kStep);
+    const int64_t s0 = pairs * split / a.splits * 2, s1 = pairs * (split + 1) / a.splits * 2;
     const int64_t k0 = s0 * kStep;
     const Operand op{a.w + (a.v0 + k0) * a.ldw + p0, a.ldw,
                      (int)(a.K - p0 < C::BP ? a.K - p0 : C::BP), a.nv - k0};
@@ -440,8 +446,8 @@ __global__ __launch_bounds__(CX::THREADS) void xent_grad_kernel(GradArgs a, int 
     int64_t pt, qt;
     raster(gemm::xcd_remap(bid - NX, NW), PT, QW, pt, qt);
     const int64_t p0 = pt * C::BP, q0 = qt * C::BQ;
-    const int64_t steps = (rows + kStep - 1) / kStep;
-    const bool direct = a.r.h->uniform && rows == a.M && rows % kStep == 0;
+    const int64_t steps = (rows + 2 * kStep - 1) / (2 * kStep) * 2;
+    const bool direct = a.r.h->uniform && rows == a.M && rows % kPad == 0;
     const uint16_t* x = direct ? a.x : a.r.h->uniform ? a.xc : a.xs;
     const int64_t ldx = direct ? a.ldx : a.K;
     const int64_t kr = steps * kStep;
@@ -533,7 +539,7 @@ LossPlan loss_plan(void* ws, int64_t M, int64_t V, int64_t K) {
   p.at = c.take<float>(M);
   if (!few) {
     p.r = take_rows(c, M, false);
-    p.xc = c.take<uint16_t>(cdiv(M, kStep) * kStep * K);
+    p.xc = c.take<uint16_t>(cdiv(M, kPad) * kPad * K);
   }
   p.bytes = c.used;
   return p;
@@ -570,8 +576,8 @@ GradPlan grad_plan(void* ws, int64_t M, int64_t V, int64_t K) {
   while (p.splits < 32 && sx / p.splits > 8 && 2 * 256 * (sx / p.splits) > tx * sx + tw * sw)
     p.splits *= 2;
   p.r = take_rows(c, M, true);
-  p.xc = c.take<uint16_t>(cdiv(M, kStep) * kStep * K);
-  p.xs = c.take<uint16_t>(cdiv(M, kStep) * kStep * K);
+  p.xc = c.take<uint16_t>(cdiv(M, kPad) * kPad * K);
+  p.xs = c.take<uint16_t>(cdiv(M, kPad) * kPad * K);
   p.g = c.take<uint16_t>(Mt * p.ldg);
   p.dxp = c.take<float>(p.splits * M * K);
   p.bytes = c.used;
@@ -606,7 +612,7 @@ hipError_t launch_xent(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_
                     static_cast<const float*>(nullptr), static_cast<const float*>(nullptr), loss,
                     lse);
   if (e != hipSuccess) return e;
-  e = launch_kernel(xent_pack_kernel, dim3((unsigned)cdiv(cdiv(M, kStep) * kStep, 4)), dim3(256),
+  e = launch_kernel(xent_pack_kernel, dim3((unsigned)cdiv(cdiv(M, kPad) * kPad, 4)), dim3(256),
                     stream, x, ldx, M, K, p.r, p.xc, static_cast<uint16_t*>(nullptr));
   if (e != hipSuccess) return e;
   e = launch_kernel(xent_loss_kernel<C, false>, dim3((unsigned)tiles), dim3(C::THREADS), stream, a);
@@ -630,7 +636,7 @@ hipError_t launch_xent_backward(const uint16_t* x, int64_t ldx, const uint16_t* 
                                static_cast<float*>(nullptr));
   if (e != hipSuccess) return e;
   if (M > 0) {
-    e = launch_kernel(xent_pack_kernel, dim3((unsigned)cdiv(cdiv(M, kStep) * kStep, 4)), dim3(256),
+    e = launch_kernel(xent_pack_kernel, dim3((unsigned)cdiv(cdiv(M, kPad) * kPad, 4)), dim3(256),
                       stream, x, ldx, M, K, p.r, p.xc, p.xs);
     if (e != hipSuccess) return e;
   }
