@@ -285,13 +285,14 @@ __device__ __forceinline__ void product(const Operand& op, const Operand& oq, in
   const auto fp = frag_offsets<C, true>(wave / C::WQ, lane);
   const auto fq = frag_offsets<C, false>(wave % C::WQ, lane);
   const Copiers<C> cp(op, oq, wave, lane);
-  constexpr int D = 3, R = 2 * C::FP, RING = D + 1;
+  constexpr int D = 3, R = 2 * C::FP, RING = D + 1, PER = 1;
   static_assert(R % RING == 0 && C::FP > D, "ring of P fragments");
   bf16x8 p[RING], q[2][C::FQ];
 
   // one step from stage `st`; next: its successor's stage
   auto step = [&](int64_t s, uint8_t* st, uint8_t* next) {
     const int64_t refill = s + 2 < steps ? s + 2 : steps - 1;
+    const int64_t refill_next = s + 1 < steps ? s + 1 : steps - 1;
     static_for<0, R>([&](auto r_) {
       constexpr int r = decltype(r_)::value, h = r / C::FP, i = r % C::FP;
       if constexpr (r == R - D) {
@@ -312,7 +313,12 @@ __device__ __forceinline__ void product(const Operand& op, const Operand& oq, in
         if constexpr (r >= R - D) {
           constexpr int n = (r - (R - D)) * C::FQ + j;  // of D FQ
           if constexpr (n < C::FQ) q[0][n] = load_frag<C, false>(next, fq, n, 0);
-          if constexpr (n < C::COPIES) cp.issue(refill, st, n);
+        }
+        // PER copies per row, from the barrier's row on and into the next step
+        constexpr int row = (r + D) % R, n = row * PER + j;
+        if constexpr (j < PER && n < C::COPIES) {
+          if constexpr (r >= R - D) cp.issue(refill, st, n);
+          else cp.issue(refill_next, next, n);
         }
         __builtin_amdgcn_sched_barrier(0);
       });
@@ -320,8 +326,9 @@ __device__ __forceinline__ void product(const Operand& op, const Operand& oq, in
   };
 
   cp.issue_all(0, stages[0]);
-  cp.issue_all(1, stages[1]);
-  gemm::barrier_after_vmcnt<C::COPIES>();
+#pragma unroll
+  for (int n = 0; n < D * PER && n < C::COPIES; ++n) cp.issue(1, stages[1], n);
+  gemm::barrier_after_vmcnt<(D * PER < C::COPIES ? D * PER : C::COPIES)>();
 #pragma unroll
   for (int j = 0; j < C::FQ; ++j) q[0][j] = load_frag<C, false>(stages[0], fq, j, 0);
 #pragma unroll

@@ -180,6 +180,19 @@ __device__ __forceinline__ void raster(int64_t i, int64_t PT, int64_t QT, int64_
   pt = p0 + rr / gq;
 }
 
+// Tile number of workgroup `bid` of T: workgroups go round-robin to the 8
+// XCDs, 32 compute units each.  Every full round of 256 tiles gives each XCD
+// 32 consecutive tiles of the raster (an 8 x 4 block sharing its L2) and the
+// XCDs neighbouring blocks, so that a panel of the large operand, which
+// several XCDs need, is wanted by all of them at one time and comes from HBM
+// once.  The rest of the tiles is dealt evenly.  A bijection of [0, T).
+__device__ __forceinline__ int64_t tile_of(int64_t bid, int64_t T) {
+  const int64_t full = T / 256 * 256;
+  if (bid >= full) return full + gemm::xcd_remap(bid - full, T - full);
+  const int64_t x = bid % 8, j = bid / 8;
+  return j / 32 * 256 + x * 32 + j % 32;
+}
+
 template <class C>
 __device__ __forceinline__ void clear(gemm16::Acc<C>& acc) {
 #pragma unroll
@@ -211,7 +224,7 @@ __global__ __launch_bounds__(C::THREADS) void xent_loss_kernel(LossArgs a) {
   const int64_t PT = (a.V + C::BP - 1) / C::BP, QT = (rows + C::BQ - 1) / C::BQ;
   if ((int64_t)blockIdx.x >= PT * QT) return;  // whole workgroup
   int64_t pt, qt;
-  raster(gemm::xcd_remap(blockIdx.x, PT * QT), PT, QT, pt, qt);
+  raster(tile_of(blockIdx.x, PT * QT), PT, QT, pt, qt);
   const int64_t p0 = pt * C::BP, q0 = qt * C::BQ;
   const bool direct = FEW || rows == a.M;
   const uint16_t* x = direct ? a.x : a.xc;
@@ -347,7 +360,7 @@ __global__ __launch_bounds__(C::THREADS) void xent_grad_logits_kernel(GradArgs a
   const int64_t PT = (a.nv + C::BP - 1) / C::BP, QT = (rows + C::BQ - 1) / C::BQ;
   if ((int64_t)blockIdx.x >= PT * QT) return;  // whole workgroup
   int64_t pt, qt;
-  raster(gemm::xcd_remap(blockIdx.x, PT * QT), PT, QT, pt, qt);
+  raster(tile_of(blockIdx.x, PT * QT), PT, QT, pt, qt);
   const int64_t p0 = pt * C::BP, q0 = qt * C::BQ;
   const uint16_t* x = rows == a.M ? a.x : a.xc;
   const int64_t ldx = rows == a.M ? a.ldx : a.K;
@@ -411,7 +424,7 @@ __global__ __launch_bounds__(CX::THREADS) void xent_grad_kernel(GradArgs a, int 
   const int64_t bid = blockIdx.x;
   if (bid < NX) {
     using C = CX;
-    const int64_t i = gemm::xcd_remap(bid, NX);
+    const int64_t i = tile_of(bid, NX);
     const int64_t split = i / (PT * QX);
     int64_t pt, qt;
     raster(i % (PT * QX), PT, QX, pt, qt);
@@ -444,7 +457,7 @@ __global__ __launch_bounds__(CX::THREADS) void xent_grad_kernel(GradArgs a, int 
   } else if (bid - NX < NW) {
     using C = CW;
     int64_t pt, qt;
-    raster(gemm::xcd_remap(bid - NX, NW), PT, QW, pt, qt);
+    raster(tile_of(bid - NX, NW), PT, QW, pt, qt);
     const int64_t p0 = pt * C::BP, q0 = qt * C::BQ;
     const int64_t steps = (rows + 2 * kStep - 1) / (2 * kStep) * 2;
     const bool direct = a.r.h->uniform && rows == a.M && rows % kPad == 0;
