@@ -67,9 +67,9 @@ struct Cfg {
 // hold zeros there.
 struct Operand {
   const uint16_t* base;
-  int64_t ld;
+  uint32_t ld;  // bytes
   int rows;
-  int64_t k_rows;
+  int k_rows;
 };
 
 // Tile row held by LDS row r of a permuted kRow P stage (see NI).
@@ -80,10 +80,15 @@ __device__ __forceinline__ int p_row(int r) {
 }
 
 // First p, within the wave's TP, of the four that lane group g holds in MFMA
-// tile i.
+// tile i: p_tile(i) + p_lane(g).  (Split so that what depends on i is a
+// constant of the unrolled code.)
 template <class C>
-__device__ __forceinline__ constexpr int p_of(int i, int g) {
-  return 16 * C::NI * (i / C::NI) + 4 * C::NI * g + 4 * (i % C::NI);
+__device__ __forceinline__ constexpr int p_tile(int i) {
+  return 16 * C::NI * (i / C::NI) + 4 * (i % C::NI);
+}
+template <class C>
+__device__ __forceinline__ constexpr int p_lane(int g) {
+  return 4 * C::NI * g;
 }
 
 __device__ __forceinline__ int col_swizzle(int k) { return 2 * ((k & 3) | (((k >> 4) & 1) << 2)); }
@@ -136,6 +141,14 @@ __device__ __forceinline__ bf16x8 load_frag(uint8_t* st, const FragOffs& f, int 
 template <class C>
 using Acc = v4f[C::FP][C::FQ];
 
+template <class C>
+__device__ __forceinline__ void clear(Acc<C>& acc) {
+#pragma unroll
+  for (int i = 0; i < C::FP; ++i)
+#pragma unroll
+    for (int j = 0; j < C::FQ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+}
+
 // One operand's share of a wave's copies HBM->LDS: N 1-KB copies per k-step,
 // copy c of wave w being block c NWAVES + w.  Byte offsets are relative to the
 // operand's base at the step's first k.
@@ -149,15 +162,14 @@ struct Copier {
   static_assert(!COL || DK % 16 == 0, "swizzle by the copy's parity");
 
   const uint8_t* base;
-  int64_t step, k_rows;    // step: bytes per k
-  uint32_t ld;             // bytes
+  uint32_t ld;  // bytes
+  int k_rows;
   uint32_t at[COL ? 3 : N];  // kRow: the copies' offsets; kCol: k0 and the two chunks' offsets
   int lds;                 // of copy 0
 
   __device__ __forceinline__ Copier(const Operand& o, int wave, int lane)
-      : base(reinterpret_cast<const uint8_t*>(o.base)), k_rows(o.k_rows), ld((uint32_t)(o.ld * 2)),
+      : base(reinterpret_cast<const uint8_t*>(o.base)), ld(o.ld), k_rows(o.k_rows),
         lds((IS_P ? 0 : C::Q_OFF) + wave * 1024) {
-    step = COL ? o.ld * 2 : 2;
     if constexpr (COL) {
       const int k0 = wave * (64 / CH) + lane / CH, last = (o.rows - 1) / 8;
       at[0] = (uint32_t)k0;
@@ -178,21 +190,21 @@ struct Copier {
   }
 
   // copy c of k-step s into stage st
-  __device__ __forceinline__ void issue(int64_t s, uint8_t* st, int c) const {
+  __device__ __forceinline__ void issue(int s, uint8_t* st, int c) const {
 #if defined(__HIP_DEVICE_COMPILE__)
     uint32_t v;
-    int64_t first = s * kStep;
+    int first = s * kStep;
     if constexpr (COL) {
       // k-rows past the last repeat it
       first = first < k_rows ? first : k_rows - 1;
-      const int64_t left = k_rows - 1 - first;
-      const uint32_t lim = left < kStep - 1 ? (uint32_t)left : kStep - 1;
+      const uint32_t left = (uint32_t)(k_rows - 1 - first);
+      const uint32_t lim = left < kStep - 1 ? left : kStep - 1;
       const uint32_t k = at[0] + (uint32_t)(c * DK);
       v = (k < lim ? k : lim) * ld + at[1 + (c & 1)];
     } else {
       v = at[c];
     }
-    const __amdgpu_buffer_rsrc_t rs = gemm::make_rsrc(base + first * step);
+    const __amdgpu_buffer_rsrc_t rs = gemm::make_rsrc(base + (uint64_t)(uint32_t)first * (COL ? ld : 2u));
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         rs, (gemm::lds_void*)(st + lds + c * C::NWAVES * 1024), 16, v, 0, 0, 0);
 #endif
@@ -206,14 +218,14 @@ struct Copiers {
   Copier<C, false> q;
   __device__ __forceinline__ Copiers(const Operand& op, const Operand& oq, int wave, int lane)
       : p(op, wave, lane), q(oq, wave, lane) {}
-  __device__ __forceinline__ void issue(int64_t s, uint8_t* st, int c) const {
+  __device__ __forceinline__ void issue(int s, uint8_t* st, int c) const {
     if (c < C::CP) {
       p.issue(s, st, c);
     } else {
       q.issue(s, st, c - C::CP);
     }
   }
-  __device__ __forceinline__ void issue_all(int64_t s, uint8_t* st) const {
+  __device__ __forceinline__ void issue_all(int s, uint8_t* st) const {
 #pragma unroll
     for (int c = 0; c < C::COPIES; ++c) issue(s, st, c);
   }
@@ -222,7 +234,7 @@ struct Copiers {
 // acc += the product over `steps` k-steps (steps >= 0), few MFMAs per step:
 // the stream of the operands bounds it, so STAGES - 1 steps are in flight.
 template <class C>
-__device__ __forceinline__ void product_deep(const Operand& op, const Operand& oq, int64_t steps,
+__device__ __forceinline__ void product_deep(const Operand& op, const Operand& oq, int steps,
                                              uint8_t* const (&stages)[4], Acc<C>& acc) {
   if (steps <= 0) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -232,10 +244,10 @@ __device__ __forceinline__ void product_deep(const Operand& op, const Operand& o
   const Copiers<C> cp(op, oq, wave, lane);
   // step s lives in stage s % STAGES; past the last step its copies are
   // issued again, never read, so that the wait counts stay constants
-  auto last = [&](int64_t s) { return s < steps ? s : steps - 1; };
+  auto last = [&](int s) { return s < steps ? s : steps - 1; };
 #pragma unroll
   for (int s = 0; s < C::STAGES - 1; ++s) cp.issue_all(last(s), stages[s]);
-  for (int64_t s = 0; s < steps; s += C::STAGES) {
+  for (int s = 0; s < steps; s += C::STAGES) {
 #pragma unroll
     for (int u = 0; u < C::STAGES; ++u) {
       if (s + u < steps) {
@@ -261,43 +273,62 @@ __device__ __forceinline__ void product_deep(const Operand& op, const Operand& o
   gemm::barrier_after_vmcnt<0>();
 }
 
-// acc += the product over `steps` k-steps (even, >= 0), MFMA-bound.
+// A tile of a product: its operands and its k-steps (even, >= 2).
+struct Job {
+  Operand p, q;
+  int steps;
+};
+
+// The tiles number 0 .. n - 1 of one workgroup, MFMA-bound: job(i) describes
+// tile i, done(i, acc) takes its finished sums (it may not touch the stages).
 //
 // Two stages.  A step is 2 FP rows of FQ MFMAs (half h = row / FP, tile i =
 // row mod FP).  Row r's P fragment is read from LDS at row r - D, so that the
 // read is D FQ MFMAs old when it is used; the Q fragments of the second half
 // are read over the first rows.  The step's one barrier stands D rows before
 // its end, when the last fragment of the stage has been read: behind it the
-// next stage has landed (its copies are most of a step old), so the last D
-// rows read the first fragments of the next step, and the copies of the step
-// after it refill the stage just left.  The matrix cores so have work through
-// the barrier and the step's change.  One loop with one exit, without a peeled
-// end: several exits have the compiler move the accumulators between copies of
-// the step, and spill.  So past the last step its copies are issued again and
-// the fragments of a successor that is not there are read, both unused.
-template <class C>
-__device__ __forceinline__ void product(const Operand& op, const Operand& oq, int64_t steps,
-                                        uint8_t* const (&stages)[4], Acc<C>& acc) {
+// next stage has landed, so the last D rows read the first fragments of the
+// next step, and the copies of the step after it refill the stage just left,
+// one per row (a burst would fill the copy queue and hold up the wave).  The
+// matrix cores so have work through the barrier and the step's change.
+//
+// The stream of steps runs on over the tiles: the last steps of a tile copy
+// the first two of the next, whose first fragments are in registers when the
+// tile's sums are handed on, so a tile pays for no empty pipeline.  Past the
+// last tile its own first steps are copied again, unused.  The loop over a
+// tile's steps is one body without a peeled end: with one, the compiler moves
+// the accumulators between the copies of the step, and spills.
+template <class C, class JobF, class DoneF>
+__device__ __forceinline__ void run_tiles(int n, uint8_t* const (&stages)[4], JobF&& job_of,
+                                          DoneF&& done) {
   static_assert(C::STAGES == 2, "two stages");
-  if (steps <= 0) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   const auto fp = frag_offsets<C, true>(wave / C::WQ, lane);
   const auto fq = frag_offsets<C, false>(wave % C::WQ, lane);
-  const Copiers<C> cp(op, oq, wave, lane);
-  constexpr int D = 3, R = 2 * C::FP, RING = D + 1, PER = 1;
+  constexpr int D = 3, R = 2 * C::FP, RING = D + 1;
   static_assert(R % RING == 0 && C::FP > D, "ring of P fragments");
+  static_assert(C::COPIES - D <= R - D, "copies fit a step's rows");
+  // the copies of a step go on into the next step's rows up to this one
+  constexpr int LAST_ROW = C::COPIES - D;
   bf16x8 p[RING], q[2][C::FQ];
 
-  // one step from stage `st`; next: its successor's stage
-  auto step = [&](int64_t s, uint8_t* st, uint8_t* next) {
-    const int64_t refill = s + 2 < steps ? s + 2 : steps - 1;
-    const int64_t refill_next = s + 1 < steps ? s + 1 : steps - 1;
+  if (n <= 0) return;
+  Job job = job_of(0);
+  Copiers<C> cp(job.p, job.q, wave, lane);
+  int off = 0;  // steps of the stream before cp's first
+  auto step = [&](int s, uint8_t* st, uint8_t* next, Acc<C>& acc, const Job& then, bool turn) {
     static_for<0, R>([&](auto r_) {
       constexpr int r = decltype(r_)::value, h = r / C::FP, i = r % C::FP;
       if constexpr (r == R - D) {
         gemm::barrier_after_vmcnt<0>();
         __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (r == LAST_ROW) {
+        if (turn) {  // what is copied from here on is the next tile's
+          cp = Copiers<C>(then.p, then.q, wave, lane);
+          off = s + 2;
+        }
       }
       if constexpr (r + D < R) {
         p[(r + D) % RING] = load_frag<C, true>(st, fp, (r + D) % C::FP, (r + D) / C::FP);
@@ -311,14 +342,13 @@ __device__ __forceinline__ void product(const Operand& op, const Operand& oq, in
         // step's over the last D rows
         if constexpr (j == 0 && r < C::FQ) q[1][r] = load_frag<C, false>(st, fq, r, 1);
         if constexpr (r >= R - D) {
-          constexpr int n = (r - (R - D)) * C::FQ + j;  // of D FQ
-          if constexpr (n < C::FQ) q[0][n] = load_frag<C, false>(next, fq, n, 0);
+          constexpr int m = (r - (R - D)) * C::FQ + j;  // of D FQ
+          if constexpr (m < C::FQ) q[0][m] = load_frag<C, false>(next, fq, m, 0);
         }
-        // PER copies per row, from the barrier's row on and into the next step
-        constexpr int row = (r + D) % R, n = row * PER + j;
-        if constexpr (j < PER && n < C::COPIES) {
-          if constexpr (r >= R - D) cp.issue(refill, st, n);
-          else cp.issue(refill_next, next, n);
+        constexpr int c = (r + D) % R;
+        if constexpr (j == 0 && c < C::COPIES) {
+          if constexpr (r >= R - D) cp.issue(s + 2 - off, st, c);
+          else cp.issue(s + 1 - off, next, c);
         }
         __builtin_amdgcn_sched_barrier(0);
       });
@@ -327,18 +357,31 @@ __device__ __forceinline__ void product(const Operand& op, const Operand& oq, in
 
   cp.issue_all(0, stages[0]);
 #pragma unroll
-  for (int n = 0; n < D * PER && n < C::COPIES; ++n) cp.issue(1, stages[1], n);
-  gemm::barrier_after_vmcnt<(D * PER < C::COPIES ? D * PER : C::COPIES)>();
+  for (int c = 0; c < D && c < C::COPIES; ++c) cp.issue(1, stages[1], c);
+  gemm::barrier_after_vmcnt<(D < C::COPIES ? D : C::COPIES)>();
 #pragma unroll
   for (int j = 0; j < C::FQ; ++j) q[0][j] = load_frag<C, false>(stages[0], fq, j, 0);
 #pragma unroll
   for (int r = 0; r < D; ++r) p[r] = load_frag<C, true>(stages[0], fp, r, 0);
-  for (int64_t s = 0; s < steps; s += 2) {
-    step(s, stages[0], stages[1]);
-    step(s + 1, stages[1], stages[0]);
+
+  for (int i = 0;;) {
+    const bool more = i + 1 < n;
+    const Job then = job_of(more ? i + 1 : i);
+    Acc<C> acc;
+    clear<C>(acc);
+    for (int s = 0; s < job.steps; s += 2) {
+      step(s, stages[0], stages[1], acc, then, s + 2 == job.steps);
+      step(s + 1, stages[1], stages[0], acc, then, false);
+    }
+    off = 0;
+    done(i, acc);
+    if (!more) break;
+    job = then;
+    ++i;
   }
-  // the copies past the last step have landed before the stages are left
-  gemm::wait_vmcnt<0>();
+  // the copies past the last step have landed, and every wave has left the
+  // stages
+  gemm::barrier_after_vmcnt<0>();
 }
 
 // The stage buffers: separate objects, so that the compiler can tell reads of

@@ -45,10 +45,18 @@ using DxCfg = gemm16::Cfg<256, 256, 2, 4, 2, kCol, kRow>;
 using DwCfg = gemm16::Cfg<256, 256, 2, 4, 2, kCol, kCol>;
 
 constexpr int64_t kTile = 256;
+constexpr int64_t kMaxTiles = INT32_MAX;  // of one launch: tile numbers are 32 bits
 constexpr int64_t kPad = 2 * kStep;  // k-steps come in pairs
 constexpr int64_t kFewXentRows = 64;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Workgroups for `tiles` tiles: one per compute unit at most (each holds most
+// of its LDS), every one taking its share.
+dim3 tile_grid(int64_t tiles) {
+  const int64_t cus = gemm::device_cus() > 0 ? gemm::device_cus() : 256;
+  return dim3((unsigned)(tiles < cus ? tiles : cus));
+}
 
 // What the row pass leaves for the others.
 struct Header {
@@ -167,39 +175,40 @@ __global__ __launch_bounds__(256) void xent_pack_kernel(const uint16_t* x, int64
   }
 }
 
-// Tile (pt, qt) number i of a raster of PT x QT tiles: 8 p-tiles x all
-// q-tiles, in blocks of 8 x 4, before the next 8 p-tiles.
-__device__ __forceinline__ void raster(int64_t i, int64_t PT, int64_t QT, int64_t& pt,
-                                       int64_t& qt) {
-  constexpr int64_t GP = 8, GQ = 4;
-  const int64_t p0 = i / (GP * QT) * GP, r = i % (GP * QT);
-  const int64_t gp = PT - p0 < GP ? PT - p0 : GP;
-  const int64_t q0 = r / (GQ * gp) * GQ, rr = r % (GQ * gp);
-  const int64_t gq = QT - q0 < GQ ? QT - q0 : GQ;
-  qt = q0 + rr % gq;
-  pt = p0 + rr / gq;
+// Tile number `i` of a raster of PT x QT tiles: 8 p-tiles x all q-tiles, in
+// blocks of 8 x 4, before the next 8 p-tiles.
+struct TileAt {
+  uint32_t p, q;
+};
+__device__ __forceinline__ TileAt raster(uint32_t i, uint32_t PT, uint32_t QT) {
+  constexpr uint32_t GP = 8, GQ = 4;
+  const uint32_t p0 = i / (GP * QT) * GP, r = i % (GP * QT);
+  const uint32_t gp = PT - p0 < GP ? PT - p0 : GP;
+  const uint32_t q0 = r / (GQ * gp) * GQ, rr = r % (GQ * gp);
+  const uint32_t gq = QT - q0 < GQ ? QT - q0 : GQ;
+  return {p0 + rr / gq, q0 + rr % gq};
 }
 
-// Tile number of workgroup `bid` of T: workgroups go round-robin to the 8
-// XCDs, 32 compute units each.  Every full round of 256 tiles gives each XCD
-// 32 consecutive tiles of the raster (an 8 x 4 block sharing its L2) and the
-// XCDs neighbouring blocks, so that a panel of the large operand, which
-// several XCDs need, is wanted by all of them at one time and comes from HBM
-// once.  The rest of the tiles is dealt evenly.  A bijection of [0, T).
-__device__ __forceinline__ int64_t tile_of(int64_t bid, int64_t T) {
-  const int64_t full = T / 256 * 256;
-  if (bid >= full) return full + gemm::xcd_remap(bid - full, T - full);
-  const int64_t x = bid % 8, j = bid / 8;
+// Tile number in the raster of the number `i` of T in order of work:
+// workgroups go round-robin to the 8 XCDs, 32 compute units each.  Every full
+// round of 256 tiles gives each XCD 32 consecutive tiles of the raster (an
+// 8 x 4 block sharing its L2) and the XCDs neighbouring blocks, so that a
+// panel of the large operand, which several XCDs need, is wanted by all of
+// them at one time and comes from HBM once.  The rest of the tiles is dealt
+// evenly.  A bijection of [0, T).
+__device__ __forceinline__ uint32_t in_rounds(uint32_t i, uint32_t T) {
+  const uint32_t full = T / 256 * 256;
+  if (i >= full) return full + (uint32_t)gemm::xcd_remap(i - full, T - full);
+  const uint32_t x = i % 8, j = i / 8;
   return j / 32 * 256 + x * 32 + j % 32;
 }
 
-template <class C>
-__device__ __forceinline__ void clear(gemm16::Acc<C>& acc) {
-#pragma unroll
-  for (int i = 0; i < C::FP; ++i)
-#pragma unroll
-    for (int j = 0; j < C::FQ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+// Tiles number w, w + G, ... of T for workgroup w of G.
+__device__ __forceinline__ int share(uint32_t T, uint32_t w, uint32_t G) {
+  return w < T ? (int)((T - w - 1) / G + 1) : 0;
 }
+
+__device__ __forceinline__ uint32_t ld2(int64_t ld) { return (uint32_t)(2 * ld); }
 
 struct LossArgs {
   const uint16_t* x;
@@ -215,30 +224,11 @@ struct LossArgs {
   float* at;              // logit of each row's target
 };
 
-// Forward: one tile of logits -> the rows' pairs over each wave's TP columns.
+// A tile's logits -> its rows' pairs over each wave's TP columns, and the
+// targets' logits.
 template <class C, bool FEW>
-__global__ __launch_bounds__(C::THREADS) void xent_loss_kernel(LossArgs a) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  FP8BS_GEMM16_STAGES(C);
-  const int64_t rows = FEW ? a.M : a.r.h->rows;
-  const int64_t PT = (a.V + C::BP - 1) / C::BP, QT = (rows + C::BQ - 1) / C::BQ;
-  if ((int64_t)blockIdx.x >= PT * QT) return;  // whole workgroup
-  int64_t pt, qt;
-  raster(tile_of(blockIdx.x, PT * QT), PT, QT, pt, qt);
-  const int64_t p0 = pt * C::BP, q0 = qt * C::BQ;
-  const bool direct = FEW || rows == a.M;
-  const uint16_t* x = direct ? a.x : a.xc;
-  const int64_t ldx = direct ? a.ldx : a.K;
-  const Operand op{a.w + p0 * a.ldw, a.ldw, (int)(a.V - p0 < C::BP ? a.V - p0 : C::BP), 0};
-  const Operand oq{x + q0 * ldx, ldx, (int)(rows - q0 < C::BQ ? rows - q0 : C::BQ), 0};
-  gemm16::Acc<C> acc;
-  clear<C>(acc);
-  if constexpr (FEW) {
-    gemm16::product_deep<C>(op, oq, a.K / kStep, stages, acc);
-  } else {
-    gemm16::product<C>(op, oq, a.K / kStep, stages, acc);
-  }
-
+__device__ __forceinline__ void reduce_logits(const LossArgs& a, int64_t rows, int64_t p0,
+                                              int64_t q0, gemm16::Acc<C>& acc) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
   const int wp = wave / C::WQ, wq = wave % C::WQ;
@@ -246,25 +236,26 @@ __global__ __launch_bounds__(C::THREADS) void xent_loss_kernel(LossArgs a) {
   if (pw >= a.V) return;
   const int64_t left = a.V - pw;
   const int n = left < C::TP ? (int)left : C::TP;  // its valid columns
+  const int pl = gemm16::p_lane<C>(g);
+  if (n < C::TP) {  // the vocabulary ends here
+#pragma unroll
+    for (int i = 0; i < C::FP; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const bool past = gemm16::p_tile<C>(i) + r >= n - pl;
+#pragma unroll
+        for (int j = 0; j < C::FQ; ++j) acc[i][j][r] = past ? -INFINITY : acc[i][j][r];
+      }
+  }
 #pragma unroll
   for (int j = 0; j < C::FQ; ++j) {
     const int64_t q = q0 + wq * C::TQ + 16 * j + l16;
     const bool real = q < rows;
-    float m = -INFINITY;
-    if (n == C::TP) {
+    float m = acc[0][j][0];
 #pragma unroll
-      for (int i = 0; i < C::FP; ++i)
+    for (int i = 0; i < C::FP; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) m = fmaxf(m, acc[i][j][r]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < C::FP; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if (gemm16::p_of<C>(i, g) + r >= n) acc[i][j][r] = -INFINITY;
-          m = fmaxf(m, acc[i][j][r]);
-        }
-    }
+      for (int r = 0; r < 4; ++r) m = fmaxf(m, acc[i][j][r]);
     m = fmaxf(m, __shfl_xor(m, 16, 64));
     m = fmaxf(m, __shfl_xor(m, 32, 64));
     // a block of -inf logits alone has no sum
@@ -281,14 +272,62 @@ __global__ __launch_bounds__(C::THREADS) void xent_loss_kernel(LossArgs a) {
     // the target's logit, on the one lane that holds it
     int64_t t = -1;
     if (real) t = FEW ? a.target[q] : (int64_t)a.r.target[q];
-    const int64_t d = t - pw;
-    if (__any(d >= 0 && d < n)) {
+    const int64_t tp = t - pw;
+    if (__any(tp >= 0 && tp < n)) {
+      const int d = tp >= 0 && tp < n ? (int)tp - pl : -1;
+      float at = 0.0f;
+      bool here = false;
 #pragma unroll
       for (int i = 0; i < C::FP; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (d == gemm16::p_of<C>(i, g) + r) a.at[q] = acc[i][j][r];
+        for (int r = 0; r < 4; ++r) {
+          const bool hit = d == gemm16::p_tile<C>(i) + r;
+          at = hit ? acc[i][j][r] : at;
+          here = here || hit;
+        }
+      if (here) a.at[q] = at;
     }
+    __builtin_amdgcn_sched_barrier(0);  // one j at a time: few registers beside the sums
+  }
+}
+
+// Forward.  FEW: one tile per workgroup, bound by the stream of w; otherwise
+// every workgroup takes its share of the tiles.
+template <class C, bool FEW>
+__global__ __launch_bounds__(C::THREADS) void xent_loss_kernel(LossArgs a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  FP8BS_GEMM16_STAGES(C);
+  const int64_t rows = FEW ? a.M : a.r.h->rows;
+  const uint32_t PT = (uint32_t)((a.V + C::BP - 1) / C::BP), QT = (uint32_t)((rows + C::BQ - 1) / C::BQ);
+  const bool direct = FEW || rows == a.M;
+  const uint16_t* x = direct ? a.x : a.xc;
+  const int64_t ldx = direct ? a.ldx : a.K;
+  auto job_at = [&](int64_t p0, int64_t q0) {
+    return gemm16::Job{
+        {a.w + p0 * a.ldw, ld2(a.ldw), (int)(a.V - p0 < C::BP ? a.V - p0 : C::BP), 0},
+        {x + q0 * ldx, ld2(ldx), (int)(rows - q0 < C::BQ ? rows - q0 : C::BQ), 0},
+        (int)(a.K / kStep)};
+  };
+  if constexpr (FEW) {
+    const int64_t p0 = (int64_t)blockIdx.x * C::BP;
+    const gemm16::Job j = job_at(p0, 0);
+    gemm16::Acc<C> acc;
+    gemm16::clear<C>(acc);
+    gemm16::product_deep<C>(j.p, j.q, j.steps, stages, acc);
+    reduce_logits<C, FEW>(a, rows, p0, 0, acc);
+  } else {
+    const uint32_t T = PT * QT, w = blockIdx.x, G = gridDim.x;
+    auto at = [&](int i) { return raster(in_rounds(w + (uint32_t)i * G, T), PT, QT); };
+    gemm16::run_tiles<C>(
+        share(T, w, G), stages,
+        [&](int i) {
+          const TileAt t = at(i);
+          return job_at((int64_t)t.p * C::BP, (int64_t)t.q * C::BQ);
+        },
+        [&](int i, gemm16::Acc<C>& acc) {
+          const TileAt t = at(i);
+          reduce_logits<C, FEW>(a, rows, (int64_t)t.p * C::BP, (int64_t)t.q * C::BQ, acc);
+        });
   }
 #endif
 }
@@ -350,40 +389,28 @@ struct GradArgs {
   int64_t lddw;
 };
 
-// Backward, first launch of a piece: logits rebuilt, G stored.  Rows past the
-// last and columns past the vocabulary are zeros up to whole tiles.
+// A tile's logits -> G.  Rows past the last and columns past the vocabulary
+// are zeros up to whole tiles.
 template <class C>
-__global__ __launch_bounds__(C::THREADS) void xent_grad_logits_kernel(GradArgs a) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  FP8BS_GEMM16_STAGES(C);
-  const int64_t rows = a.r.h->rows;
-  const int64_t PT = (a.nv + C::BP - 1) / C::BP, QT = (rows + C::BQ - 1) / C::BQ;
-  if ((int64_t)blockIdx.x >= PT * QT) return;  // whole workgroup
-  int64_t pt, qt;
-  raster(tile_of(blockIdx.x, PT * QT), PT, QT, pt, qt);
-  const int64_t p0 = pt * C::BP, q0 = qt * C::BQ;
-  const uint16_t* x = rows == a.M ? a.x : a.xc;
-  const int64_t ldx = rows == a.M ? a.ldx : a.K;
-  const Operand op{a.w + (a.v0 + p0) * a.ldw, a.ldw,
-                   (int)(a.nv - p0 < C::BP ? a.nv - p0 : C::BP), 0};
-  const Operand oq{x + q0 * ldx, ldx, (int)(rows - q0 < C::BQ ? rows - q0 : C::BQ), 0};
-  gemm16::Acc<C> acc;
-  clear<C>(acc);
-  gemm16::product<C>(op, oq, a.K / kStep, stages, acc);
-
+__device__ __forceinline__ void store_g(const GradArgs& a, int64_t rows, int64_t p0, int64_t q0,
+                                        const gemm16::Acc<C>& acc) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
   const int wp = wave / C::WQ, wq = wave % C::WQ;
   const int64_t pw = p0 + wp * C::TP;
-  const int64_t n = a.nv - pw;  // columns from pw on (<= 0: none)
+  const int64_t left = a.nv - pw;  // columns from pw on (<= 0: none)
+  const int pl = gemm16::p_lane<C>(g);
+  const int n = (left < C::TP ? (int)left : C::TP) - pl;  // the lane's first column past them
   static_assert(C::NI == 4, "runs of 16 columns per lane");
 #pragma unroll
   for (int j = 0; j < C::FQ; ++j) {
     const int64_t q = q0 + wq * C::TQ + 16 * j + l16;
     const bool real = q < rows;
     const float b = real ? -a.r.lse[q] * kLog2e : 0.0f;
-    const int64_t t = real ? (int64_t)a.r.target[q] - (a.v0 + pw) : -1;
-    uint16_t* dst = a.g + q * a.ldg + pw;
+    const int64_t tp = real ? (int64_t)a.r.target[q] - (a.v0 + pw) : -1;
+    const int t = tp >= 0 && tp < C::TP ? (int)tp - pl : -1;
+    const int last = real ? n : -C::TP;  // a row past the last: zeros
+    uint16_t* dst = a.g + q * a.ldg + pw + pl;
 #pragma unroll
     for (int i4 = 0; i4 < C::FP; i4 += 4) {
       uint32_t o[8];
@@ -393,23 +420,99 @@ __global__ __launch_bounds__(C::THREADS) void xent_grad_logits_kernel(GradArgs a
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
           const int i = i4 + e / 2, r = 2 * (e & 1) + z;
-          const int p = gemm16::p_of<C>(i, g) + r;
+          const int p = gemm16::p_tile<C>(i) + r;
           float v = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, b));
           v = t == p ? v - 1.0f : v;
-          f[z] = real && p < n ? v : 0.0f;
+          f[z] = p < last ? v : 0.0f;
         }
         o[e] = bf16x2_rne(f[0], f[1]);
       }
-      uint16_t* d = dst + gemm16::p_of<C>(i4, g);
+      uint16_t* d = dst + gemm16::p_tile<C>(i4);
       *reinterpret_cast<u32x4*>(d) = u32x4{o[0], o[1], o[2], o[3]};
       *reinterpret_cast<u32x4*>(d + 8) = u32x4{o[4], o[5], o[6], o[7]};
     }
+    __builtin_amdgcn_sched_barrier(0);  // one j at a time: few registers beside the sums
   }
+}
+
+// Backward, first launch of a piece: logits rebuilt, G stored.
+template <class C>
+__global__ __launch_bounds__(C::THREADS) void xent_grad_logits_kernel(GradArgs a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  FP8BS_GEMM16_STAGES(C);
+  const int64_t rows = a.r.h->rows;
+  const uint32_t PT = (uint32_t)((a.nv + C::BP - 1) / C::BP), QT = (uint32_t)((rows + C::BQ - 1) / C::BQ);
+  const uint16_t* x = rows == a.M ? a.x : a.xc;
+  const int64_t ldx = rows == a.M ? a.ldx : a.K;
+  const uint32_t T = PT * QT, w = blockIdx.x, G = gridDim.x;
+  auto at = [&](int i) { return raster(in_rounds(w + (uint32_t)i * G, T), PT, QT); };
+  gemm16::run_tiles<C>(
+      share(T, w, G), stages,
+      [&](int i) {
+        const TileAt t = at(i);
+        const int64_t p0 = (int64_t)t.p * C::BP, q0 = (int64_t)t.q * C::BQ;
+        return gemm16::Job{{a.w + (a.v0 + p0) * a.ldw, ld2(a.ldw),
+                            (int)(a.nv - p0 < C::BP ? a.nv - p0 : C::BP), 0},
+                           {x + q0 * ldx, ld2(ldx),
+                            (int)(rows - q0 < C::BQ ? rows - q0 : C::BQ), 0},
+                           (int)(a.K / kStep)};
+      },
+      [&](int i, const gemm16::Acc<C>& acc) {
+        const TileAt t = at(i);
+        store_g<C>(a, rows, (int64_t)t.p * C::BP, (int64_t)t.q * C::BQ, acc);
+      });
 #endif
 }
 
-// Backward, second launch of a piece: tiles of its part of dx (first, they are
-// the longer ones), then of its dw.
+// A tile of a piece's part of dx, added to the earlier pieces'.
+template <class C>
+__device__ __forceinline__ void add_dx(const GradArgs& a, int64_t rows, bool first, int64_t split,
+                                       int64_t p0, int64_t q0, const gemm16::Acc<C>& acc) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  const int64_t pw = p0 + wave / C::WQ * C::TP;
+  float* out = a.dxp + split * a.M * a.K;
+  if (pw >= a.K) return;  // K is a multiple of 128: a wave's columns exist or do not
+#pragma unroll
+  for (int j = 0; j < C::FQ; ++j) {
+    const int64_t q = q0 + wave % C::WQ * C::TQ + 16 * j + l16;
+    if (q >= rows) continue;
+#pragma unroll
+    for (int i = 0; i < C::FP; ++i) {
+      v4f* d = reinterpret_cast<v4f*>(out + q * a.K + pw + gemm16::p_lane<C>(g) + gemm16::p_tile<C>(i));
+      *d = first ? acc[i][j] : *d + acc[i][j];
+    }
+  }
+}
+
+// A tile of a piece's dw.
+template <class C>
+__device__ __forceinline__ void store_dw(const GradArgs& a, int64_t p0, int64_t q0,
+                                         const gemm16::Acc<C>& acc) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  const int64_t pw = p0 + wave / C::WQ * C::TP;
+  const float c = a.r.h->c;
+  if (pw >= a.K) return;
+#pragma unroll
+  for (int j = 0; j < C::FQ; ++j) {
+    const int64_t q = q0 + wave % C::WQ * C::TQ + 16 * j + l16;
+    if (q >= a.nv) continue;
+#pragma unroll
+    for (int i = 0; i < C::FP; ++i) {
+      const v4f v = acc[i][j] * c;
+      *reinterpret_cast<u32x2*>(a.dw + (a.v0 + q) * a.lddw + pw + gemm16::p_lane<C>(g) + gemm16::p_tile<C>(i)) =
+          u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+    }
+  }
+}
+
+// Backward, second launch of a piece: tiles of its part of dx, then of its
+// dw.  The dx tiles, long, go round the workgroups; those left out of the last
+// round of them take dw tiles worth a dx tile's steps meanwhile; the other dw
+// tiles go round all workgroups.  kTileSteps: a tile's start and end in steps.
+constexpr uint32_t kTileSteps = 3;
+
 template <class CX, class CW>
 __global__ __launch_bounds__(CX::THREADS) void xent_grad_kernel(GradArgs a, int first) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -417,73 +520,78 @@ __global__ __launch_bounds__(CX::THREADS) void xent_grad_kernel(GradArgs a, int 
                     CX::THREADS == CW::THREADS, "one workgroup shape");
   FP8BS_GEMM16_STAGES(CX);
   const int64_t rows = a.r.h->rows;
-  const int64_t PT = (a.K + CX::BP - 1) / CX::BP, QX = (rows + CX::BQ - 1) / CX::BQ;
-  const int64_t NX = PT * QX * a.splits, QW = (a.nv + CW::BQ - 1) / CW::BQ, NW = PT * QW;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
-  const int64_t bid = blockIdx.x;
-  if (bid < NX) {
+  const uint32_t w = blockIdx.x, G = gridDim.x;
+  const uint32_t PT = (uint32_t)((a.K + CX::BP - 1) / CX::BP), QX = (uint32_t)((rows + CX::BQ - 1) / CX::BQ);
+  // k-steps in pairs; G is zero past the vocabulary, up to whole tiles
+  const uint32_t pairs = (uint32_t)((a.nv + 2 * kStep - 1) / (2 * kStep));
+  const uint32_t splits = (uint32_t)a.splits < pairs ? (uint32_t)a.splits : pairs;
+  const uint32_t NX = PT * QX * splits;
+  {
     using C = CX;
-    const int64_t i = tile_of(bid, NX);
-    const int64_t split = i / (PT * QX);
-    int64_t pt, qt;
-    raster(i % (PT * QX), PT, QX, pt, qt);
-    const int64_t p0 = pt * C::BP, q0 = qt * C::BQ;
-    // in pairs of k-steps; G is zero past the vocabulary, up to whole tiles
-    const int64_t pairs = (a.nv + 2 * kStep - 1) / (2 * kStep);
-    const int64_t s0 = pairs * split / a.splits * 2, s1 = pairs * (split + 1) / a.splits * 2;
-    const int64_t k0 = s0 * kStep;
-    const Operand op{a.w + (a.v0 + k0) * a.ldw + p0, a.ldw,
-                     (int)(a.K - p0 < C::BP ? a.K - p0 : C::BP), a.nv - k0};
-    // G holds whole tiles of rows
-    const Operand oq{a.g + q0 * a.ldg + k0, a.ldg, C::BQ, 0};
-    gemm16::Acc<C> acc;
-    clear<C>(acc);
-    gemm16::product<C>(op, oq, s1 - s0, stages, acc);
-    const int wp = wave / C::WQ, wq = wave % C::WQ;
-    float* out = a.dxp + split * a.M * a.K;
-#pragma unroll
-    for (int j = 0; j < C::FQ; ++j) {
-      const int64_t q = q0 + wq * C::TQ + 16 * j + l16;
-      if (q >= rows) continue;
-#pragma unroll
-      for (int i2 = 0; i2 < C::FP; ++i2) {
-        const int64_t p = p0 + wp * C::TP + gemm16::p_of<C>(i2, g);
-        if (p >= a.K) continue;
-        v4f* d = reinterpret_cast<v4f*>(out + q * a.K + p);
-        *d = first ? acc[i2][j] : *d + acc[i2][j];
-      }
-    }
-  } else if (bid - NX < NW) {
+    auto at = [&](int i, uint32_t& split) {
+      const uint32_t n = in_rounds(w + (uint32_t)i * G, NX);
+      split = n / (PT * QX);
+      return raster(n % (PT * QX), PT, QX);
+    };
+    gemm16::run_tiles<C>(
+        share(NX, w, G), stages,
+        [&](int i) {
+          uint32_t split;
+          const TileAt t = at(i, split);
+          const int64_t p0 = (int64_t)t.p * C::BP, q0 = (int64_t)t.q * C::BQ;
+          const int64_t s0 = (int64_t)pairs * split / splits * 2;
+          const int64_t s1 = (int64_t)pairs * (split + 1) / splits * 2, k0 = s0 * kStep;
+          return gemm16::Job{{a.w + (a.v0 + k0) * a.ldw + p0, ld2(a.ldw),
+                              (int)(a.K - p0 < C::BP ? a.K - p0 : C::BP), (int)(a.nv - k0)},
+                             // G: whole tiles of rows
+                             {a.g + q0 * a.ldg + k0, ld2(a.ldg), C::BQ, 0},
+                             (int)(s1 - s0)};
+        },
+        [&](int i, const gemm16::Acc<C>& acc) {
+          uint32_t split;
+          const TileAt t = at(i, split);
+          add_dx<C>(a, rows, first, split, (int64_t)t.p * C::BP, (int64_t)t.q * C::BQ, acc);
+        });
+  }
+  {
     using C = CW;
-    int64_t pt, qt;
-    raster(tile_of(bid - NX, NW), PT, QW, pt, qt);
-    const int64_t p0 = pt * C::BP, q0 = qt * C::BQ;
-    const int64_t steps = (rows + 2 * kStep - 1) / (2 * kStep) * 2;
+    const uint32_t QW = (uint32_t)((a.nv + C::BQ - 1) / C::BQ), NW = PT * QW;
+    const uint32_t steps = (uint32_t)((rows + 2 * kStep - 1) / (2 * kStep) * 2);
+    // early tiles: `ahead` for each of the workgroups behind the last round
+    const uint32_t last = NX % G, behind = last ? G - last : 0;
+    uint32_t ahead = last ? (2 * pairs / splits + kTileSteps) / (steps + kTileSteps) : 0;
+    if (ahead * behind > NW) ahead = NW / behind;
+    const uint32_t early = ahead * behind, mine = behind && w >= last ? ahead : 0;
+    auto at = [&](int i) {
+      const uint32_t n = (uint32_t)i < mine ? w - last + (uint32_t)i * behind
+                                            : early + w + ((uint32_t)i - mine) * G;
+      return raster(n < early ? n : early + in_rounds(n - early, NW - early), PT, QW);
+    };
+    const int n = (int)mine + share(NW - early, w, G);
+    auto finish = [&](int i, const gemm16::Acc<C>& acc) {
+      const TileAt t = at(i);
+      store_dw<C>(a, (int64_t)t.p * C::BP, (int64_t)t.q * C::BQ, acc);
+    };
+    if (steps == 0) {  // no row has a loss
+      gemm16::Acc<C> zero;
+      gemm16::clear<C>(zero);
+      for (int i = 0; i < n; ++i) finish(i, zero);
+      return;
+    }
     const bool direct = a.r.h->uniform && rows == a.M && rows % kPad == 0;
     const uint16_t* x = direct ? a.x : a.r.h->uniform ? a.xc : a.xs;
     const int64_t ldx = direct ? a.ldx : a.K;
-    const int64_t kr = steps * kStep;
-    const Operand op{x + p0, ldx, (int)(a.K - p0 < C::BP ? a.K - p0 : C::BP), kr};
-    const Operand oq{a.g + q0, a.ldg, C::BQ, kr};
-    gemm16::Acc<C> acc;
-    clear<C>(acc);
-    gemm16::product<C>(op, oq, steps, stages, acc);
-    const int wp = wave / C::WQ, wq = wave % C::WQ;
-    const float c = a.r.h->c;
-#pragma unroll
-    for (int j = 0; j < C::FQ; ++j) {
-      const int64_t q = q0 + wq * C::TQ + 16 * j + l16;
-      if (q >= a.nv) continue;
-#pragma unroll
-      for (int i = 0; i < C::FP; ++i) {
-        const int64_t p = p0 + wp * C::TP + gemm16::p_of<C>(i, g);
-        if (p >= a.K) continue;
-        const v4f v = acc[i][j] * c;
-        *reinterpret_cast<u32x2*>(a.dw + (a.v0 + q) * a.lddw + p) =
-            u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
-      }
-    }
+    gemm16::run_tiles<C>(
+        n, stages,
+        [&](int i) {
+          const TileAt t = at(i);
+          const int64_t p0 = (int64_t)t.p * C::BP, q0 = (int64_t)t.q * C::BQ;
+          return gemm16::Job{{x + p0, ld2(ldx), (int)(a.K - p0 < C::BP ? a.K - p0 : C::BP),
+                              (int)steps * kStep},
+                             {a.g + q0, ld2(a.ldg), C::BQ, (int)steps * kStep},
+                             (int)steps};
+        },
+        finish);
   }
 #endif
 }
@@ -620,7 +728,7 @@ hipError_t launch_xent(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_
   }
   using C = LogitsCfg;
   const int64_t tiles = cdiv(V, C::BP) * cdiv(M, C::BQ);
-  if (tiles > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  if (tiles > kMaxTiles) return hipErrorInvalidConfiguration;
   e = launch_kernel(xent_rows_kernel, dim3(1), dim3(1024), stream, target, M, V, ignore, p.r,
                     static_cast<const float*>(nullptr), static_cast<const float*>(nullptr), loss,
                     lse);
@@ -628,7 +736,7 @@ hipError_t launch_xent(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_
   e = launch_kernel(xent_pack_kernel, dim3((unsigned)cdiv(cdiv(M, kPad) * kPad, 4)), dim3(256),
                     stream, x, ldx, M, K, p.r, p.xc, static_cast<uint16_t*>(nullptr));
   if (e != hipSuccess) return e;
-  e = launch_kernel(xent_loss_kernel<C, false>, dim3((unsigned)tiles), dim3(C::THREADS), stream, a);
+  e = launch_kernel(xent_loss_kernel<C, false>, tile_grid(tiles), dim3(C::THREADS), stream, a);
   if (e != hipSuccess) return e;
   return launch_kernel(xent_join_kernel<false>, dim3((unsigned)cdiv(M, 4)), dim3(256), stream, a,
                        ignore, loss, lse);
@@ -643,7 +751,7 @@ hipError_t launch_xent_backward(const uint16_t* x, int64_t ldx, const uint16_t* 
   GradArgs a{x, ldx, p.xc, p.xs, w, ldw, M, V, K, p.r, p.g, p.ldg, 0, 0, p.dxp, p.splits, dw, lddw};
   const int64_t MT = cdiv(M, kTile), KT = cdiv(K, kTile);
   const int64_t t1 = MT * (p.ldg / kTile), t2 = KT * (MT * p.splits + p.ldg / kTile);
-  if (t1 > 0x7FFFFFFF || t2 > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  if (t1 > kMaxTiles || t2 > kMaxTiles) return hipErrorInvalidConfiguration;
   hipError_t e = launch_kernel(xent_rows_kernel, dim3(1), dim3(1024), stream, target, M, V, ignore,
                                p.r, lse, dloss, static_cast<float*>(nullptr),
                                static_cast<float*>(nullptr));
@@ -657,11 +765,11 @@ hipError_t launch_xent_backward(const uint16_t* x, int64_t ldx, const uint16_t* 
     a.v0 = i * p.ldg;
     a.nv = V - a.v0 < p.ldg ? V - a.v0 : p.ldg;
     if (M > 0) {
-      e = launch_kernel(xent_grad_logits_kernel<LogitsCfg>, dim3((unsigned)t1),
+      e = launch_kernel(xent_grad_logits_kernel<LogitsCfg>, tile_grid(t1),
                         dim3(LogitsCfg::THREADS), stream, a);
       if (e != hipSuccess) return e;
     }
-    e = launch_kernel(xent_grad_kernel<DxCfg, DwCfg>, dim3((unsigned)t2), dim3(DxCfg::THREADS),
+    e = launch_kernel(xent_grad_kernel<DxCfg, DwCfg>, tile_grid(t2), dim3(DxCfg::THREADS),
                       stream, a, i == 0 ? 1 : 0);
     if (e != hipSuccess) return e;
   }
