@@ -36,26 +36,42 @@ using gemm16::kStep;
 using gemm16::Operand;
 
 
-// Large tiles, and the tile of few rows.  q are the rows of x, p the
-// vocabulary.
+// Logits: q are the rows of x, p the vocabulary.  Large tiles, their half for a
+// last tile of at most 128 rows, and the small tile of few rows or small heads
+// (deep stream).
 using LogitsCfg = gemm16::Cfg<256, 256, 2, 4, 2, kRow, kRow>;
-using LogitsFewCfg = gemm16::Cfg<128, 64, 4, 1, 4, kRow, kRow>;
+using LogitsHalf = gemm16::Cfg<256, 128, 4, 2, 2, kRow, kRow>;
+using LogitsSmall = gemm16::Cfg<128, 64, 4, 1, 4, kRow, kRow>;
 // dx: q rows, p hidden, k vocabulary.  dw: q vocabulary, p hidden, k rows.
+// Large, and small (two workgroups per compute unit).
 using DxCfg = gemm16::Cfg<256, 256, 2, 4, 2, kCol, kRow>;
 using DwCfg = gemm16::Cfg<256, 256, 2, 4, 2, kCol, kCol>;
+using DxSmall = gemm16::Cfg<128, 128, 2, 2, 2, kCol, kRow>;
+using DwSmall = gemm16::Cfg<128, 128, 2, 2, 2, kCol, kCol>;
 
 constexpr int64_t kTile = 256;
 constexpr int64_t kMaxTiles = INT32_MAX;  // of one launch: tile numbers are 32 bits
 constexpr int64_t kPad = 2 * kStep;  // k-steps come in pairs
-constexpr int64_t kFewXentRows = 64;
+constexpr int64_t kFewXentRows = LogitsSmall::BQ;  // these are not packed
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Workgroups for `tiles` tiles: one per compute unit at most (each holds most
-// of its LDS), every one taking its share.
-dim3 tile_grid(int64_t tiles) {
-  const int64_t cus = gemm::device_cus() > 0 ? gemm::device_cus() : 256;
-  return dim3((unsigned)(tiles < cus ? tiles : cus));
+int64_t compute_units() { return gemm::device_cus() > 0 ? gemm::device_cus() : 256; }
+
+// Workgroups for `tiles` tiles, `per_cu` of them resident on a compute unit,
+// every one taking its share.
+dim3 tile_grid(int64_t tiles, int64_t per_cu = 1) {
+  const int64_t most = compute_units() * per_cu;
+  return dim3((unsigned)(tiles < most ? tiles : most));
+}
+
+// Whether a head's logits take the small tiles: by the estimated rounds of
+// workgroups, a round of 256x256 and of 128x64 tiles taking 100 and kSmallCost.
+constexpr int64_t kSmallCost = 35;
+bool small_logits(int64_t M, int64_t V) {
+  const int64_t cus = compute_units();
+  return kSmallCost * cdiv(cdiv(M, LogitsSmall::BQ) * cdiv(V, LogitsSmall::BP), cus) <
+         100 * cdiv(cdiv(M, LogitsCfg::BQ) * cdiv(V, LogitsCfg::BP), cus);
 }
 
 // What the row pass leaves for the others.
@@ -219,8 +235,8 @@ struct LossArgs {
   int64_t M, V, K;
   Rows r;
   const int64_t* target;  // few rows: of the rows themselves
-  float2* part;           // [rows][blocks]: maximum, sum
-  int64_t blocks;         // pairs per row
+  float2* part;           // [rows][blocks]: maximum, sum of a wave's TP columns
+  int64_t blocks;         // room for the pairs of a row
   float* at;              // logit of each row's target
 };
 
@@ -291,81 +307,119 @@ __device__ __forceinline__ void reduce_logits(const LossArgs& a, int64_t rows, i
   }
 }
 
-// Forward.  FEW: one tile per workgroup, bound by the stream of w; otherwise
-// every workgroup takes its share of the tiles.
+// Rows of a last q-tile of at most 128 rows, which runs as half tiles; 0: there
+// is none.
+__device__ __forceinline__ uint32_t half_rows(int64_t rows) {
+  const uint32_t rem = (uint32_t)(rows % LogitsCfg::BQ);
+  return rem <= LogitsHalf::BQ ? rem : 0;
+}
+
+// The product of logits behind both directions: done(C{}, p0, q0, acc) takes the
+// tiles that hold rows [0, rows).  Small tiles: one per workgroup.  Large
+// tiles: every workgroup takes its share, then its share of the half tiles, the
+// workgroups left out of the last round of large ones first.
+template <class C, class F>
+__device__ __forceinline__ void logits_tiles(const uint16_t* x, int64_t ldx, int64_t rows,
+                                             const uint16_t* w, int64_t ldw, int64_t V, int64_t K,
+                                             uint32_t QT, uint8_t* const (&stages)[4], F&& done) {
+  const uint32_t PT = (uint32_t)((V + C::BP - 1) / C::BP);
+  auto job = [&](auto c, int64_t p0, int64_t q0) {
+    using T = decltype(c);
+    return gemm16::Job{{w + p0 * ldw, ld2(ldw), (int)(V - p0 < T::BP ? V - p0 : T::BP), 0},
+                       {x + q0 * ldx, ld2(ldx), (int)(rows - q0 < T::BQ ? rows - q0 : T::BQ), 0},
+                       (int)(K / kStep)};
+  };
+  if constexpr (C::STAGES > 2) {
+    if (blockIdx.x >= PT * QT) return;  // whole workgroup
+    const TileAt t = raster(in_rounds(blockIdx.x, PT * QT), PT, QT);
+    const int64_t p0 = (int64_t)t.p * C::BP;
+    int64_t q0 = (int64_t)t.q * C::BQ;
+    // a tile past the last row (whose outputs are padding) reads the last one
+    const gemm16::Job j = job(C{}, p0, q0 < rows ? q0 : rows - 1);
+    gemm16::Acc<C> acc;
+    gemm16::clear<C>(acc);
+    gemm16::product_deep<C>(j.p, j.q, j.steps, stages, acc);
+    done(C{}, p0, q0, acc);
+  } else {
+    const uint32_t w0 = blockIdx.x, G = gridDim.x;
+    auto run = [&](auto c, uint32_t id, uint32_t qt, int64_t first_q) {
+      using T = decltype(c);
+      const uint32_t n = PT * qt;
+      auto at = [&](int i) { return raster(in_rounds(id + (uint32_t)i * G, n), PT, qt); };
+      gemm16::run_tiles<T>(
+          share(n, id, G), stages,
+          [&](int i) {
+            const TileAt t = at(i);
+            return job(c, (int64_t)t.p * T::BP, first_q + (int64_t)t.q * T::BQ);
+          },
+          [&](int i, gemm16::Acc<T>& acc) {
+            const TileAt t = at(i);
+            done(c, (int64_t)t.p * T::BP, first_q + (int64_t)t.q * T::BQ, acc);
+          });
+    };
+    const uint32_t half = half_rows(rows), full = half ? QT - 1 : QT;
+    run(C{}, w0, full, 0);
+    if (half) {
+      const uint32_t taken = PT * full % G;
+      run(LogitsHalf{}, w0 >= taken ? w0 - taken : w0 + G - taken, 1, rows - half);
+    }
+  }
+}
+
+// Forward.  FEW: the rows as they are, in one tile of q.
 template <class C, bool FEW>
 __global__ __launch_bounds__(C::THREADS) void xent_loss_kernel(LossArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   FP8BS_GEMM16_STAGES(C);
   const int64_t rows = FEW ? a.M : a.r.h->rows;
-  const uint32_t PT = (uint32_t)((a.V + C::BP - 1) / C::BP), QT = (uint32_t)((rows + C::BQ - 1) / C::BQ);
   const bool direct = FEW || rows == a.M;
-  const uint16_t* x = direct ? a.x : a.xc;
-  const int64_t ldx = direct ? a.ldx : a.K;
-  auto job_at = [&](int64_t p0, int64_t q0) {
-    return gemm16::Job{
-        {a.w + p0 * a.ldw, ld2(a.ldw), (int)(a.V - p0 < C::BP ? a.V - p0 : C::BP), 0},
-        {x + q0 * ldx, ld2(ldx), (int)(rows - q0 < C::BQ ? rows - q0 : C::BQ), 0},
-        (int)(a.K / kStep)};
-  };
-  if constexpr (FEW) {
-    const int64_t p0 = (int64_t)blockIdx.x * C::BP;
-    const gemm16::Job j = job_at(p0, 0);
-    gemm16::Acc<C> acc;
-    gemm16::clear<C>(acc);
-    gemm16::product_deep<C>(j.p, j.q, j.steps, stages, acc);
-    reduce_logits<C, FEW>(a, rows, p0, 0, acc);
-  } else {
-    const uint32_t T = PT * QT, w = blockIdx.x, G = gridDim.x;
-    auto at = [&](int i) { return raster(in_rounds(w + (uint32_t)i * G, T), PT, QT); };
-    gemm16::run_tiles<C>(
-        share(T, w, G), stages,
-        [&](int i) {
-          const TileAt t = at(i);
-          return job_at((int64_t)t.p * C::BP, (int64_t)t.q * C::BQ);
-        },
-        [&](int i, gemm16::Acc<C>& acc) {
-          const TileAt t = at(i);
-          reduce_logits<C, FEW>(a, rows, (int64_t)t.p * C::BP, (int64_t)t.q * C::BQ, acc);
-        });
-  }
+  logits_tiles<C>(direct ? a.x : a.xc, direct ? a.ldx : a.K, rows, a.w, a.ldw, a.V, a.K,
+                  (uint32_t)((rows + C::BQ - 1) / C::BQ), stages,
+                  [&](auto c, int64_t p0, int64_t q0, gemm16::Acc<decltype(c)>& acc) {
+                    reduce_logits<decltype(c), FEW>(a, rows, p0, q0, acc);
+                  });
 #endif
 }
 
-// One wave per (packed) row: joins its pairs.
+// (m, s) += (m2, s2); -inf - -inf: a pair without a sum adds nothing
+__device__ __forceinline__ void join_pair(float& m, float& s, float m2, float s2) {
+  const float top = fmaxf(m, m2);
+  s = (m == -INFINITY ? s : s * __builtin_amdgcn_exp2f((m - top) * kLog2e)) +
+      (m2 == -INFINITY ? s2 : s2 * __builtin_amdgcn_exp2f((m2 - top) * kLog2e));
+  m = top;
+}
+
+// Joins the pairs of a (packed) row: a wave per row, or with FEW, where the
+// rows are too few to fill the chip, a workgroup per row.  tp, tp_half: columns
+// per pair, of the rows of large tiles and of half tiles.
 template <bool FEW>
-__global__ __launch_bounds__(256) void xent_join_kernel(LossArgs a, int64_t ignore, float* loss,
-                                                        float* lse) {
-  const int64_t q = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
+__global__ __launch_bounds__(256) void xent_join_kernel(LossArgs a, int tp, int tp_half,
+                                                        int64_t ignore, float* loss, float* lse) {
+  __shared__ float2 part[4];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t q = FEW ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + wave;
   const int64_t rows = FEW ? a.M : a.r.h->rows;
   if (q >= rows) return;
+  const int w = q < rows - (int64_t)half_rows(rows) ? tp : tp_half;
+  const int64_t blocks = (a.V + w - 1) / w;
   const float2* p = a.part + q * a.blocks;
   float m = -INFINITY, s = 0.0f;
-  for (int64_t b = lane; b < a.blocks; b += 64) {
-    const float2 v = p[b];
-    const float top = fmaxf(m, v.x);
-    // -inf - -inf: a pair without a sum adds nothing
-    s = (m == -INFINITY ? 0.0f : s * __builtin_amdgcn_exp2f((m - top) * kLog2e)) +
-        (v.x == -INFINITY ? v.y : v.y * __builtin_amdgcn_exp2f((v.x - top) * kLog2e));
-    m = top;
-  }
+  for (int64_t b = FEW ? threadIdx.x : lane; b < blocks; b += FEW ? 256 : 64)
+    join_pair(m, s, p[b].x, p[b].y);
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const float m2 = __shfl_xor(m, d, 64), s2 = __shfl_xor(s, d, 64);
-    const float top = fmaxf(m, m2);
-    s = (m == -INFINITY ? s : s * __builtin_amdgcn_exp2f((m - top) * kLog2e)) +
-        (m2 == -INFINITY ? s2 : s2 * __builtin_amdgcn_exp2f((m2 - top) * kLog2e));
-    m = top;
-  }
-  if (lane != 0) return;
+  for (int d = 1; d < 64; d <<= 1) join_pair(m, s, __shfl_xor(m, d, 64), __shfl_xor(s, d, 64));
   if constexpr (FEW) {
+    if (lane == 0) part[wave] = make_float2(m, s);
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int k = 1; k < 4; ++k) join_pair(m, s, part[k].x, part[k].y);
     const int64_t t = a.target[q];
     if (t == ignore || t < 0 || t >= a.V) {
       loss[q] = lse[q] = 0.0f;
       return;
     }
   }
+  if (lane != 0) return;
   const float l = m + logf(s);
   const int64_t row = FEW ? q : (int64_t)a.r.index[q];
   lse[row] = l;
@@ -383,8 +437,8 @@ struct GradArgs {
   uint16_t* g;      // [rows, whole tiles][ldg] of the piece
   int64_t ldg;      // columns of a piece, a multiple of 256
   int64_t v0, nv;   // the piece's vocabulary [v0, v0 + nv)
-  float* dxp;       // FP32 parts of dx, [splits][M][K]
-  int64_t splits;
+  float* dxp;       // FP32 parts of dx, [splits][rows][K], at most dx_rows rows in all
+  int64_t dx_rows;
   uint16_t* dw;
   int64_t lddw;
 };
@@ -401,7 +455,7 @@ __device__ __forceinline__ void store_g(const GradArgs& a, int64_t rows, int64_t
   const int64_t left = a.nv - pw;  // columns from pw on (<= 0: none)
   const int pl = gemm16::p_lane<C>(g);
   const int n = (left < C::TP ? (int)left : C::TP) - pl;  // the lane's first column past them
-  static_assert(C::NI == 4, "runs of 16 columns per lane");
+  static_assert(C::NI % 2 == 0, "runs of 8 or 16 columns per lane");
 #pragma unroll
   for (int j = 0; j < C::FQ; ++j) {
     const int64_t q = q0 + wq * C::TQ + 16 * j + l16;
@@ -412,14 +466,14 @@ __device__ __forceinline__ void store_g(const GradArgs& a, int64_t rows, int64_t
     const int last = real ? n : -C::TP;  // a row past the last: zeros
     uint16_t* dst = a.g + q * a.ldg + pw + pl;
 #pragma unroll
-    for (int i4 = 0; i4 < C::FP; i4 += 4) {
-      uint32_t o[8];
+    for (int i0 = 0; i0 < C::FP; i0 += 2) {
+      uint32_t o[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < 4; ++e) {
         float f[2];
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-          const int i = i4 + e / 2, r = 2 * (e & 1) + z;
+          const int i = i0 + e / 2, r = 2 * (e & 1) + z;
           const int p = gemm16::p_tile<C>(i) + r;
           float v = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, b));
           v = t == p ? v - 1.0f : v;
@@ -427,40 +481,27 @@ __device__ __forceinline__ void store_g(const GradArgs& a, int64_t rows, int64_t
         }
         o[e] = bf16x2_rne(f[0], f[1]);
       }
-      uint16_t* d = dst + gemm16::p_tile<C>(i4);
-      *reinterpret_cast<u32x4*>(d) = u32x4{o[0], o[1], o[2], o[3]};
-      *reinterpret_cast<u32x4*>(d + 8) = u32x4{o[4], o[5], o[6], o[7]};
+      *reinterpret_cast<u32x4*>(dst + gemm16::p_tile<C>(i0)) = u32x4{o[0], o[1], o[2], o[3]};
     }
     __builtin_amdgcn_sched_barrier(0);  // one j at a time: few registers beside the sums
   }
 }
 
-// Backward, first launch of a piece: logits rebuilt, G stored.
+// Backward, first launch of a piece: logits rebuilt, G stored, with zeros in
+// rows up to a multiple of kPad (dw's last k-steps).
 template <class C>
 __global__ __launch_bounds__(C::THREADS) void xent_grad_logits_kernel(GradArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   FP8BS_GEMM16_STAGES(C);
   const int64_t rows = a.r.h->rows;
-  const uint32_t PT = (uint32_t)((a.nv + C::BP - 1) / C::BP), QT = (uint32_t)((rows + C::BQ - 1) / C::BQ);
-  const uint16_t* x = rows == a.M ? a.x : a.xc;
-  const int64_t ldx = rows == a.M ? a.ldx : a.K;
-  const uint32_t T = PT * QT, w = blockIdx.x, G = gridDim.x;
-  auto at = [&](int i) { return raster(in_rounds(w + (uint32_t)i * G, T), PT, QT); };
-  gemm16::run_tiles<C>(
-      share(T, w, G), stages,
-      [&](int i) {
-        const TileAt t = at(i);
-        const int64_t p0 = (int64_t)t.p * C::BP, q0 = (int64_t)t.q * C::BQ;
-        return gemm16::Job{{a.w + (a.v0 + p0) * a.ldw, ld2(a.ldw),
-                            (int)(a.nv - p0 < C::BP ? a.nv - p0 : C::BP), 0},
-                           {x + q0 * ldx, ld2(ldx),
-                            (int)(rows - q0 < C::BQ ? rows - q0 : C::BQ), 0},
-                           (int)(a.K / kStep)};
-      },
-      [&](int i, const gemm16::Acc<C>& acc) {
-        const TileAt t = at(i);
-        store_g<C>(a, rows, (int64_t)t.p * C::BP, (int64_t)t.q * C::BQ, acc);
-      });
+  static_assert(kPad % C::BQ == 0 || C::BQ % kPad == 0, "whole tiles of padded rows");
+  static_assert(LogitsHalf::BQ % kPad == 0, "whole tiles of padded rows");
+  const int64_t padded = (rows + kPad - 1) / kPad * kPad;
+  logits_tiles<C>(rows == a.M ? a.x : a.xc, rows == a.M ? a.ldx : a.K, rows, a.w + a.v0 * a.ldw,
+                  a.ldw, a.nv, a.K, (uint32_t)((padded + C::BQ - 1) / C::BQ), stages,
+                  [&](auto c, int64_t p0, int64_t q0, const gemm16::Acc<decltype(c)>& acc) {
+                    store_g<decltype(c)>(a, rows, p0, q0, acc);
+                  });
 #endif
 }
 
@@ -471,7 +512,7 @@ __device__ __forceinline__ void add_dx(const GradArgs& a, int64_t rows, bool fir
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
   const int64_t pw = p0 + wave / C::WQ * C::TP;
-  float* out = a.dxp + split * a.M * a.K;
+  float* out = a.dxp + split * rows * a.K;
   if (pw >= a.K) return;  // K is a multiple of 128: a wave's columns exist or do not
 #pragma unroll
   for (int j = 0; j < C::FQ; ++j) {
@@ -507,14 +548,25 @@ __device__ __forceinline__ void store_dw(const GradArgs& a, int64_t p0, int64_t 
   }
 }
 
+// Parts that the contraction of dx over a whole piece is cut into: until a
+// tile's steps are at most half of a workgroup's share of the launch, as far
+// as the room for the parts goes.  kTileSteps: a tile's start and end in steps.
+constexpr uint32_t kTileSteps = 3;
+__device__ __forceinline__ uint32_t dx_splits(const GradArgs& a, int64_t rows, uint32_t tiles_x,
+                                              uint32_t tiles_w, uint32_t G) {
+  const uint32_t sx = (uint32_t)(a.ldg / kStep), sw = (uint32_t)(rows / kStep) + kTileSteps;
+  const uint64_t all = (uint64_t)tiles_x * sx + (uint64_t)tiles_w * sw;
+  uint32_t s = 1;
+  while (s < 32 && sx / s > 8 && 2ull * G * (sx / s) > all && 2 * s * rows <= a.dx_rows) s *= 2;
+  return s;
+}
+
 // Backward, second launch of a piece: tiles of its part of dx, then of its
 // dw.  The dx tiles, long, go round the workgroups; those left out of the last
 // round of them take dw tiles worth a dx tile's steps meanwhile; the other dw
-// tiles go round all workgroups.  kTileSteps: a tile's start and end in steps.
-constexpr uint32_t kTileSteps = 3;
-
+// tiles go round all workgroups.
 template <class CX, class CW>
-__global__ __launch_bounds__(CX::THREADS) void xent_grad_kernel(GradArgs a, int first) {
+__global__ __launch_bounds__(CX::THREADS, 2) void xent_grad_kernel(GradArgs a, int first) {
 #if defined(__HIP_DEVICE_COMPILE__)
   static_assert(CX::STAGE_BYTES == CW::STAGE_BYTES && CX::STAGES == CW::STAGES &&
                     CX::THREADS == CW::THREADS, "one workgroup shape");
@@ -524,7 +576,9 @@ __global__ __launch_bounds__(CX::THREADS) void xent_grad_kernel(GradArgs a, int 
   const uint32_t PT = (uint32_t)((a.K + CX::BP - 1) / CX::BP), QX = (uint32_t)((rows + CX::BQ - 1) / CX::BQ);
   // k-steps in pairs; G is zero past the vocabulary, up to whole tiles
   const uint32_t pairs = (uint32_t)((a.nv + 2 * kStep - 1) / (2 * kStep));
-  const uint32_t splits = (uint32_t)a.splits < pairs ? (uint32_t)a.splits : pairs;
+  // by the full piece, the same for all: a shorter last piece may use fewer
+  const uint32_t whole = dx_splits(a, rows, PT * QX, PT * (uint32_t)(a.ldg / CW::BQ), G);
+  const uint32_t splits = whole < pairs ? whole : pairs;
   const uint32_t NX = PT * QX * splits;
   {
     using C = CX;
@@ -596,25 +650,27 @@ __global__ __launch_bounds__(CX::THREADS) void xent_grad_kernel(GradArgs a, int 
 #endif
 }
 
-// One wave per row of x: adds up its parts of dx (zeros for a row without a
-// loss).
-__global__ __launch_bounds__(256) void xent_dx_kernel(GradArgs a, uint16_t* dx, int64_t lddx) {
-  const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (m >= a.M) return;
-  const int64_t q = a.r.place[m];
-  const float d = q >= 0 ? a.r.dloss[q] : 0.0f;
-  for (int64_t k = lane * 4; k < a.K; k += 256) {
-    u32x2 o = {0u, 0u};
-    if (q >= 0) {
-      v4f s = *reinterpret_cast<const v4f*>(a.dxp + q * a.K + k);
-      for (int64_t z = 1; z < a.splits; ++z)
-        s += *reinterpret_cast<const v4f*>(a.dxp + (z * a.M + q) * a.K + k);
-      s = s * d;
-      o = u32x2{bf16x2_rne(s[0], s[1]), bf16x2_rne(s[2], s[3])};
-    }
-    *reinterpret_cast<u32x2*>(dx + m * lddx + k) = o;
+// dx: adds up its parts (zeros for a row without a loss), 4 columns per thread.
+template <class CX, class CW>
+__global__ __launch_bounds__(256) void xent_dx_kernel(GradArgs a, uint32_t G, uint32_t chunks,
+                                                      uint16_t* dx, int64_t lddx) {
+  const int64_t m = blockIdx.x / chunks;
+  const int64_t k = (int64_t)(blockIdx.x % chunks) * 1024 + threadIdx.x * 4;
+  if (k >= a.K) return;
+  const int64_t q = a.r.place[m], rows = a.r.h->rows;
+  u32x2 o = {0u, 0u};
+  if (q >= 0) {
+    const uint32_t PT = (uint32_t)((a.K + CX::BP - 1) / CX::BP);
+    const uint32_t QX = (uint32_t)((rows + CX::BQ - 1) / CX::BQ);
+    const uint32_t splits = dx_splits(a, rows, PT * QX, PT * (uint32_t)(a.ldg / CW::BQ), G);
+    v4f s = *reinterpret_cast<const v4f*>(a.dxp + q * a.K + k);
+#pragma unroll 4
+    for (uint32_t z = 1; z < splits; ++z)
+      s += *reinterpret_cast<const v4f*>(a.dxp + (z * rows + q) * a.K + k);
+    s = s * a.r.dloss[q];
+    o = u32x2{bf16x2_rne(s[0], s[1]), bf16x2_rne(s[2], s[3])};
   }
+  *reinterpret_cast<u32x2*>(dx + m * lddx + k) = o;
 }
 
 // Workspace, in order; every part starts at a multiple of 256 bytes.
@@ -648,6 +704,7 @@ struct LossPlan {
   float2* part;
   int64_t blocks;
   float* at;
+  bool small;
   size_t bytes;
 };
 
@@ -655,7 +712,9 @@ LossPlan loss_plan(void* ws, int64_t M, int64_t V, int64_t K) {
   Carver c{static_cast<uint8_t*>(ws)};
   LossPlan p{};
   const bool few = M <= kFewXentRows;
-  p.blocks = few ? cdiv(V, LogitsFewCfg::TP) : cdiv(V, LogitsCfg::TP);
+  p.small = few || small_logits(M, V);
+  // half tiles have narrower waves than large ones
+  p.blocks = p.small ? cdiv(V, LogitsSmall::TP) : cdiv(V, LogitsHalf::TP);
   p.part = c.take<float2>(M * p.blocks);
   p.at = c.take<float>(M);
   if (!few) {
@@ -676,7 +735,8 @@ struct GradPlan {
   uint16_t *xc, *xs, *g;
   int64_t ldg, pieces;
   float* dxp;
-  int64_t splits;
+  int64_t dx_rows;
+  bool small_logits, small;
   size_t bytes;
 };
 
@@ -689,18 +749,18 @@ GradPlan grad_plan(void* ws, int64_t M, int64_t V, int64_t K) {
   p.pieces = cdiv(V, most);
   p.ldg = cdiv(cdiv(V, p.pieces), kTile) * kTile;
   p.pieces = cdiv(V, p.ldg);
-  // dx's tiles contract over the whole piece: cut that axis until a tile takes
-  // at most half of a compute unit's share of the launch
-  const int64_t tx = cdiv(M, kTile) * cdiv(K, kTile), sx = p.ldg / kStep;
-  const int64_t tw = p.ldg / kTile * cdiv(K, kTile), sw = cdiv(M, kStep) + 4;
-  p.splits = 1;
-  while (p.splits < 32 && sx / p.splits > 8 && 2 * 256 * (sx / p.splits) > tx * sx + tw * sw)
-    p.splits *= 2;
+  p.small_logits = small_logits(M, p.ldg);
+  // too few large tiles of dw to go round: small ones
+  p.small = p.ldg / kTile * cdiv(K, kTile) < 192;
+  // room for the parts of dx (see dx_splits): 32 for few rows, then as many as
+  // keep it at 8192 rows
+  const int64_t parts = 32 * M < 8192 ? 32 * M : 8192;
+  p.dx_rows = M > parts ? M : parts;
   p.r = take_rows(c, M, true);
   p.xc = c.take<uint16_t>(cdiv(M, kPad) * kPad * K);
   p.xs = c.take<uint16_t>(cdiv(M, kPad) * kPad * K);
   p.g = c.take<uint16_t>(Mt * p.ldg);
-  p.dxp = c.take<float>(p.splits * M * K);
+  p.dxp = c.take<float>(p.dx_rows * K);
   p.bytes = c.used;
   return p;
 }
@@ -717,18 +777,17 @@ hipError_t launch_xent(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_
                        int64_t V, int64_t K, void* workspace, hipStream_t stream) {
   const LossPlan p = loss_plan(workspace, M, V, K);
   const LossArgs a{x, ldx, p.xc, w, ldw, M, V, K, p.r, target, p.part, p.blocks, p.at};
+  const dim3 block(LogitsSmall::THREADS), large(LogitsCfg::THREADS);
+  const int64_t tiles = p.small ? cdiv(V, LogitsSmall::BP) * cdiv(M, LogitsSmall::BQ)
+                                : cdiv(V, LogitsCfg::BP) * cdiv(M, LogitsCfg::BQ);
+  if (tiles > kMaxTiles) return hipErrorInvalidConfiguration;
   hipError_t e;
   if (M <= kFewXentRows) {
-    using C = LogitsFewCfg;
-    e = launch_kernel(xent_loss_kernel<C, true>, dim3((unsigned)cdiv(V, C::BP)), dim3(C::THREADS),
-                      stream, a);
+    e = launch_kernel(xent_loss_kernel<LogitsSmall, true>, dim3((unsigned)tiles), block, stream, a);
     if (e != hipSuccess) return e;
-    return launch_kernel(xent_join_kernel<true>, dim3((unsigned)cdiv(M, 4)), dim3(256), stream, a,
-                         ignore, loss, lse);
+    return launch_kernel(xent_join_kernel<true>, dim3((unsigned)M), dim3(256), stream, a,
+                         LogitsSmall::TP, LogitsSmall::TP, ignore, loss, lse);
   }
-  using C = LogitsCfg;
-  const int64_t tiles = cdiv(V, C::BP) * cdiv(M, C::BQ);
-  if (tiles > kMaxTiles) return hipErrorInvalidConfiguration;
   e = launch_kernel(xent_rows_kernel, dim3(1), dim3(1024), stream, target, M, V, ignore, p.r,
                     static_cast<const float*>(nullptr), static_cast<const float*>(nullptr), loss,
                     lse);
@@ -736,11 +795,52 @@ hipError_t launch_xent(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_
   e = launch_kernel(xent_pack_kernel, dim3((unsigned)cdiv(cdiv(M, kPad) * kPad, 4)), dim3(256),
                     stream, x, ldx, M, K, p.r, p.xc, static_cast<uint16_t*>(nullptr));
   if (e != hipSuccess) return e;
-  e = launch_kernel(xent_loss_kernel<C, false>, tile_grid(tiles), dim3(C::THREADS), stream, a);
+  e = p.small ? launch_kernel(xent_loss_kernel<LogitsSmall, false>, dim3((unsigned)tiles), block,
+                              stream, a)
+              : launch_kernel(xent_loss_kernel<LogitsCfg, false>, tile_grid(tiles), large, stream,
+                              a);
   if (e != hipSuccess) return e;
   return launch_kernel(xent_join_kernel<false>, dim3((unsigned)cdiv(M, 4)), dim3(256), stream, a,
-                       ignore, loss, lse);
+                       p.small ? LogitsSmall::TP : LogitsCfg::TP,
+                       p.small ? LogitsSmall::TP : LogitsHalf::TP, ignore, loss, lse);
 }
+
+namespace {
+
+template <class CX, class CW>
+hipError_t launch_pieces(const GradPlan& p, GradArgs a, int per_cu, uint16_t* dx, int64_t lddx,
+                         hipStream_t stream) {
+  using CL = LogitsCfg;
+  using CS = LogitsSmall;
+  const int64_t QL = cdiv(a.M, CL::BQ), QS = cdiv(a.M, kPad) * (kPad / CS::BQ);
+  const int64_t tl = p.small_logits ? QS * (p.ldg / CS::BP) : QL * (p.ldg / CL::BP);
+  const int64_t KT = cdiv(a.K, CX::BP), chunks = cdiv(a.K, 1024);
+  // dx may be cut into 32 parts
+  const int64_t most = KT * (cdiv(a.M, CX::BQ) * 32 + p.ldg / CW::BQ);
+  if (tl > kMaxTiles || most > kMaxTiles || a.M * chunks > kMaxTiles)
+    return hipErrorInvalidConfiguration;
+  const dim3 grid = tile_grid(most, per_cu);
+  for (int64_t i = 0; i < p.pieces; ++i) {
+    const int64_t left = a.V - i * p.ldg;
+    a.v0 = i * p.ldg;
+    a.nv = left < p.ldg ? left : p.ldg;
+    hipError_t e = hipSuccess;
+    if (a.M > 0)
+      e = p.small_logits ? launch_kernel(xent_grad_logits_kernel<CS>, dim3((unsigned)tl),
+                                         dim3(CS::THREADS), stream, a)
+                         : launch_kernel(xent_grad_logits_kernel<CL>, tile_grid(tl),
+                                         dim3(CL::THREADS), stream, a);
+    if (e != hipSuccess) return e;
+    e = launch_kernel(xent_grad_kernel<CX, CW>, grid, dim3(CX::THREADS), stream, a,
+                      i == 0 ? 1 : 0);
+    if (e != hipSuccess) return e;
+  }
+  if (a.M == 0) return hipSuccess;
+  return launch_kernel(xent_dx_kernel<CX, CW>, dim3((unsigned)(a.M * chunks)), dim3(256), stream, a,
+                       grid.x, (uint32_t)chunks, dx, lddx);
+}
+
+}  // namespace
 
 hipError_t launch_xent_backward(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw,
                                 const int64_t* target, int64_t ignore, const float* lse,
@@ -748,10 +848,8 @@ hipError_t launch_xent_backward(const uint16_t* x, int64_t ldx, const uint16_t* 
                                 int64_t lddw, int64_t M, int64_t V, int64_t K, void* workspace,
                                 hipStream_t stream) {
   const GradPlan p = grad_plan(workspace, M, V, K);
-  GradArgs a{x, ldx, p.xc, p.xs, w, ldw, M, V, K, p.r, p.g, p.ldg, 0, 0, p.dxp, p.splits, dw, lddw};
-  const int64_t MT = cdiv(M, kTile), KT = cdiv(K, kTile);
-  const int64_t t1 = MT * (p.ldg / kTile), t2 = KT * (MT * p.splits + p.ldg / kTile);
-  if (t1 > kMaxTiles || t2 > kMaxTiles) return hipErrorInvalidConfiguration;
+  const GradArgs a{x,   ldx, p.xc, p.xs,  w, ldw, M,     V,         K,
+                   p.r, p.g, p.ldg, 0,    0, p.dxp, p.dx_rows, dw, lddw};
   hipError_t e = launch_kernel(xent_rows_kernel, dim3(1), dim3(1024), stream, target, M, V, ignore,
                                p.r, lse, dloss, static_cast<float*>(nullptr),
                                static_cast<float*>(nullptr));
@@ -761,20 +859,8 @@ hipError_t launch_xent_backward(const uint16_t* x, int64_t ldx, const uint16_t* 
                       stream, x, ldx, M, K, p.r, p.xc, p.xs);
     if (e != hipSuccess) return e;
   }
-  for (int64_t i = 0; i < p.pieces; ++i) {
-    a.v0 = i * p.ldg;
-    a.nv = V - a.v0 < p.ldg ? V - a.v0 : p.ldg;
-    if (M > 0) {
-      e = launch_kernel(xent_grad_logits_kernel<LogitsCfg>, tile_grid(t1),
-                        dim3(LogitsCfg::THREADS), stream, a);
-      if (e != hipSuccess) return e;
-    }
-    e = launch_kernel(xent_grad_kernel<DxCfg, DwCfg>, tile_grid(t2), dim3(DxCfg::THREADS),
-                      stream, a, i == 0 ? 1 : 0);
-    if (e != hipSuccess) return e;
-  }
-  if (M == 0) return hipSuccess;
-  return launch_kernel(xent_dx_kernel, dim3((unsigned)cdiv(M, 4)), dim3(256), stream, a, dx, lddx);
+  return p.small ? launch_pieces<DxSmall, DwSmall>(p, a, 2, dx, lddx, stream)
+                 : launch_pieces<DxCfg, DwCfg>(p, a, 1, dx, lddx, stream);
 }
 
 }  // namespace fp8bs
