@@ -307,11 +307,24 @@ __device__ __forceinline__ void reduce_logits(const LossArgs& a, int64_t rows, i
   }
 }
 
-// Rows of a last q-tile of at most 128 rows, which runs as half tiles; 0: there
-// is none.
-__device__ __forceinline__ uint32_t half_rows(int64_t rows) {
+// Rows of a last q-tile of at most 128 rows that runs as half tiles; 0: there
+// is none.  Half tiles go over w a second time, so they are taken only where w
+// stays in the last-level cache between (kCachedBytes), and only where the
+// rounds of workgroups come out shorter, a round of half tiles taking 3/4 of one
+// of large tiles (they do not halve a k-step's latency).  Measured: 613 x
+// 32003 x 2048, 2 rounds against 1.75: 106 and 95 us; 300 x 129280 x 7168,
+// read twice from HBM: 755 and 841 us.
+constexpr int64_t kCachedBytes = int64_t(192) << 20;
+__device__ __forceinline__ uint32_t half_rows(int64_t rows, int64_t V, int64_t K, uint32_t G) {
   const uint32_t rem = (uint32_t)(rows % LogitsCfg::BQ);
-  return rem <= LogitsHalf::BQ ? rem : 0;
+  if (rem == 0 || rem > LogitsHalf::BQ || 2 * V * K > kCachedBytes) return 0;
+  const uint32_t PT = (uint32_t)((V + LogitsCfg::BP - 1) / LogitsCfg::BP);
+  const uint32_t full = PT * (uint32_t)(rows / LogitsCfg::BQ), idle = full % G ? G - full % G : 0;
+  const uint32_t plain = 4 * ((full + PT + G - 1) / G);
+  const uint32_t over = PT > idle ? PT - idle : 0;
+  const uint32_t halved = full ? 4 * ((full + G - 1) / G) + 3 * ((over + G - 1) / G)
+                               : 3 * ((PT + G - 1) / G);
+  return halved < plain ? rem : 0;
 }
 
 // The product of logits behind both directions: done(C{}, p0, q0, acc) takes the
@@ -357,7 +370,7 @@ __device__ __forceinline__ void logits_tiles(const uint16_t* x, int64_t ldx, int
             done(c, (int64_t)t.p * T::BP, first_q + (int64_t)t.q * T::BQ, acc);
           });
     };
-    const uint32_t half = half_rows(rows), full = half ? QT - 1 : QT;
+    const uint32_t half = half_rows(rows, V, K, G), full = half ? QT - 1 : QT;
     run(C{}, w0, full, 0);
     if (half) {
       const uint32_t taken = PT * full % G;
@@ -390,17 +403,20 @@ __device__ __forceinline__ void join_pair(float& m, float& s, float m2, float s2
 }
 
 // Joins the pairs of a (packed) row: a wave per row, or with FEW, where the
-// rows are too few to fill the chip, a workgroup per row.  tp, tp_half: columns
-// per pair, of the rows of large tiles and of half tiles.
+// rows are too few to fill the chip, a workgroup per row.  G: workgroups of the
+// product; tp, tp_half: columns per pair, of its large (or small) tiles and of
+// its half tiles.
 template <bool FEW>
-__global__ __launch_bounds__(256) void xent_join_kernel(LossArgs a, int tp, int tp_half,
-                                                        int64_t ignore, float* loss, float* lse) {
+__global__ __launch_bounds__(256) void xent_join_kernel(LossArgs a, uint32_t G, int tp,
+                                                        int tp_half, int64_t ignore, float* loss,
+                                                        float* lse) {
   __shared__ float2 part[4];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t q = FEW ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + wave;
   const int64_t rows = FEW ? a.M : a.r.h->rows;
   if (q >= rows) return;
-  const int w = q < rows - (int64_t)half_rows(rows) ? tp : tp_half;
+  int w = tp;
+  if (tp != tp_half && q >= rows - (int64_t)half_rows(rows, a.V, a.K, G)) w = tp_half;
   const int64_t blocks = (a.V + w - 1) / w;
   const float2* p = a.part + q * a.blocks;
   float m = -INFINITY, s = 0.0f;
@@ -785,7 +801,7 @@ hipError_t launch_xent(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_
   if (M <= kFewXentRows) {
     e = launch_kernel(xent_loss_kernel<LogitsSmall, true>, dim3((unsigned)tiles), block, stream, a);
     if (e != hipSuccess) return e;
-    return launch_kernel(xent_join_kernel<true>, dim3((unsigned)M), dim3(256), stream, a,
+    return launch_kernel(xent_join_kernel<true>, dim3((unsigned)M), dim3(256), stream, a, 0u,
                          LogitsSmall::TP, LogitsSmall::TP, ignore, loss, lse);
   }
   e = launch_kernel(xent_rows_kernel, dim3(1), dim3(1024), stream, target, M, V, ignore, p.r,
@@ -801,7 +817,7 @@ hipError_t launch_xent(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_
                               a);
   if (e != hipSuccess) return e;
   return launch_kernel(xent_join_kernel<false>, dim3((unsigned)cdiv(M, 4)), dim3(256), stream, a,
-                       p.small ? LogitsSmall::TP : LogitsCfg::TP,
+                       tile_grid(tiles).x, p.small ? LogitsSmall::TP : LogitsCfg::TP,
                        p.small ? LogitsSmall::TP : LogitsHalf::TP, ignore, loss, lse);
 }
 
