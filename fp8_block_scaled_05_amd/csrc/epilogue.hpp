@@ -35,8 +35,11 @@ __device__ __forceinline__ float activate(float z) {
   } else if constexpr (ACT == kActSilu) {
     return z * sigmoid_fast(z);
   } else if constexpr (ACT == kActGelu) {
+    // e^(-2 u) = 2^(c (k1 + k1 a c^2))
+    constexpr float k1 = -2.0f * kGeluC * kLog2e, k3 = k1 * kGeluA;
     const float c = __builtin_amdgcn_fmed3f(z, -kGeluTop, kGeluTop);
-    return z * sigmoid_fast(2.0f * kGeluC * c * __builtin_fmaf(kGeluA * c, c, 1.0f));
+    const float e = __builtin_amdgcn_exp2f(c * __builtin_fmaf(c * c, k3, k1));
+    return z * __builtin_amdgcn_rcpf(1.0f + e);
   } else {
     return z;
   }

@@ -13,21 +13,63 @@ namespace fp8bs {
 namespace {
 
 struct LinearEpilogue {
+  static constexpr bool kStream = true;
   Epilogue e;
 
-  // Lane (g, l) holds rows 16 i + 4 g + r and FN consecutive columns (see
-  // gemm::store_tile).
+  // Bias and residual of a lane's outputs, rows 16 i + 4 g + r and FN
+  // consecutive columns (see gemm::store_tile).  Tiles with registers to spare
+  // (kEarly) load them before the K loop, which hides their latency: 333 x 2050 x
+  // 2048 with all parts 17.8 against 15.5 us.  Larger tiles load them after it.
+  template <class C>
+  struct Early {
+    static constexpr bool kEarly = C::FM * C::FN <= 8;
+    float bias[kEarly ? C::FN : 1];
+    uint16_t res[kEarly ? C::FM : 1][kEarly ? 4 : 1][kEarly ? C::FN : 1];
+  };
+
+  template <class C>
+  __device__ __forceinline__ void load_bias(const GemmArgs& p, int64_t col, float* bias) const {
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) bias[j] = e.bias[col + j < p.N ? col + j : p.N - 1];
+  }
+
+  template <class C>
+  __device__ __forceinline__ void load(const GemmArgs& p, const gemm::TileCoords& t, int wm,
+                                       int wn, int lane, Early<C>& early) const {
+    if constexpr (Early<C>::kEarly) {
+      const int64_t col = t.col0 + wn * C::TN + C::FN * (lane & 15);
+      const int64_t row0 = t.row0 + wm * C::TM + 4 * (lane >> 4);
+      if (e.bias) load_bias<C>(p, col, early.bias);
+      if (e.residual) {
+        // rows and columns past the end repeat the last: loaded, never stored
+        const int64_t last = t.row_end - 1;
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int64_t row = row0 + 16 * i + r;
+            const uint16_t* src = e.residual + (row < last ? row : last) * e.ldr;
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j)
+              early.res[i][r][j] = src[col + j < p.N ? col + j : p.N - 1];
+          }
+      }
+    }
+  }
+
   template <class C>
   __device__ __forceinline__ void apply(const GemmArgs& p, const gemm::TileCoords& t,
-                                        v4f (&acc)[C::FM][C::FN], int wm, int wn,
-                                        int lane) const {
-    const int g4 = lane >> 4, l16 = lane & 15;
-    const int64_t col = t.col0 + wn * C::TN + C::FN * l16;
-    const int64_t wrow0 = t.row0 + wm * C::TM;
+                                        v4f (&acc)[C::FM][C::FN], int wm, int wn, int lane,
+                                        const Early<C>& early) const {
+    constexpr bool EARLY = Early<C>::kEarly;
+    const int64_t col = t.col0 + wn * C::TN + C::FN * (lane & 15);
+    const int64_t row0 = t.row0 + wm * C::TM + 4 * (lane >> 4);
     if (e.bias) {
+      float late[C::FN];
+      if constexpr (!EARLY) load_bias<C>(p, col, late);
 #pragma unroll
       for (int j = 0; j < C::FN; ++j) {
-        const float b = col + j < p.N ? e.bias[col + j] : 0.0f;
+        const float b = EARLY ? early.bias[EARLY ? j : 0] : late[j];
 #pragma unroll
         for (int i = 0; i < C::FM; ++i)
 #pragma unroll
@@ -39,44 +81,75 @@ struct LinearEpilogue {
       pz.ldc = e.ldz;
       gemm::TileCoords tz = t;
       tz.c = e.z;
-      gemm::store_tile<C, kOutBF16>(pz, tz, acc, wm, wn, lane);
+      gemm::store_tile<C, kOutBF16, true>(pz, tz, acc, wm, wn, lane);
     }
     with_activation(e.act, [&](auto act) {
 #pragma unroll
-      for (int i = 0; i < C::FM; ++i)
+      for (int i = 0; i < C::FM; ++i) {
 #pragma unroll
         for (int j = 0; j < C::FN; ++j)
 #pragma unroll
           for (int r = 0; r < 4; ++r) acc[i][j][r] = activate<decltype(act)::value>(acc[i][j][r]);
+        __builtin_amdgcn_sched_barrier(0);  // few temporaries beside the sums
+      }
     });
     if (e.residual) {
-      using VT = typename gemm::Vec<uint16_t, C::FN>::type;
-      const bool vec = reinterpret_cast<uintptr_t>(e.residual) % (C::FN * 2) == 0 &&
-                       e.ldr % C::FN == 0 && col + C::FN <= p.N;
+      if constexpr (EARLY) {
 #pragma unroll
-      for (int i = 0; i < C::FM; ++i)
+        for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int64_t row = wrow0 + 16 * i + 4 * g4 + r;
-          if (row >= t.row_end) continue;
-          const uint16_t* src = e.residual + row * e.ldr + col;
-          if (vec) {
-            VT v;
-            if constexpr (C::FN == 1) {
-              v[0] = *src;
-            } else {
-              v = *reinterpret_cast<const VT*>(src);
-            }
+          for (int r = 0; r < 4; ++r)
 #pragma unroll
             for (int j = 0; j < C::FN; ++j)
-              acc[i][j][r] += __uint_as_float((uint32_t)v[j] << 16);
-          } else {
-#pragma unroll
-            for (int j = 0; j < C::FN; ++j)
-              if (col + j < p.N) acc[i][j][r] += __uint_as_float((uint32_t)src[j] << 16);
-          }
-        }
+              acc[i][j][r] += __uint_as_float((uint32_t)early.res[i][r][j] << 16);
+      } else {
+        add_residual<C>(p, t, acc, row0, col, t.row0 + (wm + 1) * C::TM <= t.row_end);
+      }
     }
+  }
+
+  // acc += residual, loaded here.  row0, col: the lane's first; inside: every
+  // row of the wave exists.
+  template <class C>
+  __device__ __forceinline__ void add_residual(const GemmArgs& p, const gemm::TileCoords& t,
+                                               v4f (&acc)[C::FM][C::FN], int64_t row0, int64_t col,
+                                               bool inside) const {
+    using VT = typename gemm::Vec<uint16_t, C::FN>::type;
+    const bool vec = reinterpret_cast<uintptr_t>(e.residual) % (C::FN * 2) == 0 &&
+                     e.ldr % C::FN == 0 && col + C::FN <= p.N;
+    const uint16_t* const src = e.residual + row0 * e.ldr + col;
+    if (inside && __all(vec)) {
+      // the whole wave: the loads of HB MFMA rows in flight together
+      constexpr int HB = C::FM < 4 ? C::FM : 4;
+#pragma unroll
+      for (int i0 = 0; i0 < C::FM; i0 += HB) {
+        VT v[HB][4];
+#pragma unroll
+        for (int i = 0; i < HB; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            v[i][r] = *reinterpret_cast<const VT*>(src + (16 * (i0 + i) + r) * e.ldr);
+#pragma unroll
+        for (int i = 0; i < HB; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j)
+              acc[i0 + i][j][r] += __uint_as_float((uint32_t)v[i][r][j] << 16);
+        __builtin_amdgcn_sched_barrier(0);  // few loads beside the sums
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (row0 + 16 * i + r >= t.row_end) continue;
+        const uint16_t* at = src + (16 * i + r) * e.ldr;
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+          if (col + j < p.N) acc[i][j][r] += __uint_as_float((uint32_t)at[j] << 16);
+      }
   }
 };
 

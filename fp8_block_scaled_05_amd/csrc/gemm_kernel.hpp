@@ -601,7 +601,10 @@ struct RowVals {
 // FN l .. FN l + FN - 1 of the wave's TN columns: one store per row (vector
 // when the row start is aligned for it).  A wave whose whole sub-tile lies
 // inside C (the common case) stores without per-row tests.
-template <class C, int OUT>
+// STREAM: those stores bypass the caches' retention.  Every workgroup of a round
+// stores its tile at the same time, and with a second output the bursts are
+// larger than the L2s.
+template <class C, int OUT, bool STREAM = false>
 __device__ __forceinline__ void store_tile(const GemmArgs& p, const TileCoords& t,
                                            const v4f (&acc)[C::FM][C::FN], int wm, int wn,
                                            int lane) {
@@ -623,8 +626,15 @@ __device__ __forceinline__ void store_tile(const GemmArgs& p, const TileCoords& 
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const RowVals<C, OUT> rv(acc, i, r);
-          *reinterpret_cast<VT*>(base + (16 * i + r) * p.ldc) = rv.v;
+          VT* const dst = reinterpret_cast<VT*>(base + (16 * i + r) * p.ldc);
+          if constexpr (STREAM) {
+            __builtin_nontemporal_store(rv.v, dst);
+          } else {
+            *dst = rv.v;
+          }
         }
+        // few addresses at a time (the sums fill the registers)
+        if constexpr (STREAM) __builtin_amdgcn_sched_barrier(0);
       }
       return;
     }
@@ -730,13 +740,21 @@ __device__ __forceinline__ void store_tile_e4m3(const GemmArgs& p, const TileCoo
 
 // Epilogue of the plain product: the FP32 sums are stored as they are.
 struct NoEpilogue {
+  static constexpr bool kStream = false;  // see store_tile
+  template <class C>
+  struct Early {};
+  template <class C>
+  __device__ __forceinline__ void load(const GemmArgs&, const TileCoords&, int, int, int,
+                                       Early<C>&) const {}
   template <class C>
   __device__ __forceinline__ void apply(const GemmArgs&, const TileCoords&,
-                                        v4f (&)[C::FM][C::FN], int, int, int) const {}
+                                        v4f (&)[C::FM][C::FN], int, int, int,
+                                        const Early<C>&) const {}
 };
 
-// ep.apply<C>(p, t, acc, wm, wn, lane) may change a wave's finished sums
-// before they are stored.
+// ep.load<C>(p, t, wm, wn, lane, early) may load operands of its own before the
+// K loop; ep.apply<C>(p, t, acc, wm, wn, lane, early) may change a wave's
+// finished sums before they are stored.
 template <class C, int OUT, class E = NoEpilogue>
 __device__ __forceinline__ void block_gemm_body(const GemmArgs& p, const TileCoords& t,
                                                 const LdsSet& L, const E& ep = E()) {
@@ -750,6 +768,8 @@ __device__ __forceinline__ void block_gemm_body(const GemmArgs& p, const TileCoo
   make_plan<C>(p, t, wave, lane, lp);
   const FragOffs fo = frag_offsets<C>(wm, wn, lane);
   const Rsrc rs = make_rsrc_set<C>(p, t);
+  typename E::template Early<C> early;
+  ep.template load<C>(p, t, wm, wn, lane, early);
 
   v4f acc[C::FM][C::FN];
 #pragma unroll
@@ -855,11 +875,11 @@ __device__ __forceinline__ void block_gemm_body(const GemmArgs& p, const TileCoo
     }
   }
 
-  ep.template apply<C>(p, t, acc, wm, wn, lane);
+  ep.template apply<C>(p, t, acc, wm, wn, lane, early);
   if constexpr (OUT == kOutE4M3) {
     store_tile_e4m3<C>(p, t, acc, wm, wn, lane, L.red, L.rcp);
   } else {
-    store_tile<C, OUT>(p, t, acc, wm, wn, lane);
+    store_tile<C, OUT, E::kStream>(p, t, acc, wm, wn, lane);
   }
 }
 

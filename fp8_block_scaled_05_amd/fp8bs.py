@@ -140,7 +140,7 @@ _NO_SWITCH = contextlib.nullcontext()
 
 def _stream(t):
     if _raw_stream is not None:
-        return _raw_stream(t.device.index)
+        return _raw_stream(t.get_device())
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
@@ -157,17 +157,18 @@ def _ptr(t):
 
 
 def _need_device(*ts):
-    devices = set()
+    first = None
     for t in ts:
         if t is None:
             continue
-        d = t.device
-        if d.type != "cuda":
+        d = t.get_device()  # -1: not on a GPU
+        if d < 0 or not t.is_cuda:
             raise ValueError("libfp8bs works on GPU tensors only")
-        devices.add(d)
-    if len(devices) > 1:
-        raise ValueError("all tensors of a call must be on one GPU, got "
-                         f"{sorted(map(str, devices))}")
+        if first is None:
+            first = d
+        elif d != first:
+            raise ValueError("all tensors of a call must be on one GPU, got "
+                             f"{sorted({str(u.device) for u in ts if u is not None})}")
 
 
 def _mat(t, name, rows, cols, dtype, ld=None):
