@@ -45,21 +45,23 @@ __device__ __forceinline__ float activate(float z) {
   }
 }
 
-// The derivative, with the correctly rounded-to-an-ulp exponential: its
-// results are quantized, and an error here moves values over a code's edge.
+// The derivative, in the same arithmetic: where it matters to a quantized tile
+// (|z| of a few units) e^-x is within a few 2^-24.
 template <int ACT>
 __device__ __forceinline__ float activate_grad(float z) {
   if constexpr (ACT == kActRelu) {
     return z > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (ACT == kActSilu) {
-    const float s = __builtin_amdgcn_rcpf(1.0f + expf(-z));
+    const float s = sigmoid_fast(z);
     return __builtin_fmaf(z * s, 1.0f - s, s);
   } else if constexpr (ACT == kActGelu) {
+    constexpr float k1 = -2.0f * kGeluC * kLog2e, k3 = k1 * kGeluA;
+    constexpr float d1 = 2.0f * kGeluC, d3 = 3.0f * d1 * kGeluA;  // 2 u' = d1 + d3 z^2
     const float c = __builtin_amdgcn_fmed3f(z, -kGeluTop, kGeluTop);
-    const float u2 = 2.0f * kGeluC * c * __builtin_fmaf(kGeluA * c, c, 1.0f);
-    const float du2 = 2.0f * kGeluC * __builtin_fmaf(3.0f * kGeluA * c, c, 1.0f);
-    const float s = __builtin_amdgcn_rcpf(1.0f + expf(-u2));
-    return __builtin_fmaf(c * s * (1.0f - s), du2, s);
+    const float c2 = c * c;
+    const float e = __builtin_amdgcn_exp2f(c * __builtin_fmaf(c2, k3, k1));
+    const float s = __builtin_amdgcn_rcpf(1.0f + e);
+    return __builtin_fmaf(c * s * (1.0f - s), __builtin_fmaf(c2, d3, d1), s);
   } else {
     return 1.0f;
   }

@@ -36,6 +36,20 @@ struct BackwardArgs {
   float* part;  // [ceil(M/128)][N] column sums
 };
 
+// Two values -> two E4M3 codes in one half of `old`.  With |x| <= a and r =
+// RN32(448 / a) a finite |x r| is at most 448.0001, which the convert takes to
+// 448, so there is nothing to clamp.
+template <bool HI>
+__device__ __forceinline__ uint32_t codes2(float a, float b, uint32_t old) {
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, (int)old, HI);
+}
+
+// v of lane i (compile time) of the 16 lanes of this one's row.
+template <int I>
+__device__ __forceinline__ float of_row_lane(float v) {
+  return __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(v), (I << 5) | 0x10));
+}
+
 template <int ACT>
 __global__ __launch_bounds__(256) void epilogue_backward_kernel(BackwardArgs a) {
   constexpr int kPitch = 136;  // LDS row pitch of the staged codes (bytes)
@@ -66,7 +80,7 @@ __global__ __launch_bounds__(256) void epilogue_backward_kernel(BackwardArgs a) 
       for (int c = 0; c < 8; ++c) d[i][c] = 0.0f;
     }
   }
-  float cm[8], cs[8];
+  float cm[8], cs[8], rm[8];
 #pragma unroll
   for (int c = 0; c < 8; ++c) cm[c] = cs[c] = 0.0f;
 #pragma unroll
@@ -78,18 +92,30 @@ __global__ __launch_bounds__(256) void epilogue_backward_kernel(BackwardArgs a) 
       cm[c] = fmaxf(cm[c], fabsf(d[i][c]));
       cs[c] += d[i][c];
     }
-    float sc, r;
-    group_scale(max_row16(m), sc, r);
-    uint32_t lo = cvt2_e4m3<false>(d[i][0] * r, d[i][1] * r, 0u);
-    lo = cvt2_e4m3<true>(d[i][2] * r, d[i][3] * r, lo);
-    uint32_t hi = cvt2_e4m3<false>(d[i][4] * r, d[i][5] * r, 0u);
-    hi = cvt2_e4m3<true>(d[i][6] * r, d[i][7] * r, hi);
-    const int64_t row = mb * 128 + r0 + 16 * i;
-    if (row < a.M) {
-      __builtin_nontemporal_store(u32x2{lo, hi}, reinterpret_cast<u32x2*>(a.q + row * a.ldq + col));
-      if (lane == 0) a.s[nb * a.lds + row] = sc;
-    }
+    rm[i] = max_row16(m);
   }
+  // lane i (mod 8) forms the scale of row i, for all 16 lanes of the row: the
+  // IEEE divisions would otherwise be a tenth of the kernel's instructions
+  float mine = rm[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) mine = (lane & 7) == i ? rm[i] : mine;
+  float scale, rcp_mine;
+  group_scale(mine, scale, rcp_mine);
+  {
+    const int64_t row = mb * 128 + r0 + 16 * lane;
+    if (lane < 8 && row < a.M) a.s[nb * a.lds + row] = scale;
+  }
+  static_for<0, 8>([&](auto i_) {
+    constexpr int i = decltype(i_)::value;
+    const float r = of_row_lane<i>(rcp_mine);
+    uint32_t lo = codes2<false>(d[i][0] * r, d[i][1] * r, 0u);
+    lo = codes2<true>(d[i][2] * r, d[i][3] * r, lo);
+    uint32_t hi = codes2<false>(d[i][4] * r, d[i][5] * r, 0u);
+    hi = codes2<true>(d[i][6] * r, d[i][7] * r, hi);
+    const int64_t row = mb * 128 + r0 + 16 * i;
+    if (row < a.M)
+      __builtin_nontemporal_store(u32x2{lo, hi}, reinterpret_cast<u32x2*>(a.q + row * a.ldq + col));
+  });
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     cm[c] = fmaxf(cm[c], __shfl_xor(cm[c], 16, 64));
@@ -119,10 +145,10 @@ __global__ __launch_bounds__(256) void epilogue_backward_kernel(BackwardArgs a) 
   const float4 rb = *reinterpret_cast<const float4*>(rcp + lane * 8 + 4);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    uint32_t lo = cvt2_e4m3<false>(d[i][0] * ra.x, d[i][1] * ra.y, 0u);
-    lo = cvt2_e4m3<true>(d[i][2] * ra.z, d[i][3] * ra.w, lo);
-    uint32_t hi = cvt2_e4m3<false>(d[i][4] * rb.x, d[i][5] * rb.y, 0u);
-    hi = cvt2_e4m3<true>(d[i][6] * rb.z, d[i][7] * rb.w, hi);
+    uint32_t lo = codes2<false>(d[i][0] * ra.x, d[i][1] * ra.y, 0u);
+    lo = codes2<true>(d[i][2] * ra.z, d[i][3] * ra.w, lo);
+    uint32_t hi = codes2<false>(d[i][4] * rb.x, d[i][5] * rb.y, 0u);
+    hi = codes2<true>(d[i][6] * rb.z, d[i][7] * rb.w, hi);
     *reinterpret_cast<u32x2*>(tile + (r0 + 16 * i) * kPitch + lane * 8) = u32x2{lo, hi};
   }
   __syncthreads();
@@ -144,14 +170,19 @@ __global__ __launch_bounds__(256) void epilogue_backward_kernel(BackwardArgs a) 
   }
 }
 
-// dbias from the blocks' column sums, one thread per column.
-__global__ __launch_bounds__(64) void epilogue_bias_kernel(const float* part, int64_t MB,
-                                                           int64_t N, float* dbias) {
-  const int64_t n = (int64_t)blockIdx.x * 64 + threadIdx.x;
-  if (n >= N) return;
+// dbias from the blocks' column sums: 64 columns per workgroup, its four waves
+// taking every fourth block (a fixed order).
+__global__ __launch_bounds__(256) void epilogue_bias_kernel(const float* part, int64_t MB,
+                                                            int64_t N, float* dbias) {
+  __shared__ float sum[4][64];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t n = (int64_t)blockIdx.x * 64 + lane;  // N is a multiple of 128
   float s = 0.0f;
-  for (int64_t b = 0; b < MB; ++b) s += part[b * N + n];
-  dbias[n] = s;
+#pragma unroll 8
+  for (int64_t b = wave; b < MB; b += 4) s += part[b * N + n];
+  sum[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0) dbias[n] = (sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]);
 }
 
 }  // namespace
@@ -185,7 +216,7 @@ hipError_t launch_epilogue_backward(const uint16_t* dy, int64_t lddy, const uint
       e = launch_kernel(epilogue_backward_kernel<kActNone>, grid, block, stream, a);
   }
   if (e != hipSuccess) return e;
-  return launch_kernel(epilogue_bias_kernel, dim3((unsigned)((N + 63) / 64)), dim3(64), stream,
+  return launch_kernel(epilogue_bias_kernel, dim3((unsigned)(N / 64)), dim3(256), stream,
                        static_cast<const float*>(part), MB, N, dbias);
 }
 
