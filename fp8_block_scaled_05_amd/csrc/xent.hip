@@ -90,105 +90,146 @@ struct Rows {
   float* dloss;    // of the packed rows (backward)
 };
 
-// One workgroup: packs the rows with a loss, in order.
-__global__ __launch_bounds__(1024) void xent_rows_kernel(const int64_t* target, int64_t M,
-                                                         int64_t V, int64_t ignore, Rows r,
-                                                         const float* lse, const float* dloss,
-                                                         float* loss_out, float* lse_out) {
+struct RowArgs {
+  const int64_t* target;
+  int64_t M, V, ignore;
+  Rows r;
+  const float *lse, *dloss;      // backward
+  float *loss_out, *lse_out;     // forward: zeroed for the rows without a loss
+  const uint16_t* x;
+  int64_t ldx, K;
+  uint16_t *xc, *xs;             // see pack_row; xs: backward
+};
+
+constexpr int kRowThreads = 1024;
+
+// One workgroup: numbers the rows with a loss, in order.  write: leaves it all in
+// a.r (and the zeros); index: optional, the packed rows' numbers (M <=
+// kRowThreads).  Returns the header, to every thread.
+__device__ __forceinline__ Header number_rows(const RowArgs& a, bool write, int32_t* index) {
   __shared__ int32_t count[16];
   __shared__ float red[2][16];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  int32_t base = 0;
+  Header h{0, 0, 1.0f};
   float top = 0.0f, low = INFINITY, high = -INFINITY;
   bool nan = false;
-  for (int64_t m0 = 0; m0 < M; m0 += 1024) {
+  for (int64_t m0 = 0; m0 < a.M; m0 += kRowThreads) {
     const int64_t m = m0 + threadIdx.x;
-    const int64_t t = m < M ? target[m] : ignore;
-    const bool valid = m < M && t != ignore && t >= 0 && t < V;
+    const int64_t t = m < a.M ? a.target[m] : a.ignore;
+    const bool valid = m < a.M && t != a.ignore && t >= 0 && t < a.V;
     const unsigned long long mask = __ballot(valid);
     __syncthreads();
     if (lane == 0) count[wave] = __popcll(mask);
     __syncthreads();
-    int32_t at = base, all = 0;
+    int32_t at = h.rows, all = 0;
     for (int w = 0; w < 16; ++w) {
       at += w < wave ? count[w] : 0;
       all += count[w];
     }
-    base += all;
+    h.rows += all;
     at += __popcll(mask & ((1ull << lane) - 1ull));
+    if (valid && index) index[at] = (int32_t)m;
+    if (valid && a.dloss) {
+      const float d = a.dloss[m];
+      top = fmaxf(top, fabsf(d));
+      low = fminf(low, d);
+      high = fmaxf(high, d);
+      nan = nan || d != d;
+    }
+    if (!write || m >= a.M) continue;
     if (valid) {
-      r.index[at] = (int32_t)m;
-      r.target[at] = (int32_t)t;
-      if (dloss) {
-        const float d = dloss[m];
-        r.lse[at] = lse[m];
-        r.dloss[at] = d;
-        top = fmaxf(top, fabsf(d));
-        low = fminf(low, d);
-        high = fmaxf(high, d);
-        nan = nan || d != d;
+      a.r.index[at] = (int32_t)m;
+      a.r.target[at] = (int32_t)t;
+      if (a.dloss) {
+        a.r.lse[at] = a.lse[m];
+        a.r.dloss[at] = a.dloss[m];
       }
+    } else if (a.loss_out) {
+      a.loss_out[m] = a.lse_out[m] = 0.0f;
     }
-    if (m < M) {
-      r.place[m] = valid ? at : -1;
-      if (loss_out && !valid) loss_out[m] = lse_out[m] = 0.0f;
-    }
+    a.r.place[m] = valid ? at : -1;
   }
-  if (dloss) {
+  if (a.dloss) {
     top = max_wave64(top);
     high = max_wave64(high);
     low = -max_wave64(-low);
     nan = __any(nan);
-    __syncthreads();
     if (lane == 0) {
       red[0][wave] = top;
       red[1][wave] = !nan && (low == high || low > high) ? low : NAN;  // low > high: no rows
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-      bool same = true;
-      float v = INFINITY;
-      top = 0.0f;
-      for (int w = 0; w < 16; ++w) {
-        top = fmaxf(top, red[0][w]);
-        const float x = red[1][w];
-        if (x == INFINITY) continue;  // a wave without rows
-        same = same && x == x && (v == INFINITY || v == x);
-        v = x;
-      }
-      r.h->c = top > 0.0f && top < INFINITY ? top : 1.0f;
-      r.h->uniform = same && fabsf(v) == top && v > 0.0f ? 1 : 0;
+    bool same = true;
+    float v = INFINITY;
+    top = 0.0f;
+    for (int w = 0; w < 16; ++w) {
+      top = fmaxf(top, red[0][w]);
+      const float x = red[1][w];
+      if (x == INFINITY) continue;  // a wave without rows
+      same = same && x == x && (v == INFINITY || v == x);
+      v = x;
     }
+    h.c = top > 0.0f && top < INFINITY ? top : 1.0f;
+    h.uniform = same && fabsf(v) == top && v > 0.0f ? 1 : 0;
   }
-  if (threadIdx.x == 0) r.h->rows = base;
+  if (write && threadIdx.x == 0) *a.r.h = h;
+  return h;
 }
 
-// Packs the rows of x, one wave per packed row, zeros up to a multiple of kPad
-// rows (the last k-steps of dw's product); xs (backward, dloss not uniform):
-// the rows times dloss / c.
-__global__ __launch_bounds__(256) void xent_pack_kernel(const uint16_t* x, int64_t ldx, int64_t M,
-                                                        int64_t K, Rows r, uint16_t* xc,
-                                                        uint16_t* xs) {
-  const int64_t q = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+__global__ __launch_bounds__(kRowThreads) void xent_rows_kernel(RowArgs a) {
+  number_rows(a, true, nullptr);
+}
+
+// Packed row q of x, by one wave; zeros for rows past the last up to a multiple
+// of kPad (the last k-steps of dw's product); xs (backward, dloss not uniform):
+// the row times dloss / c.  Nothing is packed where x is used in place: all
+// rows count and, in the backward pass, end at such a multiple.
+__device__ __forceinline__ void pack_row(const RowArgs& a, const Header& h, int64_t q,
+                                         int64_t row) {
   const int lane = threadIdx.x & 63;
-  const int64_t rows = r.h->rows, upto = (rows + kPad - 1) / kPad * kPad;
-  const bool scaled = xs != nullptr && !r.h->uniform;
-  // all rows, as they are: used in place
-  if (q >= upto || (rows == M && (xs == nullptr || (rows == upto && !scaled)))) return;
+  const int64_t rows = h.rows, upto = (rows + kPad - 1) / kPad * kPad;
+  const bool scaled = a.xs != nullptr && !h.uniform;
+  if (q >= upto || (rows == a.M && (a.xs == nullptr || (rows == upto && !scaled)))) return;
   const bool real = q < rows;
-  const uint16_t* src = x + (real ? (int64_t)r.index[q] : 0) * ldx;
-  const float f = scaled && real ? r.dloss[q] / r.h->c : 1.0f;
-  for (int64_t k = lane * 8; k < K; k += 512) {
+  const uint16_t* src = a.x + (real ? row : 0) * a.ldx;
+  const float f = scaled && real ? a.dloss[row] / h.c : 1.0f;
+  for (int64_t k = lane * 8; k < a.K; k += 512) {
     u32x4 v = {0u, 0u, 0u, 0u};
     if (real) v = *reinterpret_cast<const u32x4*>(src + k);
-    *reinterpret_cast<u32x4*>(xc + q * K + k) = v;
+    *reinterpret_cast<u32x4*>(a.xc + q * a.K + k) = v;
     if (scaled) {
       u32x4 w;
 #pragma unroll
       for (int e = 0; e < 4; ++e) w[e] = bf16x2_rne(bf16_lo(v[e]) * f, bf16_hi(v[e]) * f);
-      *reinterpret_cast<u32x4*>(xs + q * K + k) = w;
+      *reinterpret_cast<u32x4*>(a.xs + q * a.K + k) = w;
     }
   }
+}
+
+__global__ __launch_bounds__(256) void xent_pack_kernel(RowArgs a) {
+  const int64_t q = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const Header h = *a.r.h;
+  pack_row(a, h, q, q < h.rows ? a.r.index[q] : 0);
+}
+
+// Both in one launch, M <= kRowThreads: every workgroup numbers the rows for
+// itself, the first one writes the numbers down.
+__global__ __launch_bounds__(kRowThreads) void xent_rows_pack_kernel(RowArgs a) {
+  __shared__ int32_t index[kRowThreads];
+  const Header h = number_rows(a, blockIdx.x == 0, index);
+  __syncthreads();
+  const int64_t q = (int64_t)blockIdx.x * (kRowThreads / 64) + (threadIdx.x >> 6);
+  pack_row(a, h, q, q < h.rows ? index[q] : 0);
+}
+
+hipError_t launch_rows(const RowArgs& a, hipStream_t stream) {
+  const int64_t padded = cdiv(a.M, kPad) * kPad;
+  if (a.M <= kRowThreads && a.M > 0)
+    return launch_kernel(xent_rows_pack_kernel, dim3((unsigned)(padded / (kRowThreads / 64))),
+                         dim3(kRowThreads), stream, a);
+  const hipError_t e = launch_kernel(xent_rows_kernel, dim3(1), dim3(kRowThreads), stream, a);
+  if (e != hipSuccess || a.M == 0) return e;
+  return launch_kernel(xent_pack_kernel, dim3((unsigned)(padded / 4)), dim3(256), stream, a);
 }
 
 // Tile number `i` of a raster of PT x QT tiles: 8 p-tiles x all q-tiles, in
@@ -542,25 +583,57 @@ __device__ __forceinline__ void add_dx(const GradArgs& a, int64_t rows, bool fir
   }
 }
 
-// A tile of a piece's dw.
+// v[t] of lane row g (16 lanes each) <-> v[g] of lane row t.
+__device__ __forceinline__ void transpose_lane_rows(uint32_t (&v)[4]) {
+  typedef uint32_t pair __attribute__((ext_vector_type(2)));
+#pragma unroll
+  for (int t = 0; t < 4; t += 2) {  // bit 0 of t and of g
+    const pair r = __builtin_amdgcn_permlane16_swap(v[t], v[t + 1], false, false);
+    v[t] = r.x;
+    v[t + 1] = r.y;
+  }
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {  // bit 1
+    const pair r = __builtin_amdgcn_permlane32_swap(v[t], v[t + 2], false, false);
+    v[t] = r.x;
+    v[t + 2] = r.y;
+  }
+}
+
+// A tile of a piece's dw.  Lane row g holds columns 4 g .. + 3 of every MFMA
+// tile; transposed over four tiles it holds the 16 columns of tile g, and a row
+// of w is stored in whole 128-byte lines.
 template <class C>
 __device__ __forceinline__ void store_dw(const GradArgs& a, int64_t p0, int64_t q0,
                                          const gemm16::Acc<C>& acc) {
+  static_assert(C::FP % 4 == 0 && C::NI == 1, "groups of four MFMA tiles");
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
   const int64_t pw = p0 + wave / C::WQ * C::TP;
   const float c = a.r.h->c;
-  if (pw >= a.K) return;
+  if (pw >= a.K) return;  // wave-uniform: a wave's columns exist or do not
 #pragma unroll
   for (int j = 0; j < C::FQ; ++j) {
     const int64_t q = q0 + wave % C::WQ * C::TQ + 16 * j + l16;
-    if (q >= a.nv) continue;
+    uint16_t* const row = a.dw + (a.v0 + q) * a.lddw + pw + 16 * g;
 #pragma unroll
-    for (int i = 0; i < C::FP; ++i) {
-      const v4f v = acc[i][j] * c;
-      *reinterpret_cast<u32x2*>(a.dw + (a.v0 + q) * a.lddw + pw + gemm16::p_lane<C>(g) + gemm16::p_tile<C>(i)) =
-          u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+    for (int i0 = 0; i0 < C::FP; i0 += 4) {
+      uint32_t lo[4], hi[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const v4f v = acc[i0 + t][j] * c;
+        lo[t] = bf16x2_rne(v[0], v[1]);
+        hi[t] = bf16x2_rne(v[2], v[3]);
+      }
+      transpose_lane_rows(lo);
+      transpose_lane_rows(hi);
+      if (q < a.nv) {
+        u32x4* d = reinterpret_cast<u32x4*>(row + 16 * i0);
+        d[0] = u32x4{lo[0], hi[0], lo[1], hi[1]};
+        d[1] = u32x4{lo[2], hi[2], lo[3], hi[3]};
+      }
     }
+    __builtin_amdgcn_sched_barrier(0);  // one j at a time: few registers beside the sums
   }
 }
 
@@ -573,7 +646,7 @@ __device__ __forceinline__ uint32_t dx_splits(const GradArgs& a, int64_t rows, u
   const uint32_t sx = (uint32_t)(a.ldg / kStep), sw = (uint32_t)(rows / kStep) + kTileSteps;
   const uint64_t all = (uint64_t)tiles_x * sx + (uint64_t)tiles_w * sw;
   uint32_t s = 1;
-  while (s < 32 && sx / s > 8 && 2ull * G * (sx / s) > all && 2 * s * rows <= a.dx_rows) s *= 2;
+  while (s < 32 && sx / s > 4 && 2ull * G * (sx / s) > all && 2 * s * rows <= a.dx_rows) s *= 2;
   return s;
 }
 
@@ -632,12 +705,14 @@ __global__ __launch_bounds__(CX::THREADS, 2) void xent_grad_kernel(GradArgs a, i
     uint32_t ahead = last ? (2 * pairs / splits + kTileSteps) / (steps + kTileSteps) : 0;
     if (ahead * behind > NW) ahead = NW / behind;
     const uint32_t early = ahead * behind, mine = behind && w >= last ? ahead : 0;
+    // too few dw tiles for that: the workgroups without a dx tile come first
+    const uint32_t id = early ? w : (w >= last ? w - last : w + G - last);
     auto at = [&](int i) {
       const uint32_t n = (uint32_t)i < mine ? w - last + (uint32_t)i * behind
-                                            : early + w + ((uint32_t)i - mine) * G;
+                                            : early + id + ((uint32_t)i - mine) * G;
       return raster(n < early ? n : early + in_rounds(n - early, NW - early), PT, QW);
     };
-    const int n = (int)mine + share(NW - early, w, G);
+    const int n = (int)mine + share(NW - early, id, G);
     auto finish = [&](int i, const gemm16::Acc<C>& acc) {
       const TileAt t = at(i);
       store_dw<C>(a, (int64_t)t.p * C::BP, (int64_t)t.q * C::BQ, acc);
@@ -804,12 +879,8 @@ hipError_t launch_xent(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_
     return launch_kernel(xent_join_kernel<true>, dim3((unsigned)M), dim3(256), stream, a, 0u,
                          LogitsSmall::TP, LogitsSmall::TP, ignore, loss, lse);
   }
-  e = launch_kernel(xent_rows_kernel, dim3(1), dim3(1024), stream, target, M, V, ignore, p.r,
-                    static_cast<const float*>(nullptr), static_cast<const float*>(nullptr), loss,
-                    lse);
-  if (e != hipSuccess) return e;
-  e = launch_kernel(xent_pack_kernel, dim3((unsigned)cdiv(cdiv(M, kPad) * kPad, 4)), dim3(256),
-                    stream, x, ldx, M, K, p.r, p.xc, static_cast<uint16_t*>(nullptr));
+  e = launch_rows({target, M, V, ignore, p.r, nullptr, nullptr, loss, lse, x, ldx, K, p.xc,
+                   nullptr}, stream);
   if (e != hipSuccess) return e;
   e = p.small ? launch_kernel(xent_loss_kernel<LogitsSmall, false>, dim3((unsigned)tiles), block,
                               stream, a)
@@ -866,15 +937,9 @@ hipError_t launch_xent_backward(const uint16_t* x, int64_t ldx, const uint16_t* 
   const GradPlan p = grad_plan(workspace, M, V, K);
   const GradArgs a{x,   ldx, p.xc, p.xs,  w, ldw, M,     V,         K,
                    p.r, p.g, p.ldg, 0,    0, p.dxp, p.dx_rows, dw, lddw};
-  hipError_t e = launch_kernel(xent_rows_kernel, dim3(1), dim3(1024), stream, target, M, V, ignore,
-                               p.r, lse, dloss, static_cast<float*>(nullptr),
-                               static_cast<float*>(nullptr));
+  const hipError_t e = launch_rows({target, M, V, ignore, p.r, lse, dloss, nullptr, nullptr, x, ldx,
+                                    K, p.xc, p.xs}, stream);
   if (e != hipSuccess) return e;
-  if (M > 0) {
-    e = launch_kernel(xent_pack_kernel, dim3((unsigned)cdiv(cdiv(M, kPad) * kPad, 4)), dim3(256),
-                      stream, x, ldx, M, K, p.r, p.xc, p.xs);
-    if (e != hipSuccess) return e;
-  }
   return p.small ? launch_pieces<DxSmall, DwSmall>(p, a, 2, dx, lddx, stream)
                  : launch_pieces<DxCfg, DwCfg>(p, a, 1, dx, lddx, stream);
 }
