@@ -33,10 +33,12 @@ DEVICE_FLAGS = [
 ]
 
 
-# Per-source additions.  The few-row kernels run one wave per SIMD, where the
-# compiler would put MFMA results in accumulation registers and copy each
-# one out before its FP32 promotion; this option keeps them in VGPRs.
-EXTRA_FLAGS = {"gemm_few_rows.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# Per-source additions.  Kernels of one wave per SIMD, where the compiler would
+# put MFMA results in accumulation registers and copy each one out before its
+# FP32 promotion (the few-row FP8 kernels) or in and out of every k-step (the
+# cross entropy's small tiles); this option keeps them in VGPRs.
+EXTRA_FLAGS = {"gemm_few_rows.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+               "xent.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def _hipcc():

@@ -244,7 +244,14 @@ __device__ __forceinline__ void product_deep(const Operand& op, const Operand& o
   const Copiers<C> cp(op, oq, wave, lane);
   // step s lives in stage s % STAGES; past the last step its copies are
   // issued again, never read, so that the wait counts stay constants
-  auto last = [&](int s) { return s < steps ? s : steps - 1; };
+  // Rows 4 KB apart share their memory channels: workgroups that walk k in step
+  // would all ask the same few, so each starts elsewhere in k (72569 x 4096, one
+  // row: 158 and 140 us; at other strides the start costs 1%)
+  const int start = (int)((blockIdx.x * (op.ld % 4096 == 0 ? 5u : 0u)) % (uint32_t)steps);
+  auto last = [&](int s) {
+    const int t = s < steps ? s : steps - 1;
+    return t + start < steps ? t + start : t + start - steps;
+  };
 #pragma unroll
   for (int s = 0; s < C::STAGES - 1; ++s) cp.issue_all(last(s), stages[s]);
   for (int s = 0; s < steps; s += C::STAGES) {
@@ -317,6 +324,14 @@ __device__ __forceinline__ void run_tiles(int n, uint8_t* const (&stages)[4], Jo
   Job job = job_of(0);
   Copiers<C> cp(job.p, job.q, wave, lane);
   int off = 0;  // steps of the stream before cp's first
+  // the XCDs start at different eighths of k, so that they do not all ask the
+  // same memory channels for the same stretch of their operands at one time
+  // (4096 x 65536 x 3968 loss 1514 and 1487 us); with k-major operands, whose k
+  // runs over rows, it gains nothing and costs registers
+  constexpr bool APART = C::LP == kRow && C::LQ == kRow;
+  const int xcd = (int)(blockIdx.x % 8);
+  int len = job.steps, from = len * xcd / 8;
+  auto at = [&](int s) { return !APART ? s : s + from < len ? s + from : s + from - len; };
   auto step = [&](int s, uint8_t* st, uint8_t* next, Acc<C>& acc, const Job& then, bool turn) {
     static_for<0, R>([&](auto r_) {
       constexpr int r = decltype(r_)::value, h = r / C::FP, i = r % C::FP;
@@ -328,6 +343,8 @@ __device__ __forceinline__ void run_tiles(int n, uint8_t* const (&stages)[4], Jo
         if (turn) {  // what is copied from here on is the next tile's
           cp = Copiers<C>(then.p, then.q, wave, lane);
           off = s + 2;
+          len = then.steps;
+          from = len * xcd / 8;
         }
       }
       if constexpr (r + D < R) {
@@ -347,17 +364,17 @@ __device__ __forceinline__ void run_tiles(int n, uint8_t* const (&stages)[4], Jo
         }
         constexpr int c = (r + D) % R;
         if constexpr (j == 0 && c < C::COPIES) {
-          if constexpr (r >= R - D) cp.issue(s + 2 - off, st, c);
-          else cp.issue(s + 1 - off, next, c);
+          if constexpr (r >= R - D) cp.issue(at(s + 2 - off), st, c);
+          else cp.issue(at(s + 1 - off), next, c);
         }
         __builtin_amdgcn_sched_barrier(0);
       });
     });
   };
 
-  cp.issue_all(0, stages[0]);
+  cp.issue_all(at(0), stages[0]);
 #pragma unroll
-  for (int c = 0; c < D && c < C::COPIES; ++c) cp.issue(1, stages[1], c);
+  for (int c = 0; c < D && c < C::COPIES; ++c) cp.issue(at(1), stages[1], c);
   gemm::barrier_after_vmcnt<(D < C::COPIES ? D : C::COPIES)>();
 #pragma unroll
   for (int j = 0; j < C::FQ; ++j) q[0][j] = load_frag<C, false>(stages[0], fq, j, 0);

@@ -116,6 +116,8 @@ __device__ __forceinline__ Header number_rows(const RowArgs& a, bool write, int3
   for (int64_t m0 = 0; m0 < a.M; m0 += kRowThreads) {
     const int64_t m = m0 + threadIdx.x;
     const int64_t t = m < a.M ? a.target[m] : a.ignore;
+    const float d = m < a.M && a.dloss ? a.dloss[m] : 0.0f;
+    const float l = m < a.M && a.dloss && write ? a.lse[m] : 0.0f;
     const bool valid = m < a.M && t != a.ignore && t >= 0 && t < a.V;
     const unsigned long long mask = __ballot(valid);
     __syncthreads();
@@ -130,7 +132,6 @@ __device__ __forceinline__ Header number_rows(const RowArgs& a, bool write, int3
     at += __popcll(mask & ((1ull << lane) - 1ull));
     if (valid && index) index[at] = (int32_t)m;
     if (valid && a.dloss) {
-      const float d = a.dloss[m];
       top = fmaxf(top, fabsf(d));
       low = fminf(low, d);
       high = fmaxf(high, d);
@@ -141,8 +142,8 @@ __device__ __forceinline__ Header number_rows(const RowArgs& a, bool write, int3
       a.r.index[at] = (int32_t)m;
       a.r.target[at] = (int32_t)t;
       if (a.dloss) {
-        a.r.lse[at] = a.lse[m];
-        a.r.dloss[at] = a.dloss[m];
+        a.r.lse[at] = l;
+        a.r.dloss[at] = d;
       }
     } else if (a.loss_out) {
       a.loss_out[m] = a.lse_out[m] = 0.0f;
@@ -386,13 +387,13 @@ __device__ __forceinline__ void logits_tiles(const uint16_t* x, int64_t ldx, int
   if constexpr (C::STAGES > 2) {
     if (blockIdx.x >= PT * QT) return;  // whole workgroup
     const TileAt t = raster(in_rounds(blockIdx.x, PT * QT), PT, QT);
-    const int64_t p0 = (int64_t)t.p * C::BP;
-    int64_t q0 = (int64_t)t.q * C::BQ;
-    // a tile past the last row (whose outputs are padding) reads the last one
-    const gemm16::Job j = job(C{}, p0, q0 < rows ? q0 : rows - 1);
+    const int64_t p0 = (int64_t)t.p * C::BP, q0 = (int64_t)t.q * C::BQ;
     gemm16::Acc<C> acc;
     gemm16::clear<C>(acc);
-    gemm16::product_deep<C>(j.p, j.q, j.steps, stages, acc);
+    if (q0 < rows) {  // otherwise padding: zeros in any case
+      const gemm16::Job j = job(C{}, p0, q0);
+      gemm16::product_deep<C>(j.p, j.q, j.steps, stages, acc);
+    }
     done(C{}, p0, q0, acc);
   } else {
     const uint32_t w0 = blockIdx.x, G = gridDim.x;
