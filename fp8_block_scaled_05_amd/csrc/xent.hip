@@ -102,11 +102,13 @@ struct RowArgs {
 };
 
 constexpr int kRowThreads = 1024;
+constexpr int kRowWaves = kRowThreads / 64;
 
 // One workgroup: numbers the rows with a loss, in order.  write: leaves it all in
-// a.r (and the zeros); index: optional, the packed rows' numbers (M <=
-// kRowThreads).  Returns the header, to every thread.
-__device__ __forceinline__ Header number_rows(const RowArgs& a, bool write, int32_t* index) {
+// a.r (and the zeros); index: optional, receives the rows of the packed rows
+// first .. first + kRowWaves - 1.  Returns the header, to every thread.
+__device__ __forceinline__ Header number_rows(const RowArgs& a, bool write, int32_t* index,
+                                              int32_t first) {
   __shared__ int32_t count[16];
   __shared__ float red[2][16];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -130,7 +132,7 @@ __device__ __forceinline__ Header number_rows(const RowArgs& a, bool write, int3
     }
     h.rows += all;
     at += __popcll(mask & ((1ull << lane) - 1ull));
-    if (valid && index) index[at] = (int32_t)m;
+    if (valid && index && at >= first && at < first + kRowWaves) index[at - first] = (int32_t)m;
     if (valid && a.dloss) {
       top = fmaxf(top, fabsf(d));
       low = fminf(low, d);
@@ -178,7 +180,7 @@ __device__ __forceinline__ Header number_rows(const RowArgs& a, bool write, int3
 }
 
 __global__ __launch_bounds__(kRowThreads) void xent_rows_kernel(RowArgs a) {
-  number_rows(a, true, nullptr);
+  number_rows(a, true, nullptr, 0);
 }
 
 // Packed row q of x, by one wave; zeros for rows past the last up to a multiple
@@ -213,20 +215,22 @@ __global__ __launch_bounds__(256) void xent_pack_kernel(RowArgs a) {
   pack_row(a, h, q, q < h.rows ? a.r.index[q] : 0);
 }
 
-// Both in one launch, M <= kRowThreads: every workgroup numbers the rows for
-// itself, the first one writes the numbers down.
+// Both in one launch: every workgroup numbers the rows for itself, the first one
+// writes the numbers down.  Up to kFusedRows rows, whose workgroups are all
+// resident at once.
+constexpr int64_t kFusedRows = 8192;
 __global__ __launch_bounds__(kRowThreads) void xent_rows_pack_kernel(RowArgs a) {
-  __shared__ int32_t index[kRowThreads];
-  const Header h = number_rows(a, blockIdx.x == 0, index);
+  __shared__ int32_t index[kRowWaves];
+  const int first = (int)blockIdx.x * kRowWaves, wave = threadIdx.x >> 6;
+  const Header h = number_rows(a, blockIdx.x == 0, index, first);
   __syncthreads();
-  const int64_t q = (int64_t)blockIdx.x * (kRowThreads / 64) + (threadIdx.x >> 6);
-  pack_row(a, h, q, q < h.rows ? index[q] : 0);
+  pack_row(a, h, first + wave, first + wave < h.rows ? index[wave] : 0);
 }
 
 hipError_t launch_rows(const RowArgs& a, hipStream_t stream) {
   const int64_t padded = cdiv(a.M, kPad) * kPad;
-  if (a.M <= kRowThreads && a.M > 0)
-    return launch_kernel(xent_rows_pack_kernel, dim3((unsigned)(padded / (kRowThreads / 64))),
+  if (a.M <= kFusedRows && a.M > 0)
+    return launch_kernel(xent_rows_pack_kernel, dim3((unsigned)(padded / kRowWaves)),
                          dim3(kRowThreads), stream, a);
   const hipError_t e = launch_kernel(xent_rows_kernel, dim3(1), dim3(kRowThreads), stream, a);
   if (e != hipSuccess || a.M == 0) return e;
@@ -646,8 +650,10 @@ __device__ __forceinline__ uint32_t dx_splits(const GradArgs& a, int64_t rows, u
                                               uint32_t tiles_w, uint32_t G) {
   const uint32_t sx = (uint32_t)(a.ldg / kStep), sw = (uint32_t)(rows / kStep) + kTileSteps;
   const uint64_t all = (uint64_t)tiles_x * sx + (uint64_t)tiles_w * sw;
+  // every part has work in the first piece, which sets them all
+  const uint32_t pads = (uint32_t)(((a.V < a.ldg ? a.V : a.ldg) + kPad - 1) / kPad);
   uint32_t s = 1;
-  while (s < 32 && sx / s > 4 && 2ull * G * (sx / s) > all && 2 * s * rows <= a.dx_rows) s *= 2;
+  while (s < 32 && 2 * s <= pads && sx / s > 4 && 2ull * G * (sx / s) > all && 2 * s * rows <= a.dx_rows) s *= 2;
   return s;
 }
 
