@@ -465,9 +465,28 @@ __global__ __launch_bounds__(256) void xent_join_kernel(LossArgs a, uint32_t G, 
   if (tp != tp_half && q >= rows - (int64_t)half_rows(rows, a.V, a.K, G)) w = tp_half;
   const int64_t blocks = (a.V + w - 1) / w;
   const float2* p = a.part + q * a.blocks;
+  // loaded ahead, and U pairs in flight per lane: with a row's 4040 pairs (FEW, V
+  // = 129280) taken one by one 9.7 us, so 4.6 us
+  const int64_t row = FEW ? q : (int64_t)a.r.index[q], t = FEW ? a.target[q] : 0;
+  const float at = a.at[q];
+  constexpr int U = FEW ? 16 : 8, STEP = FEW ? 256 : 64;
   float m = -INFINITY, s = 0.0f;
-  for (int64_t b = FEW ? threadIdx.x : lane; b < blocks; b += FEW ? 256 : 64)
-    join_pair(m, s, p[b].x, p[b].y);
+  for (int64_t b0 = FEW ? threadIdx.x : lane; b0 < blocks; b0 += U * STEP) {
+    float2 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = p[b0 + u * STEP < blocks ? b0 + u * STEP : blocks - 1];
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (b0 + u * STEP >= blocks) v[u].x = -INFINITY;
+      top = fmaxf(top, v[u].x);
+    }
+    s = m == -INFINITY ? s : s * __builtin_amdgcn_exp2f((m - top) * kLog2e);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      s += v[u].x == -INFINITY ? 0.0f : v[u].y * __builtin_amdgcn_exp2f((v[u].x - top) * kLog2e);
+    m = top;
+  }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) join_pair(m, s, __shfl_xor(m, d, 64), __shfl_xor(s, d, 64));
   if constexpr (FEW) {
@@ -475,7 +494,6 @@ __global__ __launch_bounds__(256) void xent_join_kernel(LossArgs a, uint32_t G, 
     __syncthreads();
     if (threadIdx.x != 0) return;
     for (int k = 1; k < 4; ++k) join_pair(m, s, part[k].x, part[k].y);
-    const int64_t t = a.target[q];
     if (t == ignore || t < 0 || t >= a.V) {
       loss[q] = lse[q] = 0.0f;
       return;
@@ -483,9 +501,8 @@ __global__ __launch_bounds__(256) void xent_join_kernel(LossArgs a, uint32_t G, 
   }
   if (lane != 0) return;
   const float l = m + logf(s);
-  const int64_t row = FEW ? q : (int64_t)a.r.index[q];
   lse[row] = l;
-  loss[row] = l - a.at[q];
+  loss[row] = l - at;
 }
 
 struct GradArgs {
