@@ -35,7 +35,6 @@ using gemm16::kRow;
 using gemm16::kStep;
 using gemm16::Operand;
 
-
 // Logits: q are the rows of x, p the vocabulary.  Large tiles, their half for a
 // last tile of at most 128 rows, and the small tile of few rows or small heads
 // (deep stream).
@@ -52,7 +51,9 @@ using DwSmall = gemm16::Cfg<128, 128, 2, 2, 2, kCol, kCol>;
 constexpr int64_t kTile = 256;
 constexpr int64_t kMaxTiles = INT32_MAX;  // of one launch: tile numbers are 32 bits
 constexpr int64_t kPad = 2 * kStep;  // k-steps come in pairs
-constexpr int64_t kFewXentRows = LogitsSmall::BQ;  // these are not packed
+// One tile of rows is not packed: 17 x 32003 x 2048 26 us, packed 29; 64 x 129280 x
+// 7168 370 and 378.
+constexpr int64_t kFewXentRows = LogitsSmall::BQ;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -66,7 +67,8 @@ dim3 tile_grid(int64_t tiles, int64_t per_cu = 1) {
 }
 
 // Whether a head's logits take the small tiles: by the estimated rounds of
-// workgroups, a round of 256x256 and of 128x64 tiles taking 100 and kSmallCost.
+// workgroups, a round of 256x256 and of 128x64 tiles taking 100 and kSmallCost
+// (100 x 10000 x 2048: 37 us large, 24 small; 256 x 32003 x 2048: 53 and 81).
 constexpr int64_t kSmallCost = 35;
 bool small_logits(int64_t M, int64_t V) {
   const int64_t cus = compute_units();
@@ -216,9 +218,10 @@ __global__ __launch_bounds__(256) void xent_pack_kernel(RowArgs a) {
 }
 
 // Both in one launch: every workgroup numbers the rows for itself, the first one
-// writes the numbers down.  Up to kFusedRows rows, whose workgroups are all
-// resident at once.
-constexpr int64_t kFusedRows = 8192;
+// writes the numbers down.  Up to kFusedRows rows: every workgroup reads all
+// targets (loss of 4096 x 1003 x 512 25.9 us fused, 27.6 not; of 6144 x 1003 x
+// 2048 63.7 and 59.5).
+constexpr int64_t kFusedRows = 4096;
 __global__ __launch_bounds__(kRowThreads) void xent_rows_pack_kernel(RowArgs a) {
   __shared__ int32_t index[kRowWaves];
   const int first = (int)blockIdx.x * kRowWaves, wave = threadIdx.x >> 6;
@@ -659,19 +662,48 @@ __device__ __forceinline__ void store_dw(const GradArgs& a, int64_t p0, int64_t 
   }
 }
 
-// Parts that the contraction of dx over a whole piece is cut into: until a
-// tile's steps are at most half of a workgroup's share of the launch, as far
-// as the room for the parts goes.  kTileSteps: a tile's start and end in steps.
-constexpr uint32_t kTileSteps = 3;
+// Parts that the contraction of dx over a whole piece is cut into: the number
+// whose launch (see xent_grad_kernel) ends first by an estimate in k-steps of a
+// workgroup, the parts' own cost included: they are written and added up again,
+// PART_COST / 4 steps for every 2^20 numbers.  Lane i estimates i + 1 parts;
+// whole numbers, so that every wave of every kernel comes to the same.
+// kTileSteps: a tile's start and end in steps.
+constexpr uint32_t kTileSteps = 3, kMostParts = 32;
+template <uint32_t PART_COST>
 __device__ __forceinline__ uint32_t dx_splits(const GradArgs& a, int64_t rows, uint32_t tiles_x,
                                               uint32_t tiles_w, uint32_t G) {
-  const uint32_t sx = (uint32_t)(a.ldg / kStep), sw = (uint32_t)(rows / kStep) + kTileSteps;
-  const uint64_t all = (uint64_t)tiles_x * sx + (uint64_t)tiles_w * sw;
+  const uint32_t s = threadIdx.x % kMostParts + 1;
+  const uint32_t dx = ((uint32_t)(a.ldg / kStep) + s - 1) / s + kTileSteps;
+  const uint32_t dw = (uint32_t)((rows + kStep - 1) / kStep) + kTileSteps;
+  const uint32_t NX = tiles_x * s, last = NX % G, behind = last ? G - last : 0;
+  uint32_t t = NX / G * dx;
+  if (last) {
+    uint32_t ahead = dx / dw;
+    if (ahead * behind > tiles_w) ahead = tiles_w / behind;
+    const uint32_t rem = tiles_w - ahead * behind;
+    const uint32_t more = rem > behind ? (rem - behind + G - 1) / G : 0;
+    const uint32_t all = (rem + G - 1) / G;
+    t += ahead ? dx + all * dw : (dx + more * dw > all * dw ? dx + more * dw : all * dw);
+  } else {
+    t += (tiles_w + G - 1) / G * dw;
+  }
+  t += (uint32_t)((uint64_t)s * (uint64_t)rows * (uint64_t)a.K * PART_COST >> 22);
   // every part has work in the first piece, which sets them all
   const uint32_t pads = (uint32_t)(((a.V < a.ldg ? a.V : a.ldg) + kPad - 1) / kPad);
-  uint32_t s = 1;
-  while (s < 32 && 2 * s <= pads && sx / s > 4 && 2ull * G * (sx / s) > all && 2 * s * rows <= a.dx_rows) s *= 2;
-  return s;
+  const bool fits = s == 1 || (s <= pads && s * rows <= a.dx_rows);
+  uint32_t best = fits ? (t < 0x3ffffff ? t : 0x3ffffff) << 6 | s : ~0u;
+#pragma unroll
+  for (int d = 1; d < (int)kMostParts; d <<= 1) {
+    const uint32_t o = __shfl_xor(best, d, 64);
+    best = o < best ? o : best;
+  }
+  return __builtin_amdgcn_readfirstlane(best) & 63;
+}
+
+// A small tile's step takes about half as long.
+template <class CX>
+constexpr uint32_t part_cost() {
+  return CX::BP == 256 ? 3 : 6;
 }
 
 // Backward, second launch of a piece: tiles of its part of dx, then of its
@@ -690,7 +722,7 @@ __global__ __launch_bounds__(CX::THREADS, 2) void xent_grad_kernel(GradArgs a, i
   // k-steps in pairs; G is zero past the vocabulary, up to whole tiles
   const uint32_t pairs = (uint32_t)((a.nv + 2 * kStep - 1) / (2 * kStep));
   // by the full piece, the same for all: a shorter last piece may use fewer
-  const uint32_t whole = dx_splits(a, rows, PT * QX, PT * (uint32_t)(a.ldg / CW::BQ), G);
+  const uint32_t whole = dx_splits<part_cost<CX>()>(a, rows, PT * QX, PT * (uint32_t)(a.ldg / CW::BQ), G);
   const uint32_t splits = whole < pairs ? whole : pairs;
   const uint32_t NX = PT * QX * splits;
   {
@@ -771,13 +803,14 @@ __global__ __launch_bounds__(256) void xent_dx_kernel(GradArgs a, uint32_t G, ui
                                                       uint16_t* dx, int64_t lddx) {
   const int64_t m = blockIdx.x / chunks;
   const int64_t k = (int64_t)(blockIdx.x % chunks) * 1024 + threadIdx.x * 4;
-  if (k >= a.K) return;
   const int64_t q = a.r.place[m], rows = a.r.h->rows;
+  const uint32_t PT = (uint32_t)((a.K + CX::BP - 1) / CX::BP);
+  const uint32_t QX = (uint32_t)((rows + CX::BQ - 1) / CX::BQ);
+  const uint32_t splits =
+      dx_splits<part_cost<CX>()>(a, rows, PT * QX, PT * (uint32_t)(a.ldg / CW::BQ), G);
+  if (k >= a.K) return;
   u32x2 o = {0u, 0u};
   if (q >= 0) {
-    const uint32_t PT = (uint32_t)((a.K + CX::BP - 1) / CX::BP);
-    const uint32_t QX = (uint32_t)((rows + CX::BQ - 1) / CX::BQ);
-    const uint32_t splits = dx_splits(a, rows, PT * QX, PT * (uint32_t)(a.ldg / CW::BQ), G);
     v4f s = *reinterpret_cast<const v4f*>(a.dxp + q * a.K + k);
 #pragma unroll 4
     for (uint32_t z = 1; z < splits; ++z)
@@ -841,9 +874,15 @@ LossPlan loss_plan(void* ws, int64_t M, int64_t V, int64_t K) {
 }
 
 // The vocabulary is cut into equal pieces, whole tiles each, whose G takes at
-// most kPieceBytes, the size of the last-level cache, so that G is read back
-// from there.
-constexpr int64_t kPieceBytes = int64_t(256) << 20;
+// most kPieceBytes.  Fewer pieces waste fewer partial rounds of tiles, which is
+// worth more than reading G back from the 256-MB last-level cache: 4096 x 129280
+// x 7168 in pieces of 256 MB 16.76 ms, of 1 GB 16.50; 16384 x 50257 x 4096 15.93
+// and 15.41.
+constexpr int64_t kPieceBytes = int64_t(1) << 30;
+
+// The parts of dx take at most this (or one part).  2000 x 129280 x 512: four parts
+// 1218 us, as many as are estimated best 837.
+constexpr int64_t kDxBytes = int64_t(256) << 20;
 
 struct GradPlan {
   Rows r;
@@ -865,11 +904,15 @@ GradPlan grad_plan(void* ws, int64_t M, int64_t V, int64_t K) {
   p.ldg = cdiv(cdiv(V, p.pieces), kTile) * kTile;
   p.pieces = cdiv(V, p.ldg);
   p.small_logits = small_logits(M, p.ldg);
-  // too few large tiles of dw to go round: small ones
-  p.small = p.ldg / kTile * cdiv(K, kTile) < 192;
-  // room for the parts of dx (see dx_splits): 32 for few rows, then as many as
-  // keep it at 8192 rows
-  const int64_t parts = 32 * M < 8192 ? 32 * M : 8192;
+  // Small tiles where dw has too few large ones to go round (1000 x 4096 x 1024, 64
+  // of them: 67 us large, 57 small; 1000 x 6144 x 1024, 96: 75 and 79) or dx so
+  // few that its parts cannot either (130 x 129280 x 512, 2: 184 and 152; 400 x
+  // 129280 x 512, 4: 245 and 271).
+  const int64_t KT = cdiv(K, kTile);
+  p.small = p.ldg / kTile * KT < 96 || Mt / kTile * KT < 4;
+  // room for the parts of dx (see dx_splits)
+  const int64_t room = kDxBytes / (4 * K);
+  const int64_t parts = kMostParts * M < room ? kMostParts * M : room;
   p.dx_rows = M > parts ? M : parts;
   p.r = take_rows(c, M, true);
   p.xc = c.take<uint16_t>(cdiv(M, kPad) * kPad * K);
@@ -926,8 +969,7 @@ hipError_t launch_pieces(const GradPlan& p, GradArgs a, int per_cu, uint16_t* dx
   const int64_t QL = cdiv(a.M, CL::BQ), QS = cdiv(a.M, kPad) * (kPad / CS::BQ);
   const int64_t tl = p.small_logits ? QS * (p.ldg / CS::BP) : QL * (p.ldg / CL::BP);
   const int64_t KT = cdiv(a.K, CX::BP), chunks = cdiv(a.K, 1024);
-  // dx may be cut into 32 parts
-  const int64_t most = KT * (cdiv(a.M, CX::BQ) * 32 + p.ldg / CW::BQ);
+  const int64_t most = KT * (cdiv(a.M, CX::BQ) * kMostParts + p.ldg / CW::BQ);
   if (tl > kMaxTiles || most > kMaxTiles || a.M * chunks > kMaxTiles)
     return hipErrorInvalidConfiguration;
   const dim3 grid = tile_grid(most, per_cu);
