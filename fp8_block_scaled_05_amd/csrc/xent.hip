@@ -66,16 +66,6 @@ dim3 tile_grid(int64_t tiles, int64_t per_cu = 1) {
   return dim3((unsigned)(tiles < most ? tiles : most));
 }
 
-// Whether a head's logits take the small tiles: by the estimated rounds of
-// workgroups, a round of 256x256 and of 128x64 tiles taking 100 and kSmallCost
-// (100 x 10000 x 2048: 37 us large, 24 small; 256 x 32003 x 2048: 53 and 81).
-constexpr int64_t kSmallCost = 35;
-bool small_logits(int64_t M, int64_t V) {
-  const int64_t cus = compute_units();
-  return kSmallCost * cdiv(cdiv(M, LogitsSmall::BQ) * cdiv(V, LogitsSmall::BP), cus) <
-         100 * cdiv(cdiv(M, LogitsCfg::BQ) * cdiv(V, LogitsCfg::BP), cus);
-}
-
 // What the row pass leaves for the others.
 struct Header {
   int32_t rows;     // rows with a loss
@@ -602,7 +592,8 @@ __device__ __forceinline__ void add_dx(const GradArgs& a, int64_t rows, bool fir
     if (q >= rows) continue;
 #pragma unroll
     for (int i = 0; i < C::FP; ++i) {
-      v4f* d = reinterpret_cast<v4f*>(out + q * a.K + pw + gemm16::p_lane<C>(g) + gemm16::p_tile<C>(i));
+      v4f* d = reinterpret_cast<v4f*>(out + q * a.K + pw + gemm16::p_lane<C>(g) +
+                                      gemm16::p_tile<C>(i));
       *d = first ? acc[i][j] : *d + acc[i][j];
     }
   }
@@ -718,11 +709,13 @@ __global__ __launch_bounds__(CX::THREADS, 2) void xent_grad_kernel(GradArgs a, i
   FP8BS_GEMM16_STAGES(CX);
   const int64_t rows = a.r.h->rows;
   const uint32_t w = blockIdx.x, G = gridDim.x;
-  const uint32_t PT = (uint32_t)((a.K + CX::BP - 1) / CX::BP), QX = (uint32_t)((rows + CX::BQ - 1) / CX::BQ);
+  const uint32_t PT = (uint32_t)((a.K + CX::BP - 1) / CX::BP);
+  const uint32_t QX = (uint32_t)((rows + CX::BQ - 1) / CX::BQ);
   // k-steps in pairs; G is zero past the vocabulary, up to whole tiles
   const uint32_t pairs = (uint32_t)((a.nv + 2 * kStep - 1) / (2 * kStep));
   // by the full piece, the same for all: a shorter last piece may use fewer
-  const uint32_t whole = dx_splits<part_cost<CX>()>(a, rows, PT * QX, PT * (uint32_t)(a.ldg / CW::BQ), G);
+  const uint32_t whole =
+      dx_splits<part_cost<CX>()>(a, rows, PT * QX, PT * (uint32_t)(a.ldg / CW::BQ), G);
   const uint32_t splits = whole < pairs ? whole : pairs;
   const uint32_t NX = PT * QX * splits;
   {
@@ -846,6 +839,17 @@ Rows take_rows(Carver& c, int64_t M, bool grad) {
   return r;
 }
 
+// Whether a head's logits take the small tiles: by the estimated rounds of
+// workgroups, a round of 256x256 tiles taking 100, of their halves (see half_rows)
+// 75, of 128x64 tiles 38 and the first 10 more (loss of 100 x 10000 x 2048: 37 us
+// large, 24 small; 100 x 32003 x 2048: 40 and 51; 256 x 32003 x 2048: 53 and 81).
+bool small_logits(int64_t M, int64_t V, int64_t K) {
+  const int64_t cus = compute_units();
+  const bool half = M <= LogitsHalf::BQ && 2 * V * K <= kCachedBytes;
+  return 10 + 38 * cdiv(cdiv(M, LogitsSmall::BQ) * cdiv(V, LogitsSmall::BP), cus) <
+         (half ? 75 : 100) * cdiv(cdiv(M, LogitsCfg::BQ) * cdiv(V, LogitsCfg::BP), cus);
+}
+
 struct LossPlan {
   Rows r;
   uint16_t* xc;
@@ -860,7 +864,7 @@ LossPlan loss_plan(void* ws, int64_t M, int64_t V, int64_t K) {
   Carver c{static_cast<uint8_t*>(ws)};
   LossPlan p{};
   const bool few = M <= kFewXentRows;
-  p.small = few || small_logits(M, V);
+  p.small = few || small_logits(M, V, K);
   // half tiles have narrower waves than large ones
   p.blocks = p.small ? cdiv(V, LogitsSmall::TP) : cdiv(V, LogitsHalf::TP);
   p.part = c.take<float2>(M * p.blocks);
@@ -903,7 +907,7 @@ GradPlan grad_plan(void* ws, int64_t M, int64_t V, int64_t K) {
   p.pieces = cdiv(V, most);
   p.ldg = cdiv(cdiv(V, p.pieces), kTile) * kTile;
   p.pieces = cdiv(V, p.ldg);
-  p.small_logits = small_logits(M, p.ldg);
+  p.small_logits = small_logits(M, p.ldg, K);
   // Small tiles where dw has too few large ones to go round (1000 x 4096 x 1024, 64
   // of them: 67 us large, 57 small; 1000 x 6144 x 1024, 96: 75 and 79) or dx so
   // few that its parts cannot either (130 x 129280 x 512, 2: 184 and 152; 400 x
