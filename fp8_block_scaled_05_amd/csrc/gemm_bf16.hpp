@@ -305,6 +305,12 @@ struct Job {
 // last tile its own first steps are copied again, unused.  The loop over a
 // tile's steps is one body without a peeled end: with one, the compiler moves
 // the accumulators between the copies of the step, and spills.
+//
+// Steps taken (rebuilt logits, 4096 x 32512 x 7168): fragments read at the row
+// that uses them and a barrier between steps 1.85 ms; read D rows ahead 1.46;
+// copies one per row and tiles in rounds 1.39; the stream over the tiles 1.35.
+// Four stages of half the k measured slower (twice the L2 requests: loss of 4096
+// x 129280 x 7168 5.7 ms against 5.3).
 template <class C, class JobF, class DoneF>
 __device__ __forceinline__ void run_tiles(int n, uint8_t* const (&stages)[4], JobF&& job_of,
                                           DoneF&& done) {
