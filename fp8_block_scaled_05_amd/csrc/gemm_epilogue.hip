@@ -158,6 +158,20 @@ struct LinearEpilogue {
   }
 };
 
+// Tiles of a bf16 output whose 64x64 tiles are at most three per compute unit
+// (an E4M3 output needs whole 128-column tiles): the K loop of such a launch is
+// latency, and smaller tiles in more workgroups have more loads in flight.  us,
+// with bias, silu, residual and z:
+//                        128x256  64x128  64x64  32x64
+//    200 x 1000 x 512              10.6    7.4    5.9
+//    128 x 4096 x 7168             27.0   19.5   21.3   (128 tiles of 64x64)
+//    333 x 2050 x 2048             15.6   11.5   10.9
+//    300 x 2048 x 4096             19.8   14.4   17.2   (160)
+//    700 x 4096 x 2048     30.4           21.9          (704)
+//   1000 x 4096 x 7168     63.2           72.6          (1024)
+using SmallCfg = gemm::Cfg<64, 64, 2, 2, 4, 1>;
+using TinyCfg = gemm::Cfg<32, 64, 2, 2, 4, 1>;
+
 template <class C, class TAIL = C>
 hipError_t launch_tiles(const GemmArgs& a, const LinearEpilogue& ep, OutKind out,
                         hipStream_t stream) {
@@ -166,11 +180,17 @@ hipError_t launch_tiles(const GemmArgs& a, const LinearEpilogue& ep, OutKind out
   if (blocks == 0) return hipSuccess;
   if (blocks < 0) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)blocks), block(C::THREADS);
-  if (out == kOutBF16)
-    return launch_kernel(gemm::block_gemm_epilogue_kernel<C, TAIL, kOutBF16, LinearEpilogue>, grid,
-                         block, stream, a, full, ep);
-  return launch_kernel(gemm::block_gemm_epilogue_kernel<C, TAIL, kOutE4M3, LinearEpilogue>, grid,
-                       block, stream, a, full, ep);
+  if constexpr (C::BN % 128 == 0) {
+    if (out == kOutE4M3)
+      return launch_kernel(gemm::block_gemm_epilogue_kernel<C, TAIL, kOutE4M3, LinearEpilogue>,
+                           grid, block, stream, a, full, ep);
+  }
+  if constexpr (C::BN != gemm::Rows64Cfg::BN) {
+    if (out == kOutBF16)
+      return launch_kernel(gemm::block_gemm_epilogue_kernel<C, TAIL, kOutBF16, LinearEpilogue>,
+                           grid, block, stream, a, full, ep);
+  }
+  return hipErrorInvalidConfiguration;
 }
 
 }  // namespace
@@ -178,9 +198,18 @@ hipError_t launch_tiles(const GemmArgs& a, const LinearEpilogue& ep, OutKind out
 hipError_t launch_block_gemm_epilogue(const GemmArgs& args, const Epilogue& e, OutKind out,
                                       hipStream_t stream) {
   const LinearEpilogue ep{e};
-  if (args.M <= 64) return launch_tiles<gemm::Rows64Cfg>(args, ep, out, stream);
+  if (out == kOutBF16) {
+    const int64_t cus = gemm::device_cus() > 0 ? gemm::device_cus() : 256;
+    const int64_t tiles = ((args.M + 63) / 64) * ((args.N + 63) / 64);
+    if (2 * tiles <= cus) return launch_tiles<TinyCfg>(args, ep, out, stream);
+    if (tiles <= 3 * cus) return launch_tiles<SmallCfg>(args, ep, out, stream);
+  }
+  if (args.M <= 64 && out == kOutE4M3)
+    return launch_tiles<gemm::Rows64Cfg>(args, ep, out, stream);
   switch (gemm::pick_tiles(args)) {
-    case gemm::Tiles::kSmall: return launch_tiles<gemm::Rows64Cfg>(args, ep, out, stream);
+    case gemm::Tiles::kSmall:
+      return out == kOutBF16 ? launch_tiles<SmallCfg>(args, ep, out, stream)
+                             : launch_tiles<gemm::Rows64Cfg>(args, ep, out, stream);
     case gemm::Tiles::kHalf: return launch_tiles<gemm::LargeTail>(args, ep, out, stream);
     default: return launch_tiles<gemm::LargeCfg, gemm::LargeTail>(args, ep, out, stream);
   }
