@@ -200,7 +200,8 @@ hipError_t launch_epilogue_backward(const uint16_t* dy, int64_t lddy, const uint
                                     hipStream_t stream) {
   const int64_t MB = (M + 127) / 128, blocks = MB * (N / 128);
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  float* part = static_cast<float*>(workspace);
+  // one block of rows: its sums are dbias
+  float* part = MB == 1 ? dbias : static_cast<float*>(workspace);
   const BackwardArgs a{dy, lddy, z, ldz, M, N / 128, q, ldq, s, lds, qt, ldqt, st, ldst, part};
   const dim3 grid((unsigned)blocks), block(256);
   hipError_t e;
@@ -217,7 +218,7 @@ hipError_t launch_epilogue_backward(const uint16_t* dy, int64_t lddy, const uint
     default:
       e = launch_kernel(epilogue_backward_kernel<kActNone>, grid, block, stream, a);
   }
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || MB == 1) return e;
   return launch_kernel(epilogue_bias_kernel, dim3((unsigned)(N / 64)), dim3(256), stream,
                        static_cast<const float*>(part), MB, N, dbias);
 }

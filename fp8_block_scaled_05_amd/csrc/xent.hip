@@ -40,6 +40,7 @@ using gemm16::Operand;
 // (deep stream).
 using LogitsCfg = gemm16::Cfg<256, 256, 2, 4, 2, kRow, kRow>;
 using LogitsHalf = gemm16::Cfg<256, 128, 4, 2, 2, kRow, kRow>;
+using LogitsQuarter = gemm16::Cfg<128, 128, 2, 4, 2, kRow, kRow>;  // see logits_tiles
 using LogitsSmall = gemm16::Cfg<128, 64, 4, 1, 4, kRow, kRow>;
 // dx: q rows, p hidden, k vocabulary.  dw: q vocabulary, p hidden, k rows.
 // Large, and small (two workgroups per compute unit).
@@ -396,8 +397,8 @@ __device__ __forceinline__ void logits_tiles(const uint16_t* x, int64_t ldx, int
     const uint32_t w0 = blockIdx.x, G = gridDim.x;
     auto run = [&](auto c, uint32_t id, uint32_t qt, int64_t first_q) {
       using T = decltype(c);
-      const uint32_t n = PT * qt;
-      auto at = [&](int i) { return raster(in_rounds(id + (uint32_t)i * G, n), PT, qt); };
+      const uint32_t pt = (uint32_t)((V + T::BP - 1) / T::BP), n = pt * qt;
+      auto at = [&](int i) { return raster(in_rounds(id + (uint32_t)i * G, n), pt, qt); };
       gemm16::run_tiles<T>(
           share(n, id, G), stages,
           [&](int i) {
@@ -413,7 +414,14 @@ __device__ __forceinline__ void logits_tiles(const uint16_t* x, int64_t ldx, int
     run(C{}, w0, full, 0);
     if (half) {
       const uint32_t taken = PT * full % G;
-      run(LogitsHalf{}, w0 >= taken ? w0 - taken : w0 + G - taken, 1, rows - half);
+      const uint32_t id = w0 >= taken ? w0 - taken : w0 + G - taken;
+      // at most half a round of them is cut once more (613 x 32003 x 2048: 90 us
+      // with halves, 85 so); both have pairs of 64 columns
+      static_assert(LogitsQuarter::TP == LogitsHalf::TP, "pairs");
+      if (2 * PT <= G)
+        run(LogitsQuarter{}, id, 1, rows - half);
+      else
+        run(LogitsHalf{}, id, 1, rows - half);
     }
   }
 }
@@ -423,8 +431,7 @@ __device__ __forceinline__ void logits_tiles(const uint16_t* x, int64_t ldx, int
 // Many rows: MFMA-bound, in fact by the clock that the board's power allows.
 // 4096 x 129280 x 7168: 5.3 ms, 1.43 PFLOP/s, MFMA pipe busy 0.78 of the cycles
 // (the library's product alone, which stores the logits: 5.28 ms).  613 x 32003
-// x 2048: 85 us, 0.94 PFLOP/s, one round of large tiles and half a round of half
-// ones.  One row: the stream of w, 325 us for 1.85 GB, 5.7 TB/s, read once.
+// x 2048: 79 us, 1.02 PFLOP/s, one round of large tiles and one of quarters.  One row: the stream of w, 325 us for 1.85 GB, 5.7 TB/s, read once.
 template <class C, bool FEW>
 __global__ __launch_bounds__(C::THREADS) void xent_loss_kernel(LossArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)

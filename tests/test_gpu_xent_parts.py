@@ -17,6 +17,8 @@ pytestmark = pytest.mark.gpu
     (250, 70001, 256, 0.0), (1000, 70001, 256, 0.3), (60, 70001, 128, 0.0),
     # parts that do not divide the contraction; dw tiles fewer than workgroups
     (1030, 6100, 1024, 0.0), (1000, 4100, 1152, 0.5), (2050, 20003, 512, 0.1),
+    # two rounds of large tiles for the logits but for the last rows
+    (613, 32003, 128, 0.0), (1531, 32003, 256, 0.6),
 ])
 def test_parts(fp8bs, M, V, K, ignored):  # noqa: F811
     x, w, t = make(M, V, K, M + V + K, ignored)
@@ -41,3 +43,18 @@ def test_parts(fp8bs, M, V, K, ignored):  # noqa: F811
     # the same call again gives the same bits
     again = fp8bs.bf16_linear_xent_backward(x, w, t, lse, d)
     assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
+
+
+# the last rows' tiles cut in four (two rows of large tiles, 1, 101 and 128 rows
+# more), an uncut last tile (129), and a vocabulary that ends inside each
+@pytest.mark.parametrize("M", [513, 613, 640, 641])
+@pytest.mark.parametrize("V", [32003, 32640, 30721])
+def test_forward_last_rows(fp8bs, M, V):  # noqa: F811
+    x, w, t = make(M, V, 128, M + V, 0.0)
+    loss, lse = fp8bs.bf16_linear_xent(x, w, t)
+    rows, _, _, l, err = logits(x, w, t)
+    want_lse = torch.logsumexp(l, dim=1)
+    want = want_lse - l[torch.arange(M, device="cuda"), t]
+    tol = err + 6e-5 + 2 * U * want_lse.abs()
+    assert torch.all((lse.double() - want_lse).abs() <= tol)
+    assert torch.all((loss.double() - want).abs() <= 2 * tol)
