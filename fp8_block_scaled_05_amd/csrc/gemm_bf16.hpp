@@ -37,6 +37,7 @@ using gemm::lds_swizzle;
 enum Layout { kRow = 0, kCol = 1 };
 
 constexpr int kStep = 64;  // k per LDS stage
+constexpr int kNonTemporal = 2;  // cache policy bit of a buffer load
 
 template <int BP_, int BQ_, int WP_, int WQ_, int STAGES_, int LP_, int LQ_>
 struct Cfg {
@@ -58,6 +59,14 @@ struct Cfg {
   static_assert(LP == kRow || BP >= 128, "swizzle of the k-major stage");
   static_assert(LQ == kRow || BQ >= 128, "swizzle of the k-major stage");
   static_assert(STAGES * STAGE_BYTES <= 160 * 1024, "LDS budget");
+  static constexpr bool STREAM_P = false;
+};
+
+// The same with P read past the caches: for a P that is read once and would not
+// stay in them.
+template <class C>
+struct Streamed : C {
+  static constexpr bool STREAM_P = true;
 };
 
 // One operand of a tile.  base: the tile's first row (kRow) or its first
@@ -204,9 +213,11 @@ struct Copier {
     } else {
       v = at[c];
     }
-    const __amdgpu_buffer_rsrc_t rs = gemm::make_rsrc(base + (uint64_t)(uint32_t)first * (COL ? ld : 2u));
+    const __amdgpu_buffer_rsrc_t rs =
+        gemm::make_rsrc(base + (uint64_t)(uint32_t)first * (COL ? ld : 2u));
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        rs, (gemm::lds_void*)(st + lds + c * C::NWAVES * 1024), 16, v, 0, 0, 0);
+        rs, (gemm::lds_void*)(st + lds + c * C::NWAVES * 1024), 16, v, 0, 0,
+        IS_P && C::STREAM_P ? kNonTemporal : 0);
 #endif
   }
 };

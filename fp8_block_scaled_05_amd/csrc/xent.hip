@@ -42,6 +42,9 @@ using LogitsCfg = gemm16::Cfg<256, 256, 2, 4, 2, kRow, kRow>;
 using LogitsHalf = gemm16::Cfg<256, 128, 4, 2, 2, kRow, kRow>;
 using LogitsQuarter = gemm16::Cfg<128, 128, 2, 4, 2, kRow, kRow>;  // see logits_tiles
 using LogitsSmall = gemm16::Cfg<128, 64, 4, 1, 4, kRow, kRow>;
+// Up to 16 rows, two workgroups per compute unit: copies no rows of x that do not
+// exist, and so has more of w in flight (1 x 129280 x 7168: 326 us small, 304 so).
+using LogitsToken = gemm16::Cfg<128, 16, 2, 1, 3, kRow, kRow>;
 // dx: q rows, p hidden, k vocabulary.  dw: q vocabulary, p hidden, k rows.
 // Large, and small (two workgroups per compute unit).
 using DxCfg = gemm16::Cfg<256, 256, 2, 4, 2, kCol, kRow>;
@@ -431,7 +434,8 @@ __device__ __forceinline__ void logits_tiles(const uint16_t* x, int64_t ldx, int
 // Many rows: MFMA-bound, in fact by the clock that the board's power allows.
 // 4096 x 129280 x 7168: 5.3 ms, 1.43 PFLOP/s, MFMA pipe busy 0.78 of the cycles
 // (the library's product alone, which stores the logits: 5.28 ms).  613 x 32003
-// x 2048: 79 us, 1.02 PFLOP/s, one round of large tiles and one of quarters.  One row: the stream of w, 325 us for 1.85 GB, 5.7 TB/s, read once.
+// x 2048: 79 us, 1.02 PFLOP/s, one round of large tiles and one of quarters.  One
+// row: the stream of w, 265 us for 1.85 GB, 7.0 TB/s, read once.
 template <class C, bool FEW>
 __global__ __launch_bounds__(C::THREADS) void xent_loss_kernel(LossArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -632,7 +636,8 @@ __device__ __forceinline__ void transpose_lane_rows(uint32_t (&v)[4]) {
 
 // A tile of a piece's dw.  Lane row g holds columns 4 g .. + 3 of every MFMA
 // tile; transposed over four tiles it holds the 16 columns of tile g, and a row
-// of w is stored in whole 128-byte lines.
+// of dw is stored in whole 128-byte lines, past the caches (613 x 32003 x 2048: 273
+// us through them, 254 past them).
 template <class C>
 __device__ __forceinline__ void store_dw(const GradArgs& a, int64_t p0, int64_t q0,
                                          const gemm16::Acc<C>& acc) {
@@ -659,8 +664,8 @@ __device__ __forceinline__ void store_dw(const GradArgs& a, int64_t p0, int64_t 
       transpose_lane_rows(hi);
       if (q < a.nv) {
         u32x4* d = reinterpret_cast<u32x4*>(row + 16 * i0);
-        d[0] = u32x4{lo[0], hi[0], lo[1], hi[1]};
-        d[1] = u32x4{lo[2], hi[2], lo[3], hi[3]};
+        __builtin_nontemporal_store(u32x4{lo[0], hi[0], lo[1], hi[1]}, d);
+        __builtin_nontemporal_store(u32x4{lo[2], hi[2], lo[3], hi[3]}, d + 1);
       }
     }
     __builtin_amdgcn_sched_barrier(0);  // one j at a time: few registers beside the sums
@@ -947,6 +952,25 @@ GradPlan grad_plan(void* ws, int64_t M, int64_t V, int64_t K) {
   return p;
 }
 
+// The forward call of few rows, one tile of q.  A w that cannot stay in the
+// last-level cache until it is read again is read past it (1 x 129280 x 7168: 304
+// us through the caches, 268 past them; 1 x 20000 x 4096, which stays: 31 and 48).
+constexpr int64_t kStreamBytes = int64_t(256) << 20;
+template <class C>
+hipError_t launch_few(const LossArgs& a, int64_t ignore, float* loss, float* lse,
+                      hipStream_t stream) {
+  const int64_t tiles = cdiv(a.V, C::BP);
+  if (tiles > kMaxTiles) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)tiles), block(C::THREADS);
+  const hipError_t e =
+      2 * a.V * a.K > kStreamBytes
+          ? launch_kernel(xent_loss_kernel<gemm16::Streamed<C>, true>, grid, block, stream, a)
+          : launch_kernel(xent_loss_kernel<C, true>, grid, block, stream, a);
+  if (e != hipSuccess) return e;
+  return launch_kernel(xent_join_kernel<true>, dim3((unsigned)a.M), dim3(256), stream, a, 0u,
+                       C::TP, C::TP, ignore, loss, lse);
+}
+
 }  // namespace
 
 size_t xent_workspace(int64_t M, int64_t V, int64_t K) { return loss_plan(nullptr, M, V, K).bytes; }
@@ -960,18 +984,13 @@ hipError_t launch_xent(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_
   const LossPlan p = loss_plan(workspace, M, V, K);
   const LossArgs a{x, ldx, p.xc, w, ldw, M, V, K, p.r, target, p.part, p.blocks, p.at};
   const dim3 block(LogitsSmall::THREADS), large(LogitsCfg::THREADS);
+  if (M <= LogitsToken::BQ) return launch_few<LogitsToken>(a, ignore, loss, lse, stream);
+  if (M <= kFewXentRows) return launch_few<LogitsSmall>(a, ignore, loss, lse, stream);
   const int64_t tiles = p.small ? cdiv(V, LogitsSmall::BP) * cdiv(M, LogitsSmall::BQ)
                                 : cdiv(V, LogitsCfg::BP) * cdiv(M, LogitsCfg::BQ);
   if (tiles > kMaxTiles) return hipErrorInvalidConfiguration;
-  hipError_t e;
-  if (M <= kFewXentRows) {
-    e = launch_kernel(xent_loss_kernel<LogitsSmall, true>, dim3((unsigned)tiles), block, stream, a);
-    if (e != hipSuccess) return e;
-    return launch_kernel(xent_join_kernel<true>, dim3((unsigned)M), dim3(256), stream, a, 0u,
-                         LogitsSmall::TP, LogitsSmall::TP, ignore, loss, lse);
-  }
-  e = launch_rows({target, M, V, ignore, p.r, nullptr, nullptr, loss, lse, x, ldx, K, p.xc,
-                   nullptr}, stream);
+  hipError_t e = launch_rows({target, M, V, ignore, p.r, nullptr, nullptr, loss, lse, x, ldx, K,
+                              p.xc, nullptr}, stream);
   if (e != hipSuccess) return e;
   e = p.small ? launch_kernel(xent_loss_kernel<LogitsSmall, false>, dim3((unsigned)tiles), block,
                               stream, a)
