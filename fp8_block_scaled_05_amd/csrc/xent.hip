@@ -45,6 +45,12 @@ using LogitsSmall = gemm16::Cfg<128, 64, 4, 1, 4, kRow, kRow>;
 // Up to 16 rows, two workgroups per compute unit: copies no rows of x that do not
 // exist, and so has more of w in flight (1 x 129280 x 7168: 326 us small, 304 so).
 using LogitsToken = gemm16::Cfg<128, 16, 2, 1, 3, kRow, kRow>;
+// Both at half the width, for heads whose 64x64 tiles fit one round of workgroups:
+// a step of fewer copies is shorter (55 x 1615 x 4736: 29 us small, 20 so; 20 x
+// 7889 x 4352: 33 and 25; with 395 such tiles, 300 x 5000 x 4096: 41 and 48).
+using LogitsNarrow = gemm16::Cfg<64, 64, 2, 2, 4, kRow, kRow>;
+using LogitsTokenNarrow = gemm16::Cfg<64, 16, 2, 1, 4, kRow, kRow>;
+static_assert(LogitsNarrow::TP == LogitsSmall::TP, "pairs");
 // dx: q rows, p hidden, k vocabulary.  dw: q vocabulary, p hidden, k rows.
 // Large, and small (two workgroups per compute unit).
 using DxCfg = gemm16::Cfg<256, 256, 2, 4, 2, kCol, kRow>;
@@ -60,6 +66,12 @@ constexpr int64_t kPad = 2 * kStep;  // k-steps come in pairs
 constexpr int64_t kFewXentRows = LogitsSmall::BQ;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Tiles of V columns: whole kPad columns, since dx's k-steps read G up to there.
+template <class C>
+__host__ __device__ constexpr int64_t tiles_of(int64_t V) {
+  return C::BP < kPad ? (V + kPad - 1) / kPad * (kPad / C::BP) : (V + C::BP - 1) / C::BP;
+}
 
 int64_t compute_units() { return gemm::device_cus() > 0 ? gemm::device_cus() : 256; }
 
@@ -378,7 +390,7 @@ template <class C, class F>
 __device__ __forceinline__ void logits_tiles(const uint16_t* x, int64_t ldx, int64_t rows,
                                              const uint16_t* w, int64_t ldw, int64_t V, int64_t K,
                                              uint32_t QT, uint8_t* const (&stages)[4], F&& done) {
-  const uint32_t PT = (uint32_t)((V + C::BP - 1) / C::BP);
+  const uint32_t PT = (uint32_t)tiles_of<C>(V);
   auto job = [&](auto c, int64_t p0, int64_t q0) {
     using T = decltype(c);
     return gemm16::Job{{w + p0 * ldw, ld2(ldw), (int)(V - p0 < T::BP ? V - p0 : T::BP), 0},
@@ -391,7 +403,7 @@ __device__ __forceinline__ void logits_tiles(const uint16_t* x, int64_t ldx, int
     const int64_t p0 = (int64_t)t.p * C::BP, q0 = (int64_t)t.q * C::BQ;
     gemm16::Acc<C> acc;
     gemm16::clear<C>(acc);
-    if (q0 < rows) {  // otherwise padding: zeros in any case
+    if (q0 < rows && p0 < V) {  // otherwise padding: zeros in any case
       const gemm16::Job j = job(C{}, p0, q0);
       gemm16::product_deep<C>(j.p, j.q, j.steps, stages, acc);
     }
@@ -875,6 +887,11 @@ bool small_logits(int64_t M, int64_t V, int64_t K) {
          (half ? 75 : 100) * cdiv(cdiv(M, LogitsCfg::BQ) * cdiv(V, LogitsCfg::BP), cus);
 }
 
+// Whether its small tiles are the narrow ones.
+bool narrow_logits(int64_t M, int64_t V) {
+  return cdiv(M, LogitsNarrow::BQ) * cdiv(V, LogitsNarrow::BP) <= compute_units();
+}
+
 struct LossPlan {
   Rows r;
   uint16_t* xc;
@@ -959,7 +976,7 @@ constexpr int64_t kStreamBytes = int64_t(256) << 20;
 template <class C>
 hipError_t launch_few(const LossArgs& a, int64_t ignore, float* loss, float* lse,
                       hipStream_t stream) {
-  const int64_t tiles = cdiv(a.V, C::BP);
+  const int64_t tiles = tiles_of<C>(a.V);
   if (tiles > kMaxTiles) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)tiles), block(C::THREADS);
   const hipError_t e =
@@ -984,18 +1001,26 @@ hipError_t launch_xent(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_
   const LossPlan p = loss_plan(workspace, M, V, K);
   const LossArgs a{x, ldx, p.xc, w, ldw, M, V, K, p.r, target, p.part, p.blocks, p.at};
   const dim3 block(LogitsSmall::THREADS), large(LogitsCfg::THREADS);
-  if (M <= LogitsToken::BQ) return launch_few<LogitsToken>(a, ignore, loss, lse, stream);
-  if (M <= kFewXentRows) return launch_few<LogitsSmall>(a, ignore, loss, lse, stream);
-  const int64_t tiles = p.small ? cdiv(V, LogitsSmall::BP) * cdiv(M, LogitsSmall::BQ)
-                                : cdiv(V, LogitsCfg::BP) * cdiv(M, LogitsCfg::BQ);
+  const bool narrow = narrow_logits(M, V);
+  if (M <= LogitsToken::BQ)
+    return narrow ? launch_few<LogitsTokenNarrow>(a, ignore, loss, lse, stream)
+                  : launch_few<LogitsToken>(a, ignore, loss, lse, stream);
+  if (M <= kFewXentRows)
+    return narrow ? launch_few<LogitsNarrow>(a, ignore, loss, lse, stream)
+                  : launch_few<LogitsSmall>(a, ignore, loss, lse, stream);
+  const int64_t tiles = !p.small ? cdiv(V, LogitsCfg::BP) * cdiv(M, LogitsCfg::BQ)
+                        : narrow ? tiles_of<LogitsNarrow>(V) * cdiv(M, LogitsNarrow::BQ)
+                                 : cdiv(V, LogitsSmall::BP) * cdiv(M, LogitsSmall::BQ);
   if (tiles > kMaxTiles) return hipErrorInvalidConfiguration;
   hipError_t e = launch_rows({target, M, V, ignore, p.r, nullptr, nullptr, loss, lse, x, ldx, K,
                               p.xc, nullptr}, stream);
   if (e != hipSuccess) return e;
-  e = p.small ? launch_kernel(xent_loss_kernel<LogitsSmall, false>, dim3((unsigned)tiles), block,
-                              stream, a)
-              : launch_kernel(xent_loss_kernel<LogitsCfg, false>, tile_grid(tiles), large, stream,
-                              a);
+  e = !p.small ? launch_kernel(xent_loss_kernel<LogitsCfg, false>, tile_grid(tiles), large, stream,
+                               a)
+      : narrow ? launch_kernel(xent_loss_kernel<LogitsNarrow, false>, dim3((unsigned)tiles), block,
+                               stream, a)
+               : launch_kernel(xent_loss_kernel<LogitsSmall, false>, dim3((unsigned)tiles), block,
+                               stream, a);
   if (e != hipSuccess) return e;
   return launch_kernel(xent_join_kernel<false>, dim3((unsigned)cdiv(M, 4)), dim3(256), stream, a,
                        tile_grid(tiles).x, p.small ? LogitsSmall::TP : LogitsCfg::TP,
@@ -1009,8 +1034,12 @@ hipError_t launch_pieces(const GradPlan& p, GradArgs a, int per_cu, uint16_t* dx
                          hipStream_t stream) {
   using CL = LogitsCfg;
   using CS = LogitsSmall;
+  using CN = LogitsNarrow;
+  static_assert(CS::BQ == CN::BQ && CS::THREADS == CN::THREADS, "rows and waves alike");
+  const bool narrow = narrow_logits(a.M, p.ldg);
   const int64_t QL = cdiv(a.M, CL::BQ), QS = cdiv(a.M, kPad) * (kPad / CS::BQ);
-  const int64_t tl = p.small_logits ? QS * (p.ldg / CS::BP) : QL * (p.ldg / CL::BP);
+  const int64_t tl = p.small_logits ? QS * (p.ldg / (narrow ? CN::BP : CS::BP))
+                                    : QL * (p.ldg / CL::BP);
   const int64_t KT = cdiv(a.K, CX::BP), chunks = cdiv(a.K, 1024);
   const int64_t most = KT * (cdiv(a.M, CX::BQ) * kMostParts + p.ldg / CW::BQ);
   if (tl > kMaxTiles || most > kMaxTiles || a.M * chunks > kMaxTiles)
@@ -1022,10 +1051,12 @@ hipError_t launch_pieces(const GradPlan& p, GradArgs a, int per_cu, uint16_t* dx
     a.nv = left < p.ldg ? left : p.ldg;
     hipError_t e = hipSuccess;
     if (a.M > 0)
-      e = p.small_logits ? launch_kernel(xent_grad_logits_kernel<CS>, dim3((unsigned)tl),
-                                         dim3(CS::THREADS), stream, a)
-                         : launch_kernel(xent_grad_logits_kernel<CL>, tile_grid(tl),
-                                         dim3(CL::THREADS), stream, a);
+      e = !p.small_logits ? launch_kernel(xent_grad_logits_kernel<CL>, tile_grid(tl),
+                                          dim3(CL::THREADS), stream, a)
+          : narrow        ? launch_kernel(xent_grad_logits_kernel<CN>, dim3((unsigned)tl),
+                                          dim3(CN::THREADS), stream, a)
+                          : launch_kernel(xent_grad_logits_kernel<CS>, dim3((unsigned)tl),
+                                          dim3(CS::THREADS), stream, a);
     if (e != hipSuccess) return e;
     e = launch_kernel(xent_grad_kernel<CX, CW>, grid, dim3(CX::THREADS), stream, a,
                       i == 0 ? 1 : 0);

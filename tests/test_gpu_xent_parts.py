@@ -58,3 +58,34 @@ def test_forward_last_rows(fp8bs, M, V):  # noqa: F811
     tol = err + 6e-5 + 2 * U * want_lse.abs()
     assert torch.all((lse.double() - want_lse).abs() <= tol)
     assert torch.all((loss.double() - want).abs() <= 2 * tol)
+
+
+# heads whose tiles are the narrow ones, ending inside the first and the second
+# half of a 128-column step of dx; one row to several tiles of them
+@pytest.mark.parametrize("M,K", [(1, 256), (16, 128), (17, 640), (55, 384), (130, 512)])
+@pytest.mark.parametrize("V", [1, 63, 65, 700, 1090, 1615, 3969])
+def test_narrow_tiles(fp8bs, M, V, K):  # noqa: F811
+    x, w, t = make(M, V, K, M + V + K, 0.0)
+    loss, lse = fp8bs.bf16_linear_xent(x, w, t)
+    rows, xs, ws, l, err = logits(x, w, t)
+    want_lse = torch.logsumexp(l, dim=1)
+    want = want_lse - l[torch.arange(M, device="cuda"), t]
+    tol = err + 6e-5 + 2 * U * want_lse.abs()
+    assert torch.all((lse.double() - want_lse).abs() <= tol)
+    assert torch.all((loss.double() - want).abs() <= 2 * tol)
+    d = torch.randn(M, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")
+    # the workspace holds NaN: nothing is read that was not written
+    ws_bytes = fp8bs.workspace_bytes(fp8bs.OP_XENT_BACKWARD, M, V, K)
+    space = torch.full(((ws_bytes + 3) // 4,), float("nan"), device="cuda")
+    dx, dw = fp8bs.bf16_linear_xent_backward(x, w, t, lse, d, workspace=space)
+    G = torch.exp(l - lse.double()[:, None])
+    E = 4 * G * (err + 6e-5)[:, None]
+    G[torch.arange(M, device="cuda"), t] -= 1.0
+    E += G.abs() * (2.0 ** -8 + 2 * max(M, V) * U)
+    dr = d.double()[:, None]
+    want = (dr * G) @ ws
+    assert torch.all((dx.double() - want).abs() <=
+                     (dr.abs() * E) @ ws.abs() + 2.0 ** -8 * want.abs())
+    E = dr.abs() * (E + 2.0 ** -8 * G.abs())
+    want = (dr * G).t() @ xs
+    assert torch.all((dw.double() - want).abs() <= E.t() @ xs.abs() + 2.0 ** -8 * want.abs())
