@@ -444,7 +444,7 @@ __device__ __forceinline__ void logits_tiles(const uint16_t* x, int64_t ldx, int
 // Forward.  FEW: the rows as they are, in one tile of q.
 //
 // Many rows: MFMA-bound, in fact by the clock that the board's power allows.
-// 4096 x 129280 x 7168: 5.3 ms, 1.43 PFLOP/s, MFMA pipe busy 0.78 of the cycles
+// 4096 x 129280 x 7168: 5.3 ms, 1.43 PFLOP/s, MFMA pipe busy 0.77 of the cycles
 // (the library's product alone, which stores the logits: 5.28 ms).  613 x 32003
 // x 2048: 79 us, 1.02 PFLOP/s, one round of large tiles and one of quarters.  One
 // row: the stream of w, 265 us for 1.85 GB, 7.0 TB/s, read once.
@@ -735,7 +735,7 @@ constexpr uint32_t part_cost() {
 //
 // MFMA-bound; both products in one launch, so that neither's last partial round
 // leaves compute units idle.  4096 x 129280 x 7168: 11.1 ms, 1.37 PFLOP/s, MFMA
-// pipe busy 0.73.  613 x 32003 x 2048: 175 us, 0.92 PFLOP/s; dw's tiles have ten
+// pipe busy 0.72.  613 x 32003 x 2048: 172 us, 0.93 PFLOP/s; dw's tiles have ten
 // steps there and end in stores of 131 MB.
 template <class CX, class CW>
 __global__ __launch_bounds__(CX::THREADS, 2) void xent_grad_kernel(GradArgs a, int first) {
