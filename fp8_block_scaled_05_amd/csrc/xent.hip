@@ -462,11 +462,18 @@ __global__ __launch_bounds__(C::THREADS) void xent_loss_kernel(LossArgs a) {
 #endif
 }
 
-// (m, s) += (m2, s2); -inf - -inf: a pair without a sum adds nothing
+// The sum s of a pair with maximum m, taken to the larger maximum `top`.  Equal
+// maxima are not subtracted: of two infinities the difference has no value.  A NaN
+// sum stays NaN, also beside a maximum of -inf (a block of NaN and -inf logits, to
+// which the columns past the vocabulary belong).
+__device__ __forceinline__ float rescaled(float m, float s, float top) {
+  return m == top ? s : s * __builtin_amdgcn_exp2f((m - top) * kLog2e);
+}
+
+// (m, s) += (m2, s2)
 __device__ __forceinline__ void join_pair(float& m, float& s, float m2, float s2) {
   const float top = fmaxf(m, m2);
-  s = (m == -INFINITY ? s : s * __builtin_amdgcn_exp2f((m - top) * kLog2e)) +
-      (m2 == -INFINITY ? s2 : s2 * __builtin_amdgcn_exp2f((m2 - top) * kLog2e));
+  s = rescaled(m, s, top) + rescaled(m2, s2, top);
   m = top;
 }
 
@@ -500,13 +507,12 @@ __global__ __launch_bounds__(256) void xent_join_kernel(LossArgs a, uint32_t G, 
     float top = m;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (b0 + u * STEP >= blocks) v[u].x = -INFINITY;
+      if (b0 + u * STEP >= blocks) v[u] = make_float2(-INFINITY, 0.0f);
       top = fmaxf(top, v[u].x);
     }
-    s = m == -INFINITY ? s : s * __builtin_amdgcn_exp2f((m - top) * kLog2e);
+    s = rescaled(m, s, top);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      s += v[u].x == -INFINITY ? 0.0f : v[u].y * __builtin_amdgcn_exp2f((v[u].x - top) * kLog2e);
+    for (int u = 0; u < U; ++u) s += rescaled(v[u].x, v[u].y, top);
     m = top;
   }
 #pragma unroll

@@ -1,0 +1,89 @@
+"""The head's cross entropy where logits are NaN or infinite: what the formulas
+give, also where such a logit stands alone in the last columns of the vocabulary
+or among -inf, for every tile shape.  Finite results are held to the tolerance
+derived in test_gpu_xent.py."""
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+# one row to 16 (narrow and wide tiles), 64, more (narrow, small), large tiles, and
+# large tiles with their half and quarter ones; V = 1 more than whole blocks of
+# columns, so that the last column is the only one of its block
+SHAPES = [(4, 1), (4, 33), (4, 2049), (4, 40001), (40, 129), (40, 2049), (40, 20097), (70, 65),
+          (70, 2049), (70, 20097), (300, 51073), (600, 30081), (613, 32001)]
+
+
+@pytest.fixture(scope="module")
+def fp8bs():
+    from fp8_block_scaled_05_amd import fp8bs as mod
+    return mod
+
+
+def make(M, V, K=128, seed=0):
+    """x with ones in its first column, so that w's first column adds to every
+    row's logits; every seventh row carries no loss."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(M, K, generator=g, device="cuda").to(torch.bfloat16)
+    w = (torch.randn(V, K, generator=g, device="cuda") * 0.1).to(torch.bfloat16)
+    x[:, 0] = 1.0
+    t = torch.randint(V, (M,), generator=g, device="cuda")
+    t[::7] = -100
+    return x, w, t
+
+
+def check(fp8bs, x, w, t):
+    """lse and loss against the formulas in float64, with NaN and infinities in
+    the same places."""
+    loss, lse = fp8bs.bf16_linear_xent(x, w, t)
+    l = x.double() @ w.double().t()
+    finite = torch.where(torch.isfinite(w), w, torch.zeros_like(w)).double()
+    tol = 2 * x.shape[1] * U * (x.double().abs() @ finite.abs().t()).amax(dim=1) + 6e-5
+    keep = t >= 0
+    zero = torch.zeros(len(t), dtype=torch.float64, device="cuda")
+    want = torch.where(keep, torch.logsumexp(l, dim=1), zero)
+    at = torch.where(keep, l.gather(1, t.clamp_min(0)[:, None])[:, 0], zero)
+    for got, ref, k in ((lse, want, 1), (loss, want - at, 2)):
+        got = got.double()
+        assert torch.equal(torch.isnan(got), torch.isnan(ref))
+        ok = torch.isfinite(ref)
+        assert torch.equal(got[~ok & ~torch.isnan(ref)], ref[~ok & ~torch.isnan(ref)])
+        assert torch.all((got - ref).abs()[ok] <= (k * tol + 2 * U * want.abs())[ok])
+    return lse, keep
+
+
+@pytest.mark.parametrize("M,V", SHAPES)
+def test_nan_in_the_last_column(fp8bs, M, V):
+    x, w, t = make(M, V)
+    w[V - 1, 0] = float("nan")
+    lse, keep = check(fp8bs, x, w, t)
+    assert torch.isnan(lse[keep]).all()
+
+
+@pytest.mark.parametrize("M,V", SHAPES)
+def test_nan_among_minus_infinities(fp8bs, M, V):
+    x, w, t = make(M, V, seed=1)
+    w[V // 2:, 0] = float("-inf")
+    w[V // 2 + (V - V // 2) // 3, 0] = float("nan")
+    lse, keep = check(fp8bs, x, w, t)
+    assert torch.isnan(lse[keep]).all()
+
+
+@pytest.mark.parametrize("M,V", SHAPES)
+def test_all_minus_infinity(fp8bs, M, V):
+    x, w, t = make(M, V, seed=2)
+    w[:, 0] = float("-inf")
+    lse, keep = check(fp8bs, x, w, t)
+    assert torch.all(lse[keep] == float("-inf"))
+
+
+@pytest.mark.parametrize("M,V", SHAPES)
+def test_one_finite_column(fp8bs, M, V):
+    x, w, t = make(M, V, seed=3)
+    w[:V - 1, 0] = float("-inf")
+    t[t >= 0] = V - 1
+    lse, keep = check(fp8bs, x, w, t)
+    assert torch.isfinite(lse).all()
