@@ -295,6 +295,9 @@ struct LossArgs {
   float* at;              // logit of each row's target
 };
 
+// Magnitude past which a finite logit times log2 e may leave FP32's range.
+constexpr float kFar = 0x1p126f;
+
 // A tile's logits -> its rows' pairs over each wave's TP columns, and the
 // targets' logits.
 template <class C, bool FEW>
@@ -329,17 +332,6 @@ __device__ __forceinline__ void reduce_logits(const LossArgs& a, int64_t rows, i
       for (int r = 0; r < 4; ++r) m = fmaxf(m, acc[i][j][r]);
     m = fmaxf(m, __shfl_xor(m, 16, 64));
     m = fmaxf(m, __shfl_xor(m, 32, 64));
-    // a block of -inf logits alone has no sum
-    const float b = m == -INFINITY ? 0.0f : -m * kLog2e;
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < C::FP; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, b));
-    s += __shfl_xor(s, 16, 64);
-    s += __shfl_xor(s, 32, 64);
-    if (real && g == 0) a.part[q * a.blocks + pw / C::TP] = make_float2(m, s);
     // the target's logit, on the one lane that holds it
     int64_t t = -1;
     if (real) t = FEW ? a.target[q] : (int64_t)a.r.target[q];
@@ -358,6 +350,29 @@ __device__ __forceinline__ void reduce_logits(const LossArgs& a, int64_t rows, i
         }
       if (here) a.at[q] = at;
     }
+    // l - m with log2 e folded in is one FMA.  A block of -inf logits alone has no
+    // sum; beside a maximum past kFar the fold would overflow, and of two infinities
+    // the difference has no value, so there the sums become the differences first
+    const bool far = fabsf(m) > kFar && m != -INFINITY;
+    if (__any(far)) {
+#pragma unroll
+      for (int i = 0; i < C::FP; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float l = acc[i][j][r];
+          acc[i][j][r] = !far ? l : l == m ? 0.0f : l - m;
+        }
+    }
+    const float b = far || m == -INFINITY ? 0.0f : -m * kLog2e;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < C::FP; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, b));
+    s += __shfl_xor(s, 16, 64);
+    s += __shfl_xor(s, 32, 64);
+    if (real && g == 0) a.part[q * a.blocks + pw / C::TP] = make_float2(m, s);
     __builtin_amdgcn_sched_barrier(0);  // one j at a time: few registers beside the sums
   }
 }
@@ -554,7 +569,7 @@ struct GradArgs {
 // are zeros up to whole tiles.
 template <class C>
 __device__ __forceinline__ void store_g(const GradArgs& a, int64_t rows, int64_t p0, int64_t q0,
-                                        const gemm16::Acc<C>& acc) {
+                                        gemm16::Acc<C>& acc) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
   const int wp = wave / C::WQ, wq = wave % C::WQ;
@@ -567,7 +582,15 @@ __device__ __forceinline__ void store_g(const GradArgs& a, int64_t rows, int64_t
   for (int j = 0; j < C::FQ; ++j) {
     const int64_t q = q0 + wq * C::TQ + 16 * j + l16;
     const bool real = q < rows;
-    const float b = real ? -a.r.lse[q] * kLog2e : 0.0f;
+    const float lse = real ? a.r.lse[q] : 0.0f;
+    const bool far = fabsf(lse) > kFar;  // see reduce_logits
+    if (__any(far)) {
+#pragma unroll
+      for (int i = 0; i < C::FP; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][j][r] -= far ? lse : 0.0f;
+    }
+    const float b = far ? 0.0f : -lse * kLog2e;
     const int64_t tp = real ? (int64_t)a.r.target[q] - (a.v0 + pw) : -1;
     const int t = tp >= 0 && tp < C::TP ? (int)tp - pl : -1;
     const int last = real ? n : -C::TP;  // a row past the last: zeros
@@ -607,7 +630,7 @@ __global__ __launch_bounds__(C::THREADS) void xent_grad_logits_kernel(GradArgs a
   const int64_t padded = (rows + kPad - 1) / kPad * kPad;
   logits_tiles<C>(rows == a.M ? a.x : a.xc, rows == a.M ? a.ldx : a.K, rows, a.w + a.v0 * a.ldw,
                   a.ldw, a.nv, a.K, (uint32_t)((padded + C::BQ - 1) / C::BQ), stages,
-                  [&](auto c, int64_t p0, int64_t q0, const gemm16::Acc<decltype(c)>& acc) {
+                  [&](auto c, int64_t p0, int64_t q0, gemm16::Acc<decltype(c)>& acc) {
                     store_g<decltype(c)>(a, rows, p0, q0, acc);
                   });
 #endif

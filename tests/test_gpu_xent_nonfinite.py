@@ -49,6 +49,8 @@ def check(fp8bs, x, w, t):
     for got, ref, k in ((lse, want, 1), (loss, want - at, 2)):
         got = got.double()
         assert torch.equal(torch.isnan(got), torch.isnan(ref))
+        # a loss past FP32's range is infinite there
+        ref = torch.where(torch.isinf(ref.float()), ref.float().double(), ref)
         ok = torch.isfinite(ref)
         assert torch.equal(got[~ok & ~torch.isnan(ref)], ref[~ok & ~torch.isnan(ref)])
         assert torch.all((got - ref).abs()[ok] <= (k * tol + 2 * U * want.abs())[ok])
@@ -87,3 +89,40 @@ def test_one_finite_column(fp8bs, M, V):
     t[t >= 0] = V - 1
     lse, keep = check(fp8bs, x, w, t)
     assert torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("where", ["first", "last", "both"])
+@pytest.mark.parametrize("M,V", SHAPES)
+def test_plus_infinity(fp8bs, M, V, where):
+    """lse is +inf and so is the loss, but for a target whose own logit is."""
+    x, w, t = make(M, V, seed=4)
+    if where != "last":
+        w[0, 0] = float("inf")
+    if where != "first":
+        w[V - 1, 0] = float("inf")
+    lse, keep = check(fp8bs, x, w, t)
+    assert torch.all(lse[keep] == float("inf"))
+
+
+@pytest.mark.parametrize("top", [2.6e38, -2.6e38])
+@pytest.mark.parametrize("M,V", SHAPES)
+def test_logits_at_the_end_of_the_range(fp8bs, M, V, top):
+    """Logits whose product with log2 e is past FP32's range.  w's first column
+    alone is not zero, so logits are exact and the gradients are 0 or as many
+    shares of -x and w as the formula gives."""
+    x, w, t = make(M, V, seed=5)
+    w.zero_()
+    w[:, 0] = top
+    w[:V // 2, 0] = -3e38
+    lse, keep = check(fp8bs, x, w, t)
+    d = torch.full((M,), 2.0 ** -20, device="cuda")
+    dx, dw = fp8bs.bf16_linear_xent_backward(x, w, t, lse, d)
+    # lse is the largest logit: log of at most V is less than its last bit
+    P = (w[:, 0].double()[None, :] == lse.double()[:, None]).double() * keep[:, None]
+    G = P.clone()
+    rows = torch.nonzero(keep)[:, 0]
+    G[rows, t[rows]] -= 1.0
+    want = (G.t() @ (2.0 ** -20 * x.double()))
+    # G is 0, 1 or -1: FP32 sums of exact products, one bf16 rounding
+    tol = 2 * M * U * (G.abs().t() @ (2.0 ** -20 * x.double().abs()))
+    assert torch.all((dw.double() - want).abs() <= tol + 2.0 ** -8 * want.abs())
