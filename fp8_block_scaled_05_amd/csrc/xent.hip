@@ -85,7 +85,7 @@ dim3 tile_grid(int64_t tiles, int64_t per_cu = 1) {
 // What the row pass leaves for the others.
 struct Header {
   int32_t rows;     // rows with a loss
-  int32_t uniform;  // dloss is one value over those rows (backward)
+  int32_t uniform;  // dloss is one positive, finite value over those rows (backward)
   float c;          // max |dloss| (1 where that is 0 or not finite)
 };
 
@@ -176,12 +176,14 @@ __device__ __forceinline__ Header number_rows(const RowArgs& a, bool write, int3
     for (int w = 0; w < 16; ++w) {
       top = fmaxf(top, red[0][w]);
       const float x = red[1][w];
-      if (x == INFINITY) continue;  // a wave without rows
+      if (x == INFINITY) continue;  // a wave without rows, or of infinite dloss (top)
       same = same && x == x && (v == INFINITY || v == x);
       v = x;
     }
     h.c = top > 0.0f && top < INFINITY ? top : 1.0f;
-    h.uniform = same && fabsf(v) == top && v > 0.0f ? 1 : 0;
+    // an infinite dloss is not taken as one value for all: it has to reach dw,
+    // which takes it through x (c is 1 then)
+    h.uniform = same && v == top && v > 0.0f && v < INFINITY ? 1 : 0;
   }
   if (write && threadIdx.x == 0) *a.r.h = h;
   return h;

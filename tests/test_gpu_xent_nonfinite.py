@@ -126,3 +126,20 @@ def test_logits_at_the_end_of_the_range(fp8bs, M, V, top):
     # G is 0, 1 or -1: FP32 sums of exact products, one bf16 rounding
     tol = 2 * M * U * (G.abs().t() @ (2.0 ** -20 * x.double().abs()))
     assert torch.all((dw.double() - want).abs() <= tol + 2.0 ** -8 * want.abs())
+
+
+@pytest.mark.parametrize("M,V,K", [(64, 200, 128), (200, 333, 256), (256, 512, 128),
+                                   (5000, 300, 128)])
+@pytest.mark.parametrize("which", ["all", "half", "one"])
+def test_infinite_dloss(fp8bs, M, V, K, which):
+    """An overflowed scale of the loss reaches dx of its rows and all of dw."""
+    x, w, t = make(M, V, K, seed=6)
+    _, lse = fp8bs.bf16_linear_xent(x, w, t)
+    d = torch.full((M,), 0.5, device="cuda")
+    hit = {"all": slice(None), "half": slice(M // 2, None), "one": slice(1, 2)}[which]
+    d[hit] = float("inf")
+    dx, dw = fp8bs.bf16_linear_xent_backward(x, w, t, lse, d)
+    assert not torch.isfinite(dw).any()
+    rows = torch.isinf(d) & (t >= 0)
+    assert not torch.isfinite(dx[rows]).any()
+    assert torch.isfinite(dx[~rows]).all()
