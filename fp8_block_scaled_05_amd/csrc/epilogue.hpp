@@ -45,6 +45,11 @@ __device__ __forceinline__ float activate(float z) {
   }
 }
 
+// z within [-top, top], NaN as it is (the median of three would drop it).
+__device__ __forceinline__ float clamped(float z, float top) {
+  return __builtin_elementwise_minimum(__builtin_elementwise_maximum(z, -top), top);
+}
+
 // The derivative, in the same arithmetic.  1 - s is taken as e s, with s = 1 / (1
 // + e): the difference itself, off by 2^-25 whatever its size, cost the largest
 // derivatives two more units of FP32.  z is clamped so that e stays finite, where
@@ -54,14 +59,14 @@ __device__ __forceinline__ float activate_grad(float z) {
   if constexpr (ACT == kActRelu) {
     return z > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (ACT == kActSilu) {
-    const float c = __builtin_amdgcn_fmed3f(z, -87.0f, 87.0f);
+    const float c = clamped(z, 87.0f);
     const float e = __builtin_amdgcn_exp2f(c * -kLog2e);
     const float s = __builtin_amdgcn_rcpf(1.0f + e);
     return __builtin_fmaf(c * s, e * s, s);
   } else if constexpr (ACT == kActGelu) {
     constexpr float k1 = -2.0f * kGeluC * kLog2e, k3 = k1 * kGeluA;
     constexpr float d1 = 2.0f * kGeluC, d3 = 3.0f * d1 * kGeluA;  // 2 u' = d1 + d3 z^2
-    const float c = __builtin_amdgcn_fmed3f(z, -10.0f, 10.0f);
+    const float c = clamped(z, 10.0f);
     const float c2 = c * c;
     const float e = __builtin_amdgcn_exp2f(c * __builtin_fmaf(c2, k3, k1));
     const float s = __builtin_amdgcn_rcpf(1.0f + e);
