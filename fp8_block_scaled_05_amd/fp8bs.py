@@ -700,7 +700,7 @@ def fp8_quant_epilogue_backward(dy, z, act="none", q=None, s=None, qt=None, st=N
     ``(q, s)``: E4M3 codes [M][N], scales [N/128][M], the (a, sa) of the data
     gradient; ``(qt, st)``: codes [N][Mp], scales [Mp/128][N], Mp = M rounded
     up to 128 (zero padding), the (a, sa) of the weight gradient; ``dbias``
-    fp32 [N].  Returns ``(q, s, qt, st, dbias)``.
+    fp32 [N], zeros where dy has no rows.  Returns ``(q, s, qt, st, dbias)``.
     """
     act_id = _act_id(act)
     _mat(dy, "dy", 0, 0, torch.bfloat16)
@@ -723,6 +723,8 @@ def fp8_quant_epilogue_backward(dy, z, act="none", q=None, s=None, qt=None, st=N
     qt = torch.empty(N, Mp, dtype=torch.uint8, device=dev) if qt is None else qt
     st = torch.empty(Mp // 128, N, dtype=torch.float32, device=dev) if st is None else st
     dbias = torch.empty(N, dtype=torch.float32, device=dev) if dbias is None else dbias
+    if M == 0:
+        dbias[:N].zero_()  # the library launches nothing then
     if workspace is None:
         workspace = torch.empty(workspace_bytes(OP_EPILOGUE_BACKWARD, M, N, 0), dtype=torch.uint8,
                                 device=dev)

@@ -394,7 +394,7 @@ int fp8_block_gemm_epilogue_e4m3_out(int a_kind, const void* a, int64_t lda,
  *   z       [in]  bf16 [M][ldz], as the forward call kept it (not read for
  *                 FP8BS_ACT_NONE, may be NULL then).
  *   workspace  fp8bs_workspace_bytes(FP8BS_OP_EPILOGUE_BACKWARD, M, N, 0, 0).
- * M == 0 launches nothing (dbias is not written).
+ * M == 0 launches nothing: dbias, whose value is then 0, is not written.
  * Errors: N not a multiple of 128 -> ERR_SHAPE; unknown act -> ERR_DTYPE;
  *         otherwise as the two quantizers; workspace -> ERR_WORKSPACE.
  */

@@ -34,3 +34,20 @@ def test_nan_pre_activation(fp8bs, M, N, act):
     assert torch.isfinite(ref[4]).all() and torch.isfinite(s).all() and torch.isfinite(st).all()
     rest = ~hit.any(dim=0)
     assert torch.equal(db[rest], ref[4][rest])
+
+
+@pytest.mark.parametrize("act", ["none", "gelu"])
+@pytest.mark.parametrize("N", [128, 640])
+def test_no_rows(fp8bs, N, act):
+    """The bias gradient of an empty batch is zero, as the head's weight gradient."""
+    dy = torch.empty(0, N, dtype=torch.bfloat16, device="cuda")
+    z = dy if act != "none" else None
+    db = torch.full((N + 3,), 7.0, device="cuda")
+    q, s, qt, st, got = fp8bs.fp8_quant_epilogue_backward(dy, z, act, dbias=db)
+    assert got is db and torch.all(db[:N] == 0) and torch.all(db[N:] == 7)
+    assert q.shape == (0, N) and s.shape == (N // 128, 0) and qt.shape == (N, 0)
+    assert st.shape == (0, N)
+    # freed memory holds what was there: a fresh dbias is cleared too
+    junk = torch.full((N,), 3.0, device="cuda")
+    del junk
+    assert torch.all(fp8bs.fp8_quant_epilogue_backward(dy, z, act)[4] == 0)
