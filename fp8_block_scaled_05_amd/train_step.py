@@ -89,7 +89,8 @@ def loss_and_grads(cfg, p, tokens, target, ignore_index=-100):
         x = y
     head = p["head"].to(bf16)
     loss, lse = fp8bs.bf16_linear_xent(x, head, target, ignore_index)
-    count = (target != ignore_index).sum().clamp_min(1).float()
+    counts = (target != ignore_index) & (target >= 0) & (target < cfg.vocab)
+    count = counts.sum().clamp_min(1).float()
     dloss = torch.ones_like(loss) / count
 
     grads = {}
