@@ -175,9 +175,10 @@ def _mat(t, name, rows, cols, dtype, ld=None):
     """Check that the caller's 2-D row-major tensor ``t`` (if given) holds
     ``rows`` x ``cols`` elements of ``dtype``: the library receives only its
     pointer and row stride, so a smaller tensor would be read or written
-    past its end on the device.  ``ld``: the row stride the layout fixes."""
+    past its end on the device.  ``ld``: the row stride the layout fixes.
+    Returns the leading dimension to pass (see ``_ld``), 0 without elements."""
     if t is None:
-        return
+        return 0
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     shape = t.shape
@@ -185,7 +186,7 @@ def _mat(t, name, rows, cols, dtype, ld=None):
         raise ValueError(f"{name} must be a 2-D tensor of at least [{rows}][{cols}], "
                          f"got {list(shape)}")
     if shape[0] == 0 or shape[1] == 0:
-        return  # nothing is read or written; an empty tensor's strides are arbitrary
+        return 0  # nothing is read or written; an empty tensor's strides are arbitrary
     row, col = t.stride()
     if shape[1] > 1 and col != 1:
         raise ValueError(f"{name} must have unit column stride")
@@ -193,6 +194,7 @@ def _mat(t, name, rows, cols, dtype, ld=None):
         raise ValueError(f"{name} rows overlap (row stride {row} < {cols})")
     if ld is not None and rows > 1 and row != ld:
         raise ValueError(f"{name} must have row stride {ld}, got {row}")
+    return row if shape[0] != 1 else _one_row_ld(shape[1])
 
 
 def _vec(t, name, n, dtype):
@@ -209,12 +211,19 @@ def _vec(t, name, n, dtype):
 def _rowmajor(t, name):
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be a 2-D tensor with unit column stride")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+    return _ld(t)
+
+
+def _one_row_ld(cols):
+    # A single row's stride is never used and torch leaves it arbitrary (0 or 1
+    # in broadcast and transposed views, a whole sequence in a view of one
+    # token): the library gets one that its checks take.
+    return (cols + 15) // 16 * 16
 
 
 def _ld(t):
     # leading dimension of a row-major 2-D tensor (its row stride)
-    return t.stride(0) if t.dim() == 2 else t.shape[-1]
+    return t.stride(0) if t.size(0) != 1 else _one_row_ld(t.size(1))
 
 
 def _k_of(K, name):
@@ -251,7 +260,7 @@ def fp8_quant_act_1x128(x, q=None, s=None, lds=None):
     if s is None:
         s = torch.empty(KB, lds or M, dtype=torch.float32, device=x.device)
     with _on(x.device):
-        _check(lib.fp8_quant_act_1x128(_ptr(x), M, K, ldx, _ptr(q), _ld(q), _ptr(s), s.stride(0),
+        _check(lib.fp8_quant_act_1x128(_ptr(x), M, K, ldx, _ptr(q), _ld(q), _ptr(s), _ld(s),
                                        _stream(x)), "fp8_quant_act_1x128")
     return q, s
 
@@ -293,7 +302,7 @@ def fp8_quant_act_1x128_delayed(x, hist, step, mode="tile", q=None, s=None, stat
         s = torch.empty(KB, M, dtype=torch.float32, device=x.device)
     with _on(x.device):
         _check(lib.fp8_quant_act_1x128_delayed(_ptr(x), M, K, ldx, _ptr(q), _ld(q), _ptr(s),
-                                               s.stride(0), m, _ptr(hist), ldh, H, step,
+                                               _ld(s), m, _ptr(hist), ldh, H, step,
                                                _ptr(stats), _stream(x)),
                "fp8_quant_act_1x128_delayed")
     return q, s
@@ -344,7 +353,7 @@ def fp8_quant_linear(x, w, q=None, s=None, qw=None, sw=None):
     if sw is None:
         sw = torch.empty((N + 127) // 128, KB, dtype=torch.float32, device=w.device)
     with _on(x.device):
-        _check(lib.fp8_quant_linear(_ptr(x), M, K, ldx, _ptr(q), _ld(q), _ptr(s), s.stride(0),
+        _check(lib.fp8_quant_linear(_ptr(x), M, K, ldx, _ptr(q), _ld(q), _ptr(s), _ld(s),
                                     _ptr(w), N, ldw, _ptr(qw), _ld(qw), _ptr(sw), _stream(x)),
                "fp8_quant_linear")
     return q, s, qw, sw
@@ -395,7 +404,7 @@ def fp8_quant_act_128x1_t(x, qt=None, st=None):
         st = torch.empty(M // 128, N, dtype=torch.float32, device=x.device)
     with _on(x.device):
         _check(lib.fp8_quant_act_128x1_t(_ptr(x), M, N, ldx, _ptr(qt), _ld(qt), _ptr(st),
-                                         st.stride(0), _stream(x)), "fp8_quant_act_128x1_t")
+                                         _ld(st), _stream(x)), "fp8_quant_act_128x1_t")
     return qt, st
 
 
@@ -416,8 +425,8 @@ def fp8_block_gemm_rowscaled(a, sa, b, sb, out=None, out_dtype=torch.float32):
     if out is None:
         out = torch.empty(M, N, dtype=out_dtype, device=a.device)
     with _on(a.device):
-        _check(lib.fp8_block_gemm_rowscaled(_ptr(a), _ld(a), _ptr(sa), sa.stride(0), _ptr(b),
-                                            _ld(b), _ptr(sb), sb.stride(0), _ptr(out), _ld(out),
+        _check(lib.fp8_block_gemm_rowscaled(_ptr(a), _ld(a), _ptr(sa), _ld(sa), _ptr(b),
+                                            _ld(b), _ptr(sb), _ld(sb), _ptr(out), _ld(out),
                                             _out_kind(out.dtype), M, N, K, _stream(a)),
                "fp8_block_gemm_rowscaled")
     return out
@@ -449,7 +458,7 @@ def fp8_block_kgrouped_gemm_rowscaled(a, sa, b, sb, group_offsets, out=None,
         out = torch.empty(G, M, N, dtype=out_dtype, device=a.device)
     with _on(a.device):
         _check(lib.fp8_block_kgrouped_gemm_rowscaled(
-            _ptr(a), _ld(a), _ptr(sa), sa.stride(0), _ptr(b), _ld(b), _ptr(sb), sb.stride(0),
+            _ptr(a), _ld(a), _ptr(sa), _ld(sa), _ptr(b), _ld(b), _ptr(sb), _ld(sb),
             _ptr(out), out.stride(1), out.stride(0), _out_kind(out.dtype), _ptr(group_offsets),
             G, M, N, T, _stream(a)), "fp8_block_kgrouped_gemm_rowscaled")
     return out
@@ -472,18 +481,19 @@ def _a_kind(a):
 
 
 def _dense_operands(where, a, sa, b, sb):
-    """Sizes of a dense GEMM call after checking its operand tensors."""
+    """Sizes and leading dimensions (of a, sa, b) of a dense GEMM call after
+    checking its operand tensors."""
     a_kind = _a_kind(a)
-    _mat(a, "a", 0, 0, a.dtype)
+    lda = _mat(a, "a", 0, 0, a.dtype)
     M, K = a.shape
     KB = _k_of(K, where)
     N = b.shape[0] if b.dim() == 2 else -1
-    _mat(b, "b", N, K, torch.uint8)
+    ldb = _mat(b, "b", N, K, torch.uint8)
     if a_kind == A_E4M3 and sa is None:
         raise ValueError("E4M3 codes need their scales sa")
-    _mat(sa, "sa", KB, M, torch.float32)
+    ldsa = _mat(sa, "sa", KB, M, torch.float32)
     _mat(sb, "sb", (N + 127) // 128, KB, torch.float32, ld=KB)
-    return a_kind, M, N, K
+    return a_kind, M, N, K, lda, ldsa, ldb
 
 
 def _workspace(a_kind, M, N, K, workspace, device):
@@ -501,16 +511,15 @@ def fp8_block_gemm(a, sa, b, sb, out=None, out_dtype=torch.bfloat16, workspace=N
     bfloat16 (quantized inside the call; ``sa`` is then an optional output of
     the scales).  ``b`` uint8 [N][K], ``sb`` fp32 [ceil(N/128)][K/128].
     """
-    a_kind, M, N, K = _dense_operands("fp8_block_gemm", a, sa, b, sb)
+    a_kind, M, N, K, lda, ldsa, ldb = _dense_operands("fp8_block_gemm", a, sa, b, sb)
     if out is not None:
         _mat(out, "out", M, N, out.dtype)
     _need_device(a, sa, b, sb, out, workspace)
     if out is None:
         out = torch.empty(M, N, dtype=out_dtype, device=a.device)
     workspace, ws_bytes = _workspace(a_kind, M, N, K, workspace, a.device)
-    ldsa = sa.stride(0) if sa is not None else 0
     with _on(a.device):
-        _check(lib.fp8_block_gemm(a_kind, _ptr(a), _ld(a), _ptr(sa), ldsa, _ptr(b), _ld(b),
+        _check(lib.fp8_block_gemm(a_kind, _ptr(a), lda, _ptr(sa), ldsa, _ptr(b), ldb,
                                   _ptr(sb), _ptr(out), _ld(out), _out_kind(out.dtype), M, N, K,
                                   _ptr(workspace), ws_bytes, _stream(a)), "fp8_block_gemm")
     return out
@@ -526,12 +535,11 @@ def fp8_block_gemm_bf16_noalloc(a, sa, b, sb, out):
         raise ValueError("a must be bfloat16")
     if out is None:
         raise ValueError("out must be given (this entry point allocates nothing)")
-    _, M, N, K = _dense_operands("fp8_block_gemm_bf16_noalloc", a, sa, b, sb)
+    _, M, N, K, lda, ldsa, ldb = _dense_operands("fp8_block_gemm_bf16_noalloc", a, sa, b, sb)
     _mat(out, "out", M, N, out.dtype)
     _need_device(a, sa, b, sb, out)
-    ldsa = sa.stride(0) if sa is not None else 0
     with _on(a.device):
-        _check(lib.fp8_block_gemm_bf16_noalloc(_ptr(a), _ld(a), _ptr(sa), ldsa, _ptr(b), _ld(b),
+        _check(lib.fp8_block_gemm_bf16_noalloc(_ptr(a), lda, _ptr(sa), ldsa, _ptr(b), ldb,
                                                _ptr(sb), _ptr(out), _ld(out),
                                                _out_kind(out.dtype), M, N, K, _stream(a)),
                "fp8_block_gemm_bf16_noalloc")
@@ -569,7 +577,7 @@ def fp8_block_grouped_gemm(a, sa, b, sb, group_offsets, out=None, out_dtype=torc
     if out is None:
         out = torch.empty(M_total, N, dtype=out_dtype, device=a.device)
     with _on(a.device):
-        _check(lib.fp8_block_grouped_gemm(_ptr(a), _ld(a), _ptr(sa), sa.stride(0), _ptr(b),
+        _check(lib.fp8_block_grouped_gemm(_ptr(a), _ld(a), _ptr(sa), _ld(sa), _ptr(b),
                                           b.stride(1), b.stride(0), _ptr(sb), _ptr(out), _ld(out),
                                           _out_kind(out.dtype), _ptr(group_offsets), G, M_total, N,
                                           K, None, 0, _stream(a)), "fp8_block_grouped_gemm")
@@ -598,16 +606,15 @@ def fp8_block_gemm_e4m3_out(a, sa, b, sb, qc=None, sc=None, workspace=None):
     [N/128][ldsc] (``sc[nb, m]``), the layout ``fp8_block_gemm`` takes as
     its activation input.
     """
-    a_kind, M, N, K = _dense_operands("fp8_block_gemm_e4m3_out", a, sa, b, sb)
+    a_kind, M, N, K, lda, ldsa, ldb = _dense_operands("fp8_block_gemm_e4m3_out", a, sa, b, sb)
     _e4m3_check(M, N, qc, sc)
     _need_device(a, sa, b, sb, qc, sc, workspace)
     qc, sc = _e4m3_outputs(M, N, qc, sc, a.device)
     workspace, ws_bytes = _workspace(a_kind, M, N, K, workspace, a.device)
-    ldsa = sa.stride(0) if sa is not None else 0
     with _on(a.device):
-        _check(lib.fp8_block_gemm_e4m3_out(a_kind, _ptr(a), _ld(a), _ptr(sa), ldsa, _ptr(b),
-                                           _ld(b), _ptr(sb), _ptr(qc), _ld(qc), _ptr(sc),
-                                           sc.stride(0), M, N, K, _ptr(workspace), ws_bytes,
+        _check(lib.fp8_block_gemm_e4m3_out(a_kind, _ptr(a), lda, _ptr(sa), ldsa, _ptr(b),
+                                           ldb, _ptr(sb), _ptr(qc), _ld(qc), _ptr(sc),
+                                           _ld(sc), M, N, K, _ptr(workspace), ws_bytes,
                                            _stream(a)),
                "fp8_block_gemm_e4m3_out")
     return qc, sc
@@ -624,9 +631,9 @@ def fp8_block_grouped_gemm_e4m3_out(a, sa, b, sb, group_offsets, qc=None, sc=Non
     _need_device(a, sa, b, sb, group_offsets, qc, sc)
     qc, sc = _e4m3_outputs(M_total, N, qc, sc, a.device)
     with _on(a.device):
-        _check(lib.fp8_block_grouped_gemm_e4m3_out(_ptr(a), _ld(a), _ptr(sa), sa.stride(0), _ptr(b),
+        _check(lib.fp8_block_grouped_gemm_e4m3_out(_ptr(a), _ld(a), _ptr(sa), _ld(sa), _ptr(b),
                                                    b.stride(1), b.stride(0), _ptr(sb), _ptr(qc),
-                                                   _ld(qc), _ptr(sc), sc.stride(0),
+                                                   _ld(qc), _ptr(sc), _ld(sc),
                                                    _ptr(group_offsets), G, M_total, N, K, None, 0,
                                                    _stream(a)),
                "fp8_block_grouped_gemm_e4m3_out")
@@ -642,10 +649,9 @@ def _act_id(act):
 def _epilogue_operands(M, N, bias, act, residual, z):
     act = _act_id(act)
     _vec(bias, "bias", N, torch.float32)
-    _mat(residual, "residual", M, N, torch.bfloat16)
-    _mat(z, "z", M, N, torch.bfloat16)
-    return _Epilogue(_ptr(bias), _ptr(residual), residual.stride(0) if residual is not None else 0,
-                     _ptr(z), z.stride(0) if z is not None else 0, act)
+    ldr = _mat(residual, "residual", M, N, torch.bfloat16)
+    ldz = _mat(z, "z", M, N, torch.bfloat16)
+    return _Epilogue(_ptr(bias), _ptr(residual), ldr, _ptr(z), ldz, act)
 
 
 def fp8_block_gemm_epilogue(a, sa, b, sb, bias=None, act="none", residual=None, z=None, out=None,
@@ -657,17 +663,16 @@ def fp8_block_gemm_epilogue(a, sa, b, sb, bias=None, act="none", residual=None, 
     ``residual`` bf16 [M][N]; ``z`` an optional bf16 [M][N] output that
     receives what the backward pass needs (``fp8_quant_epilogue_backward``).
     """
-    a_kind, M, N, K = _dense_operands("fp8_block_gemm_epilogue", a, sa, b, sb)
+    a_kind, M, N, K, lda, ldsa, ldb = _dense_operands("fp8_block_gemm_epilogue", a, sa, b, sb)
     ep = _epilogue_operands(M, N, bias, act, residual, z)
     _mat(out, "out", M, N, torch.bfloat16)
     _need_device(a, sa, b, sb, bias, residual, z, out, workspace)
     if out is None:
         out = torch.empty(M, N, dtype=torch.bfloat16, device=a.device)
     workspace, ws_bytes = _workspace(a_kind, M, N, K, workspace, a.device)
-    ldsa = sa.stride(0) if sa is not None else 0
     with _on(a.device):
-        _check(lib.fp8_block_gemm_epilogue(a_kind, _ptr(a), _ld(a), _ptr(sa), ldsa, _ptr(b),
-                                           _ld(b), _ptr(sb), ep, _ptr(out), _ld(out), M, N, K,
+        _check(lib.fp8_block_gemm_epilogue(a_kind, _ptr(a), lda, _ptr(sa), ldsa, _ptr(b),
+                                           ldb, _ptr(sb), ep, _ptr(out), _ld(out), M, N, K,
                                            _ptr(workspace), ws_bytes, _stream(a)),
                "fp8_block_gemm_epilogue")
     return out
@@ -677,17 +682,17 @@ def fp8_block_gemm_epilogue_e4m3_out(a, sa, b, sb, bias=None, act="none", residu
                                      qc=None, sc=None, workspace=None):
     """As ``fp8_block_gemm_epilogue``, with the result quantized per 1x128 tile
     along N: returns ``(qc, sc)`` as ``fp8_block_gemm_e4m3_out``."""
-    a_kind, M, N, K = _dense_operands("fp8_block_gemm_epilogue_e4m3_out", a, sa, b, sb)
+    a_kind, M, N, K, lda, ldsa, ldb = _dense_operands("fp8_block_gemm_epilogue_e4m3_out", a, sa,
+                                                      b, sb)
     _e4m3_check(M, N, qc, sc)
     ep = _epilogue_operands(M, N, bias, act, residual, z)
     _need_device(a, sa, b, sb, bias, residual, z, qc, sc, workspace)
     qc, sc = _e4m3_outputs(M, N, qc, sc, a.device)
     workspace, ws_bytes = _workspace(a_kind, M, N, K, workspace, a.device)
-    ldsa = sa.stride(0) if sa is not None else 0
     with _on(a.device):
         _check(lib.fp8_block_gemm_epilogue_e4m3_out(
-            a_kind, _ptr(a), _ld(a), _ptr(sa), ldsa, _ptr(b), _ld(b), _ptr(sb), ep, _ptr(qc),
-            _ld(qc), _ptr(sc), sc.stride(0), M, N, K, _ptr(workspace), ws_bytes, _stream(a)),
+            a_kind, _ptr(a), lda, _ptr(sa), ldsa, _ptr(b), ldb, _ptr(sb), ep, _ptr(qc),
+            _ld(qc), _ptr(sc), _ld(sc), M, N, K, _ptr(workspace), ws_bytes, _stream(a)),
             "fp8_block_gemm_epilogue_e4m3_out")
     return qc, sc
 
@@ -732,7 +737,7 @@ def fp8_quant_epilogue_backward(dy, z, act="none", q=None, s=None, qt=None, st=N
         _check(lib.fp8_quant_epilogue_backward(
             _ptr(dy), _rowmajor(dy, "dy") if M else N, _ptr(z),
             _rowmajor(z, "z") if z is not None and M else 0, act_id, M, N, _ptr(q), _ld(q),
-            _ptr(s), s.stride(0), _ptr(qt), _ld(qt), _ptr(st), st.stride(0), _ptr(dbias),
+            _ptr(s), _ld(s), _ptr(qt), _ld(qt), _ptr(st), _ld(st), _ptr(dbias),
             _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(dy)),
             "fp8_quant_epilogue_backward")
     return q, s, qt, st, dbias
@@ -777,8 +782,8 @@ def bf16_linear_xent(x, w, target, ignore_index=-100, loss=None, lse=None, works
     ldx = _rowmajor(x, "x") if M else K
     with _on(x.device):
         _check(lib.bf16_linear_xent(_ptr(x), ldx, _ptr(w), _rowmajor(w, "w"), _ptr(target),
-                                    ignore_index, _ptr(loss), _ptr(lse), M, V, K, _ptr(workspace), ws_bytes,
-                                    _stream(x)), "bf16_linear_xent")
+                                    ignore_index, _ptr(loss), _ptr(lse), M, V, K, _ptr(workspace),
+                                    ws_bytes, _stream(x)), "bf16_linear_xent")
     return loss, lse
 
 
