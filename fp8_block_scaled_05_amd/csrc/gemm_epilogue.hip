@@ -207,9 +207,8 @@ hipError_t launch_block_gemm_epilogue(const GemmArgs& args, const Epilogue& e, O
   if (args.M <= 64 && out == kOutE4M3)
     return launch_tiles<gemm::Rows64Cfg>(args, ep, out, stream);
   switch (gemm::pick_tiles(args)) {
-    case gemm::Tiles::kSmall:
-      return out == kOutBF16 ? launch_tiles<SmallCfg>(args, ep, out, stream)
-                             : launch_tiles<gemm::Rows64Cfg>(args, ep, out, stream);
+    // one round of 64x128 tiles at most: E4M3 outputs, the others are taken above
+    case gemm::Tiles::kSmall: return launch_tiles<gemm::Rows64Cfg>(args, ep, out, stream);
     case gemm::Tiles::kHalf: return launch_tiles<gemm::LargeTail>(args, ep, out, stream);
     default: return launch_tiles<gemm::LargeCfg, gemm::LargeTail>(args, ep, out, stream);
   }
