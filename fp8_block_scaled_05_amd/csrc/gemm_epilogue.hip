@@ -24,7 +24,8 @@ struct LinearEpilogue {
   // Bias and residual of a lane's outputs, rows 16 i + 4 g + r and FN
   // consecutive columns (see gemm::store_tile).  Tiles with registers to spare
   // (kEarly) load them before the K loop, which hides their latency: 333 x 2050 x
-  // 2048 with all parts 17.8 against 15.5 us.  Larger tiles load them after it.
+  // 2048 with all parts, by 64x128 tiles, 17.8 against 15.5 us.  Larger tiles load
+  // them after it.
   template <class C>
   struct Early {
     static constexpr bool kEarly = C::FM * C::FN <= 8;
@@ -169,6 +170,9 @@ struct LinearEpilogue {
 //    300 x 2048 x 4096             19.8   14.4   17.2   (160)
 //    700 x 4096 x 2048     30.4           21.9          (704)
 //   1000 x 4096 x 7168     63.2           72.6          (1024)
+// The rule goes by the tiles alone.  K moves the ends of it: at 128 tiles and a
+// K of 7168 it takes 32x64 where 64x64 is 8% faster, at 198 tiles and a K of 2048
+// (333 x 2050) 64x64 where 32x64 is 5% faster.
 using SmallCfg = gemm::Cfg<64, 64, 2, 2, 4, 1>;
 using TinyCfg = gemm::Cfg<32, 64, 2, 2, 4, 1>;
 

@@ -43,7 +43,8 @@ using LogitsHalf = gemm16::Cfg<256, 128, 4, 2, 2, kRow, kRow>;
 using LogitsQuarter = gemm16::Cfg<128, 128, 2, 4, 2, kRow, kRow>;  // see logits_tiles
 using LogitsSmall = gemm16::Cfg<128, 64, 4, 1, 4, kRow, kRow>;
 // Up to 16 rows, two workgroups per compute unit: copies no rows of x that do not
-// exist, and so has more of w in flight (1 x 129280 x 7168: 326 us small, 304 so).
+// exist, and so has more of w in flight (1 x 129280 x 7168, w through the caches:
+// 326 us small, 304 so; past them, as launch_few takes it, 265).
 using LogitsToken = gemm16::Cfg<128, 16, 2, 1, 3, kRow, kRow>;
 // Both at half the width, for heads whose 64x64 tiles fit one round of workgroups:
 // a step of fewer copies is shorter (55 x 1615 x 4736: 29 us small, 20 so; 20 x

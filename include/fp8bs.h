@@ -525,9 +525,13 @@ int fp8_block_grouped_gemm_e4m3_out(const uint8_t* a, int64_t lda,
  *   target  [in]  int64 [M].  A row whose target is ignore_index, or lies
  *                 outside [0, V), carries no loss: loss and lse are 0 there
  *                 and its x may hold anything, NaN and infinities too.
- *   loss, lse [out] fp32 [M].  Non-finite logits give what the formulas give.
+ *   loss, lse [out] fp32 [M].  Non-finite logits give what the formulas give:
+ *                 a NaN logit a NaN lse and loss, +inf an infinite lse.
  *   workspace  fp8bs_workspace_bytes(FP8BS_OP_XENT, M, V, K, 0) bytes,
  *              256-byte aligned; free again when the call's work is done.
+ *              It grows with rows x vocabulary: 8 bytes per row and 64 columns
+ *              (32 in small tiles), and 2 K per row beyond 64 rows; 2.0 GB
+ *              at M = 65536, V = 129280, K = 7168 (the logits: 17 GB in bf16).
  * The result does not depend on timing (no atomics).
  * Errors: M < 0, V < 1, either above 2^31 - 1, K not a positive multiple of
  *         128 or above 2^22 -> ERR_SHAPE; NULL -> ERR_NULL; ldx/ldw < K, not
@@ -550,10 +554,14 @@ int bf16_linear_xent(const uint16_t* x, int64_t ldx, const uint16_t* w,
  *   lse     [in]  fp32 [M], as the forward call left it.
  *   dloss   [in]  fp32 [M], gradient of each row's loss.  It multiplies the
  *                 finished sums of dx in FP32; dw takes bf16(x dloss / c) with
- *                 c = max |dloss|, exact where dloss is one value.
+ *                 c = max |dloss| (1 where that is 0 or infinite), exact where
+ *                 dloss is one value.
  *   dx      [out] bf16 [M][lddx]; zeros for a row without a loss.
  *   dw      [out] bf16 [V][lddw], overwritten (all zeros for M == 0).
- *   workspace  fp8bs_workspace_bytes(FP8BS_OP_XENT_BACKWARD, M, V, K, 0).
+ *   workspace  fp8bs_workspace_bytes(FP8BS_OP_XENT_BACKWARD, M, V, K, 0): at
+ *              most 1 GB for G (or 512 bytes a row, if more), the larger of
+ *              256 MB and 4 M K bytes for the parts of dx, 4 M K bytes for
+ *              packed rows, whether they are needed or not, and 20 M of lists.
  * Errors: as bf16_linear_xent; lddx/lddw < K or not a multiple of 16 ->
  *         ERR_LAYOUT.
  */
