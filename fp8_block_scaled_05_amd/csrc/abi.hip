@@ -50,6 +50,14 @@ bool head_sizes_ok(int64_t M, int64_t V, int64_t K) {
          K <= kMaxHeadLd;
 }
 
+// Rows and row length of the norm's calls.
+bool norm_sizes_ok(int64_t M, int64_t K) {
+  return M >= 0 && K > 0 && K % kTile == 0 && K <= fp8bs::kMaxNormK;
+}
+
+// The gated product's FP32 result for few rows, before its E4M3 codes.
+size_t gated_y_bytes(int64_t M, int64_t N) { return round256(size_t(M) * size_t(N) * 4); }
+
 size_t fused_q_bytes(int64_t M, int64_t K) { return round256(size_t(M) * size_t(K)); }
 size_t fused_s_bytes(int64_t M, int64_t K) { return round256(size_t(K / kTile) * size_t(M) * 4); }
 
@@ -219,16 +227,20 @@ int block_gemm_impl(int a_kind, const void* a, int64_t lda, float* sa, int64_t l
   return hip_status(fp8bs::launch_block_gemm(g, out, st));
 }
 
+bool act_of(int act, int& out) {
+  switch (act) {
+    case FP8BS_ACT_NONE: out = fp8bs::kActNone; return true;
+    case FP8BS_ACT_RELU: out = fp8bs::kActRelu; return true;
+    case FP8BS_ACT_SILU: out = fp8bs::kActSilu; return true;
+    case FP8BS_ACT_GELU: out = fp8bs::kActGelu; return true;
+    default: return false;
+  }
+}
+
 // The caller's epilogue of an M x N output, checked.
 int epilogue_of(const fp8bs_epilogue* in, int64_t M, int64_t N, fp8bs::Epilogue& e) {
   if (!in) return FP8BS_ERR_NULL;
-  switch (in->act) {
-    case FP8BS_ACT_NONE: e.act = fp8bs::kActNone; break;
-    case FP8BS_ACT_RELU: e.act = fp8bs::kActRelu; break;
-    case FP8BS_ACT_SILU: e.act = fp8bs::kActSilu; break;
-    case FP8BS_ACT_GELU: e.act = fp8bs::kActGelu; break;
-    default: return FP8BS_ERR_DTYPE;
-  }
+  if (!act_of(in->act, e.act)) return FP8BS_ERR_DTYPE;
   if (M > 0 && N > 0 &&
       ((in->bias && !aligned(in->bias, 4)) ||
        (in->residual && (in->ldr < N || !aligned(in->residual, 2))) ||
@@ -283,6 +295,142 @@ int grouped_gemm_impl(const uint8_t* a, int64_t lda, const float* sa, int64_t ld
   g.group_offsets = group_offsets;
   g.G = G;
   return hip_status(fp8bs::launch_grouped_gemm(g, out, static_cast<hipStream_t>(stream)));
+}
+
+// Shared body of the gated entry points; N: columns of the output, half of W's
+// rows.  out: bf16 or E4M3.
+int gated_gemm_impl(int a_kind, const void* a, int64_t lda, float* sa, int64_t ldsa,
+                    const uint8_t* b, int64_t ldb, const float* sb, int act, uint16_t* z,
+                    int64_t ldz, void* c, int64_t ldc, fp8bs::OutKind out, float* sc, int64_t ldsc,
+                    int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+                    void* stream) {
+  const bool e4m3 = out == fp8bs::kOutE4M3;
+  if (a_kind != FP8BS_A_E4M3 && a_kind != FP8BS_A_BF16) return FP8BS_ERR_DTYPE;
+  fp8bs::Gate gate{z, ldz, 0};
+  if (!act_of(act, gate.act)) return FP8BS_ERR_DTYPE;
+  if (M < 0 || N < 0 || K <= 0 || K % kTile != 0 || N % kTile != 0) return FP8BS_ERR_SHAPE;
+  if (M == 0 || N == 0) return FP8BS_OK;
+  const bool bf16_a = a_kind == FP8BS_A_BF16;
+  if (!a || !b || !sb || !c || (!bf16_a && !sa) || (e4m3 && !sc)) return FP8BS_ERR_NULL;
+  if (!operand_ld_ok(lda, K) || !operand_ld_ok(ldb, K) || (sa && ldsa < M)) return FP8BS_ERR_LAYOUT;
+  if (!aligned(a, 16) || !aligned(b, 16) || !aligned(sb, 4) || (sa && !aligned(sa, 4)))
+    return FP8BS_ERR_LAYOUT;
+  if (z && (ldz < 2 * N || !aligned(z, 2))) return FP8BS_ERR_LAYOUT;
+  if (e4m3 ? !ld_ok(ldc, N) || ldsc < M || !aligned(c, 16) || !aligned(sc, 4)
+           : ldc < N || !aligned(c, 2))
+    return FP8BS_ERR_LAYOUT;
+  const bool few = M <= fp8bs::kFewRows && fp8bs::few_rows_gated_fits(N, ldb);
+  if (bf16_a || (e4m3 && M <= fp8bs::kFewRows)) {
+    const int op = e4m3 ? FP8BS_OP_GEMM_GATED_E4M3 : FP8BS_OP_GEMM_BF16;
+    if (!workspace || workspace_bytes < fp8bs_workspace_bytes(op, M, N, K, 0))
+      return FP8BS_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return FP8BS_ERR_LAYOUT;
+  }
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  uint8_t* const wq = static_cast<uint8_t*>(workspace);
+  // few rows, E4M3: the weight's stream first, its FP32 result is quantized after
+  float* const y = reinterpret_cast<float*>(wq + fused_q_bytes(M, K) + fused_s_bytes(M, K));
+  void* const few_c = e4m3 ? y : c;
+  const int64_t few_ldc = e4m3 ? N : ldc;
+  auto finish = [&](hipError_t e) {
+    if (e == hipSuccess && e4m3)
+      e = fp8bs::launch_quant_f32(y, M, N, static_cast<uint8_t*>(c), ldc, sc, ldsc, st);
+    return hip_status(e);
+  };
+  if (few && bf16_a && M <= fp8bs::kFewRowsFused)
+    return finish(fp8bs::launch_few_rows_gated(a, lda, sa, ldsa, true, b, ldb, sb, few_c, few_ldc,
+                                               !e4m3, M, N, K, gate, st));
+  fp8bs::GemmArgs g{};
+  g.b = b;
+  g.ldb = ldb;
+  g.sb = sb;
+  g.c = c;
+  g.ldc = ldc;
+  g.sc = sc;
+  g.ldsc = ldsc;
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.sb_ld = K / kTile;
+  g.a = static_cast<const uint8_t*>(a);
+  g.lda = lda;
+  g.sa = sa;
+  g.ldsa = ldsa;
+  if (bf16_a) {
+    float* ws = sa ? sa : reinterpret_cast<float*>(wq + fused_q_bytes(M, K));
+    g.ldsa = sa ? ldsa : M;
+    const int s0 = hip_status(fp8bs::launch_quant_act(static_cast<const uint16_t*>(a), M, K, lda,
+                                                      wq, K, ws, g.ldsa, st));
+    if (s0 != FP8BS_OK) return s0;
+    g.a = wq;
+    g.lda = K;
+    g.sa = ws;
+  }
+  if (few)
+    return finish(fp8bs::launch_few_rows_gated(g.a, g.lda, const_cast<float*>(g.sa), g.ldsa, false,
+                                               b, ldb, sb, few_c, few_ldc, !e4m3, M, N, K, gate,
+                                               st));
+  return hip_status(fp8bs::launch_block_gemm_gated(g, gate, out, st));
+}
+
+int grouped_gated_impl(const uint8_t* a, int64_t lda, const float* sa, int64_t ldsa,
+                       const uint8_t* b, int64_t ldb, int64_t b_group_stride, const float* sb,
+                       int act, uint16_t* z, int64_t ldz, void* c, int64_t ldc, fp8bs::OutKind out,
+                       float* sc, int64_t ldsc, const int32_t* group_offsets, int64_t G,
+                       int64_t M_total, int64_t N, int64_t K, void* stream) {
+  const bool e4m3 = out == fp8bs::kOutE4M3;
+  fp8bs::Gate gate{z, ldz, 0};
+  if (!act_of(act, gate.act)) return FP8BS_ERR_DTYPE;
+  if (G < 1 || G > kMaxGroups || M_total < 0 || N < 0 || K <= 0 || K % kTile != 0 ||
+      N % kTile != 0)
+    return FP8BS_ERR_SHAPE;
+  if (M_total == 0 || N == 0) return FP8BS_OK;
+  if (!a || !sa || !b || !sb || !c || !group_offsets || (e4m3 && !sc)) return FP8BS_ERR_NULL;
+  if (!operand_ld_ok(lda, K) || !operand_ld_ok(ldb, K) || ldsa < M_total) return FP8BS_ERR_LAYOUT;
+  if (b_group_stride % 16 != 0 || b_group_stride < (2 * N - 1) * ldb + K) return FP8BS_ERR_LAYOUT;
+  if (!aligned(a, 16) || !aligned(b, 16) || !aligned(sa, 4) || !aligned(sb, 4) ||
+      !aligned(group_offsets, 4))
+    return FP8BS_ERR_LAYOUT;
+  if (z && (ldz < 2 * N || !aligned(z, 2))) return FP8BS_ERR_LAYOUT;
+  if (e4m3 ? !ld_ok(ldc, N) || ldsc < M_total || !aligned(c, 16) || !aligned(sc, 4)
+           : ldc < N || !aligned(c, 2))
+    return FP8BS_ERR_LAYOUT;
+  fp8bs::GemmArgs g{};
+  g.a = a;
+  g.lda = lda;
+  g.sa = sa;
+  g.ldsa = ldsa;
+  g.b = b;
+  g.ldb = ldb;
+  g.b_group_stride = b_group_stride;
+  g.sb = sb;
+  g.c = c;
+  g.ldc = ldc;
+  g.sc = sc;
+  g.ldsc = ldsc;
+  g.M = M_total;
+  g.N = N;
+  g.K = K;
+  g.sb_ld = K / kTile;
+  g.group_offsets = group_offsets;
+  g.G = G;
+  return hip_status(
+      fp8bs::launch_grouped_gemm_gated(g, gate, out, static_cast<hipStream_t>(stream)));
+}
+
+// Shared body of the norm's forward calls; q null: bf16 output y only.
+int rmsnorm_impl(const fp8bs::NormArgs& a, bool codes, void* stream) {
+  if (!norm_sizes_ok(a.M, a.K) || !(a.eps >= 0x1p-100f) || a.eps > 3.4e38f) return FP8BS_ERR_SHAPE;
+  if (a.M == 0) return FP8BS_OK;
+  if (!a.x || !a.weight || (codes ? !a.q || !a.s : !a.y)) return FP8BS_ERR_NULL;
+  if (!ld_ok(a.ldx, a.K) || !aligned(a.x, 16) || !aligned(a.weight, 16)) return FP8BS_ERR_LAYOUT;
+  if ((a.residual && (!ld_ok(a.ldr, a.K) || !aligned(a.residual, 16))) ||
+      (a.h && (!ld_ok(a.ldh, a.K) || !aligned(a.h, 16))) ||
+      (a.y && (!ld_ok(a.ldy, a.K) || !aligned(a.y, 16))) || (a.rstd && !aligned(a.rstd, 4)))
+    return FP8BS_ERR_LAYOUT;
+  if (codes && (!ld_ok(a.ldq, a.K) || !aligned(a.q, 16) || a.lds < a.M || !aligned(a.s, 4)))
+    return FP8BS_ERR_LAYOUT;
+  return hip_status(fp8bs::launch_rmsnorm(a, static_cast<hipStream_t>(stream)));
 }
 
 fp8bs::OutKind out_of(int out_kind) {
@@ -381,6 +529,102 @@ int fp8_quant_epilogue_backward(const uint16_t* dy, int64_t lddy, const uint16_t
   return hip_status(fp8bs::launch_epilogue_backward(dy, lddy, z, ldz, e.act, M, N, q, ldq, s, lds,
                                                     qt, ldqt, st, ldst, dbias, workspace,
                                                     static_cast<hipStream_t>(stream)));
+}
+
+int fp8_block_gemm_gated(int a_kind, const void* a, int64_t lda, float* sa, int64_t ldsa,
+                         const uint8_t* b, int64_t ldb, const float* sb, int act, uint16_t* z,
+                         int64_t ldz, uint16_t* c, int64_t ldc, int64_t M, int64_t N, int64_t K,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  return gated_gemm_impl(a_kind, a, lda, sa, ldsa, b, ldb, sb, act, z, ldz, c, ldc,
+                         fp8bs::kOutBF16, nullptr, 0, M, N, K, workspace, workspace_bytes, stream);
+}
+
+int fp8_block_gemm_gated_e4m3_out(int a_kind, const void* a, int64_t lda, float* sa, int64_t ldsa,
+                                  const uint8_t* b, int64_t ldb, const float* sb, int act,
+                                  uint16_t* z, int64_t ldz, uint8_t* qc, int64_t ldqc, float* sc,
+                                  int64_t ldsc, int64_t M, int64_t N, int64_t K, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  return gated_gemm_impl(a_kind, a, lda, sa, ldsa, b, ldb, sb, act, z, ldz, qc, ldqc,
+                         fp8bs::kOutE4M3, sc, ldsc, M, N, K, workspace, workspace_bytes, stream);
+}
+
+int fp8_block_grouped_gemm_gated(const uint8_t* a, int64_t lda, const float* sa, int64_t ldsa,
+                                 const uint8_t* b, int64_t ldb, int64_t b_group_stride,
+                                 const float* sb, int act, uint16_t* z, int64_t ldz, uint16_t* c,
+                                 int64_t ldc, const int32_t* group_offsets, int64_t G,
+                                 int64_t M_total, int64_t N, int64_t K, void* stream) {
+  return grouped_gated_impl(a, lda, sa, ldsa, b, ldb, b_group_stride, sb, act, z, ldz, c, ldc,
+                            fp8bs::kOutBF16, nullptr, 0, group_offsets, G, M_total, N, K, stream);
+}
+
+int fp8_block_grouped_gemm_gated_e4m3_out(const uint8_t* a, int64_t lda, const float* sa,
+                                          int64_t ldsa, const uint8_t* b, int64_t ldb,
+                                          int64_t b_group_stride, const float* sb, int act,
+                                          uint16_t* z, int64_t ldz, uint8_t* qc, int64_t ldqc,
+                                          float* sc, int64_t ldsc, const int32_t* group_offsets,
+                                          int64_t G, int64_t M_total, int64_t N, int64_t K,
+                                          void* stream) {
+  return grouped_gated_impl(a, lda, sa, ldsa, b, ldb, b_group_stride, sb, act, z, ldz, qc, ldqc,
+                            fp8bs::kOutE4M3, sc, ldsc, group_offsets, G, M_total, N, K, stream);
+}
+
+int fp8_quant_gated_backward(const uint16_t* dy, int64_t lddy, const uint16_t* z, int64_t ldz,
+                             int act, int64_t M, int64_t N, uint8_t* q, int64_t ldq, float* s,
+                             int64_t lds, uint8_t* qt, int64_t ldqt, float* st, int64_t ldst,
+                             uint8_t* yt, int64_t ldyt, float* syt, int64_t ldsyt, void* stream) {
+  int a = 0;
+  if (!act_of(act, a)) return FP8BS_ERR_DTYPE;
+  if (M < 0 || N < 0 || N % kTile != 0) return FP8BS_ERR_SHAPE;
+  if (M == 0 || N == 0) return FP8BS_OK;
+  if (!dy || !z || !q || !s || !qt || !st || !yt != !syt) return FP8BS_ERR_NULL;
+  const int64_t Mp = (M + kTile - 1) / kTile * kTile;
+  if (!ld_ok(lddy, N) || !ld_ok(ldz, 2 * N) || !ld_ok(ldq, 2 * N) || lds < M || !ld_ok(ldqt, Mp) ||
+      ldst < 2 * N || (yt && (!ld_ok(ldyt, Mp) || ldsyt < N)))
+    return FP8BS_ERR_LAYOUT;
+  if (!aligned(dy, 16) || !aligned(z, 16) || !aligned(q, 16) || !aligned(s, 4) ||
+      !aligned(qt, 16) || !aligned(st, 4) || (yt && (!aligned(yt, 16) || !aligned(syt, 4))))
+    return FP8BS_ERR_LAYOUT;
+  const fp8bs::GatedGradArgs g{dy, lddy, z,    ldz, M,    N,  q,    ldq, s,
+                               lds, qt,  ldqt, st,  ldst, yt, ldyt, syt, ldsyt};
+  return hip_status(fp8bs::launch_gated_backward(g, a, static_cast<hipStream_t>(stream)));
+}
+
+int fp8_quant_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr,
+                      const float* weight, float eps, uint16_t* h, int64_t ldh, uint16_t* y,
+                      int64_t ldy, float* rstd, uint8_t* q, int64_t ldq, float* s, int64_t lds,
+                      int64_t M, int64_t K, void* stream) {
+  return rmsnorm_impl(fp8bs::NormArgs{x, ldx, residual, ldr, weight, eps, h, ldh, y, ldy, rstd, q,
+                                      ldq, s, lds, M, K},
+                      true, stream);
+}
+
+int bf16_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr,
+                 const float* weight, float eps, uint16_t* h, int64_t ldh, float* rstd,
+                 uint16_t* y, int64_t ldy, int64_t M, int64_t K, void* stream) {
+  return rmsnorm_impl(fp8bs::NormArgs{x, ldx, residual, ldr, weight, eps, h, ldh, y, ldy, rstd,
+                                      nullptr, 0, nullptr, 0, M, K},
+                      false, stream);
+}
+
+int bf16_rmsnorm_backward(const uint16_t* dy, int64_t lddy, const uint16_t* h, int64_t ldh,
+                          const float* rstd, const float* weight, const uint16_t* dh,
+                          int64_t lddh, uint16_t* dx, int64_t lddx, float* dweight, int64_t M,
+                          int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!norm_sizes_ok(M, K)) return FP8BS_ERR_SHAPE;
+  if (!weight || !dweight || (M > 0 && (!dy || !h || !rstd || !dx))) return FP8BS_ERR_NULL;
+  if (!aligned(weight, 16) || !aligned(dweight, 16)) return FP8BS_ERR_LAYOUT;
+  if (M > 0 && (!ld_ok(lddy, K) || !ld_ok(ldh, K) || !ld_ok(lddx, K) || !aligned(dy, 16) ||
+                !aligned(h, 16) || !aligned(dx, 16) || !aligned(rstd, 4) ||
+                (dh && (!ld_ok(lddh, K) || !aligned(dh, 16)))))
+    return FP8BS_ERR_LAYOUT;
+  if (M > 0) {
+    if (!workspace || workspace_bytes < fp8bs::rmsnorm_backward_workspace(M, K))
+      return FP8BS_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return FP8BS_ERR_LAYOUT;
+  }
+  const fp8bs::NormGradArgs g{dy, lddy, h, ldh, rstd, weight, dh, lddh, dx, lddx, nullptr, M, K};
+  return hip_status(fp8bs::launch_rmsnorm_backward(g, dweight, workspace,
+                                                   static_cast<hipStream_t>(stream)));
 }
 
 int fp8_block_gemm_rowscaled(const uint8_t* a, int64_t lda, const float* sa, int64_t ldsa,
@@ -538,10 +782,15 @@ size_t fp8bs_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int64_t G)
     return fp8bs::xent_grad_workspace(M, N, K);
   if (op == FP8BS_OP_EPILOGUE_BACKWARD)
     return M > 0 && N > 0 ? fp8bs::epilogue_backward_workspace(M, N) : 0;
+  if (op == FP8BS_OP_RMSNORM_BACKWARD)
+    return norm_sizes_ok(M, K) ? fp8bs::rmsnorm_backward_workspace(M, K) : 0;
   if (M <= 0 || K <= 0) return 0;
   switch (op) {
     case FP8BS_OP_GEMM_BF16:
       return fused_q_bytes(M, K) + fused_s_bytes(M, K);
+    case FP8BS_OP_GEMM_GATED_E4M3:
+      return fused_q_bytes(M, K) + fused_s_bytes(M, K) +
+             (M <= fp8bs::kFewRows && N > 0 ? gated_y_bytes(M, N) : 0);
     case FP8BS_OP_XENT:
       return head_sizes_ok(M, N, K) ? fp8bs::xent_workspace(M, N, K) : 0;
     default:

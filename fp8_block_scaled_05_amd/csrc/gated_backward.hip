@@ -1,0 +1,180 @@
+// Backward of the gated product y = act(gate) up for gfx950, up to the operands
+// of its three backward GEMMs:
+//   dgate = dy up act'(gate),  dup = dy act(gate)
+// in FP32, quantized by the online E4M3 rule per 1x128 tile (the data gradient's
+// operand, contraction over gate and up columns) and per 128 rows of a column,
+// transposed (the weight gradient's); y = act(gate) up is formed again from the
+// kept values and quantized per 128 rows for the down projection's weight
+// gradient.
+//
+// HBM-bound: 6 bytes in and 5 codes out per element of y.  One workgroup per
+// 128x128 block of y holds both gradients and y in registers, so everything is
+// read once and nothing but codes and scales is written.  A thread holds 8
+// values of each of 4 rows (16 lanes span a row): row maxima are a 16-lane
+// reduction, column maxima go over the thread's rows, its wave's row groups and
+// the waves.  The codes are transposed through LDS, 128x128 bytes at a time.
+
+#include "epilogue.hpp"
+#include "transpose.hpp"
+
+namespace fp8bs {
+
+namespace {
+
+// Two values -> two E4M3 codes in one half of `old`.  With |x| <= a and r =
+// RN32(448 / a) a finite |x r| is at most 448.0001, which the convert takes to
+// 448, so there is nothing to clamp.
+template <bool HI>
+__device__ __forceinline__ uint32_t codes2(float a, float b, uint32_t old) {
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, (int)old, HI);
+}
+
+__device__ __forceinline__ u32x2 codes8(const float (&v)[8], const float (&r)[8]) {
+  uint32_t lo = codes2<false>(v[0] * r[0], v[1] * r[1], 0u);
+  lo = codes2<true>(v[2] * r[2], v[3] * r[3], lo);
+  uint32_t hi = codes2<false>(v[4] * r[4], v[5] * r[5], 0u);
+  hi = codes2<true>(v[6] * r[6], v[7] * r[7], hi);
+  return u32x2{lo, hi};
+}
+
+constexpr int kThreads = 512;
+constexpr int kRows = 4;     // rows per thread, 32 apart
+constexpr int kPitch = 132;  // LDS row pitch of the staged codes (bytes)
+
+// The 128x128 block v (kRows rows of 8 columns per thread) as codes per column,
+// transposed to qt[n0 + c][m0 ..], scales to st.  cmax: 8 x 128 floats, rcp: 128,
+// tile: 128 * kPitch bytes, all free on entry and on return.
+__device__ __forceinline__ void store_columns(const float (&v)[kRows][8], uint8_t* qt, int64_t ldqt,
+                                              float* st, float (*cmax)[128], float* rcp,
+                                              uint8_t* tile) {
+  const int lane = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+  float cm[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    cm[c] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) cm[c] = fmaxf(cm[c], fabsf(v[i][c]));
+    cm[c] = fmaxf(cm[c], __shfl_xor(cm[c], 16, 64));
+    cm[c] = fmaxf(cm[c], __shfl_xor(cm[c], 32, 64));
+  }
+  if ((threadIdx.x & 63) < 16) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) cmax[threadIdx.x >> 6][lane * 8 + c] = cm[c];
+  }
+  __syncthreads();
+  if (threadIdx.x < 128) {
+    float m = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kThreads / 64; ++w) m = fmaxf(m, cmax[w][threadIdx.x]);
+    float s, r;
+    group_scale(m, s, r);
+    rcp[threadIdx.x] = r;
+    st[threadIdx.x] = s;
+  }
+  __syncthreads();
+  float r[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) r[c] = rcp[lane * 8 + c];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const u32x2 w = codes8(v[i], r);
+    uint32_t* const dst = reinterpret_cast<uint32_t*>(tile + (r0 + 32 * i) * kPitch + lane * 8);
+    dst[0] = w.x;
+    dst[1] = w.y;
+  }
+  __syncthreads();
+  // 16 consecutive threads cover the 128 rows of one output row (whole lines)
+  const int m0 = lane * 8, c0 = r0 * 4;
+  uint32_t in[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    in[i] = *reinterpret_cast<const uint32_t*>(tile + (m0 + i) * kPitch + c0);
+  u32x2 out[4];
+  transpose8x4(in, out);
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<u32x2*>(qt + (int64_t)(c0 + c) * ldqt + m0) = out[c];
+  __syncthreads();
+}
+
+// The block's rows as codes per 1x128 tile (rows past M are not stored).
+__device__ __forceinline__ void store_rows(const float (&v)[kRows][8], int64_t row0, int64_t M,
+                                           uint8_t* q, int64_t ldq, float* s) {
+  const int lane = threadIdx.x & 15;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    float m = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) m = fmaxf(m, fabsf(v[i][c]));
+    float sc, r;
+    group_scale(max_row16(m), sc, r);
+    const int64_t row = row0 + 32 * i;
+    const float rr[8] = {r, r, r, r, r, r, r, r};
+    const u32x2 w = codes8(v[i], rr);
+    if (row < M) {
+      __builtin_nontemporal_store(w, reinterpret_cast<u32x2*>(q + row * ldq + lane * 8));
+      if (lane == 0) s[row] = sc;
+    }
+  }
+}
+
+template <int ACT>
+__global__ __launch_bounds__(kThreads) void gated_backward_kernel(GatedGradArgs a) {
+  __shared__ float cmax[kThreads / 64][128];
+  __shared__ float rcp[128];
+  __shared__ __attribute__((aligned(16))) uint8_t tile[128 * kPitch];
+  const int64_t NB = a.N / 128;
+  const int64_t nb = blockIdx.x % NB, mb = blockIdx.x / NB;
+  const int lane = threadIdx.x & 15;
+  const int64_t row0 = mb * 128 + (threadIdx.x >> 4), col = nb * 128 + lane * 8;
+  float dg[kRows][8], du[kRows][8], y[kRows][8];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int64_t row = row0 + 32 * i;
+    const int64_t rc = row < a.M ? row : a.M - 1;
+    const u32x4 vd = __builtin_nontemporal_load(
+        reinterpret_cast<const u32x4*>(a.dy + rc * a.lddy + col));
+    const u32x4 vg =
+        __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(a.z + rc * a.ldz + col));
+    const u32x4 vu =
+        __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(a.z + rc * a.ldz + a.N + col));
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float d = c & 1 ? bf16_hi(vd[c / 2]) : bf16_lo(vd[c / 2]);
+      const float g = c & 1 ? bf16_hi(vg[c / 2]) : bf16_lo(vg[c / 2]);
+      const float u = c & 1 ? bf16_hi(vu[c / 2]) : bf16_lo(vu[c / 2]);
+      const float ag = activate<ACT>(g);
+      dg[i][c] = d * u * activate_grad<ACT>(g);
+      du[i][c] = d * ag;
+      y[i][c] = ag * u;
+    }
+    if (row >= a.M) {  // padding: in no maximum, codes 0
+#pragma unroll
+      for (int c = 0; c < 8; ++c) dg[i][c] = du[i][c] = y[i][c] = 0.0f;
+    }
+  }
+  store_rows(dg, row0, a.M, a.q + nb * 128, a.ldq, a.s + nb * a.lds);
+  store_rows(du, row0, a.M, a.q + a.N + nb * 128, a.ldq, a.s + (NB + nb) * a.lds);
+  const int64_t n0 = nb * 128, m0 = mb * 128;
+  store_columns(dg, a.qt + n0 * a.ldqt + m0, a.ldqt, a.st + mb * a.ldst + n0, cmax, rcp, tile);
+  store_columns(du, a.qt + (a.N + n0) * a.ldqt + m0, a.ldqt, a.st + mb * a.ldst + a.N + n0, cmax,
+                rcp, tile);
+  if (a.yt)
+    store_columns(y, a.yt + n0 * a.ldyt + m0, a.ldyt, a.syt + mb * a.ldsyt + n0, cmax, rcp, tile);
+}
+
+}  // namespace
+
+hipError_t launch_gated_backward(const GatedGradArgs& a, int act, hipStream_t stream) {
+  const int64_t blocks = (a.M + 127) / 128 * (a.N / 128);
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)blocks), block(kThreads);
+  switch (act) {
+    case kActRelu: return launch_kernel(gated_backward_kernel<kActRelu>, grid, block, stream, a);
+    case kActSilu: return launch_kernel(gated_backward_kernel<kActSilu>, grid, block, stream, a);
+    case kActGelu: return launch_kernel(gated_backward_kernel<kActGelu>, grid, block, stream, a);
+    default: return launch_kernel(gated_backward_kernel<kActNone>, grid, block, stream, a);
+  }
+}
+
+}  // namespace fp8bs

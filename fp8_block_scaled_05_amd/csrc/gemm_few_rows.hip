@@ -52,6 +52,19 @@ using gemm::wait_vmcnt;
 constexpr int kWaves = 4;
 constexpr int kStages = 4;
 
+// What a kernel does with its finished sums: store them, apply a linear layer's
+// epilogue, or multiply gate and up sums.
+enum Mode { kStore, kEpilogue, kGated };
+
+// Gated product: a workgroup's R rows of W are 4 RC columns' gate and up rows,
+// four of the one and four of the other in turn, so that lane groups g and g ^ 1
+// hold gate and up sums of the same columns.  Row of W, relative to the
+// workgroup's first (gate) row, that LDS row r holds; up rows lie N further.
+template <Mode MODE>
+__device__ __forceinline__ int own_row(int r) {
+  return MODE == kGated ? 4 * (r >> 3) + (r & 3) : r;
+}
+
 template <int RC, int MT, bool FUSED>
 struct FewCfg {
   static constexpr int R = 8 * RC;                  // weight rows per workgroup
@@ -188,7 +201,39 @@ __device__ __forceinline__ void store_finished(const FewArgs& p, const Epilogue&
   store(static_cast<uint16_t*>(p.c), p.ldc);
 }
 
-template <int RC, int MT, bool FUSED, bool EPI>
+// The sums of 4 consecutive columns n .. n + 3 of row m: on even lane groups the
+// gate's, on odd ones the up projection's.  Every lane keeps its own (z), the
+// even groups store act(gate) up.  All lanes call; live: the outputs exist.
+__device__ __forceinline__ void store_gated(const FewArgs& p, const Epilogue& e, int64_t m,
+                                            int64_t n, bool up, bool live, v4f v) {
+  v4f other;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) other[r] = __shfl_xor(v[r], 16, 64);
+  if (!live) return;
+  auto store = [&](uint16_t* dst) {
+    if (reinterpret_cast<uintptr_t>(dst) % 8 == 0) {
+      *reinterpret_cast<u32x2*>(dst) = u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) dst[r] = f32_to_bf16_rne(v[r]);
+    }
+  };
+  if (e.z) store(e.z + m * e.ldz + (up ? p.N : 0) + n);
+  if (up) return;
+  with_activation(e.act, [&](auto act) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = activate<decltype(act)::value>(v[r]);
+  });
+  v *= other;
+  if (p.out_bf16) {
+    store(static_cast<uint16_t*>(p.c) + m * p.ldc + n);
+  } else {
+    float* const dst = static_cast<float*>(p.c) + m * p.ldc + n;  // the workspace: aligned
+    *reinterpret_cast<v4f*>(dst) = v;
+  }
+}
+
+template <int RC, int MT, bool FUSED, Mode MODE>
 __global__ __launch_bounds__(kWaves * 64) void few_rows_kteam_kernel(FewArgs p, Epilogue ep) {
 #if defined(__HIP_DEVICE_COMPILE__)
   using C = FewCfg<RC, MT, FUSED>;
@@ -202,8 +247,10 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_kteam_kernel(FewArgs p, 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   const int g = lane >> 4, l16 = lane & 15;
-  const int64_t row0 = (int64_t)blockIdx.x * C::R;
-  const int nrows = (int)((p.N - row0) < C::R ? (p.N - row0) : C::R);  // >= 1
+  // rows of W, or columns of the gated product
+  constexpr int OWN = MODE == kGated ? C::R / 2 : C::R;
+  const int64_t row0 = (int64_t)blockIdx.x * OWN;
+  const int nrows = (int)((p.N - row0) < OWN ? (p.N - row0) : OWN);  // >= 1
   const int64_t KB = p.K / 128;
   // this wave's K groups: wave, wave + 4, ... (T of them)
   const int T = KB > wave ? (int)((KB - wave + kWaves - 1) / kWaves) : 0;
@@ -224,8 +271,10 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_kteam_kernel(FewArgs p, 
 #pragma unroll
     for (int c = 0; c < RC; ++c) {
       const int r = 8 * c + (lane >> 3);
-      const int rr = r < nrows ? r : nrows - 1;
-      voff[c] = (uint32_t)rr * (uint32_t)p.ldb + (uint32_t)(((lane & 7) ^ lds_swizzle(r)) * 16);
+      const int own = own_row<MODE>(r);
+      uint32_t rr = own < nrows ? own : nrows - 1;
+      if (MODE == kGated && (r & 4)) rr += (uint32_t)p.N;
+      voff[c] = rr * (uint32_t)p.ldb + (uint32_t)(((lane & 7) ^ lds_swizzle(r)) * 16);
     }
     // W fragment reads: row 16 i + l16, K chunks 2g and 2g + 1
     const int slot0 = (2 * g) ^ lds_swizzle(l16);
@@ -243,13 +292,16 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_kteam_kernel(FewArgs p, 
     // (at most two); row tile i's lane rows 16 i + 4 g .. + 3 share one
     const int64_t NB = (p.N + 127) / 128;
     const int64_t nb_lo = row0 / 128;
-    int64_t nb_hi = (row0 + C::R - 1) / 128;
+    int64_t nb_hi = (row0 + OWN - 1) / 128;
     nb_hi = nb_hi < NB ? nb_hi : NB - 1;
     bool use_hi[RT];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) use_hi[i] = (row0 + 16 * i + 4 * g) / 128 != nb_lo;
+    for (int i = 0; i < RT; ++i)
+      use_hi[i] = (row0 + own_row<MODE>(16 * i + 4 * g)) / 128 != nb_lo;
     const float* sw_lo = p.sb + nb_lo * KB;
     const float* sw_hi = p.sb + nb_hi * KB;
+    // gated: floats from the gate's block scales to the up projection's
+    const int64_t up_scales = p.N / 128 * KB;
 
     const int last_kb = wave + kWaves * (T - 1);
     auto kb_of = [&](int t) -> int { return t < T ? wave + kWaves * t : last_kb; };
@@ -307,7 +359,12 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_kteam_kernel(FewArgs p, 
       __builtin_amdgcn_sched_barrier(0);
       wait_vmcnt<C::ADIST * RC + (C::ADIST - 1) * C::NA>();
       const int kb = kb_of(t);
-      const float swl = scalar_ld(sw_lo + kb), swh = scalar_ld(sw_hi + kb);
+      float swl = scalar_ld(sw_lo + kb), swh = scalar_ld(sw_hi + kb);
+      if constexpr (MODE == kGated) {
+        const float ul = scalar_ld(sw_lo + up_scales + kb), uh = scalar_ld(sw_hi + up_scales + kb);
+        swl = g & 1 ? ul : swl;
+        swh = g & 1 ? uh : swh;
+      }
       const uint8_t* st = stages[U];
       v8i wf[RT];
 #pragma unroll
@@ -415,10 +472,15 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_kteam_kernel(FewArgs p, 
       for (int w = 1; w < kWaves; ++w)
         sum += *reinterpret_cast<const v4f*>(red + ((w * NR + qq) * 64 + lane) * 4);
       const int64_t m = 16 * j + l16;
-      const int nl = 16 * i + 4 * g;  // first of the lane's 4 output columns
-      if (m >= p.M || nl >= nrows) continue;
+      // first of the lane's 4 output columns
+      const int nl = own_row<MODE>(16 * i + 4 * g);
       const int64_t n = row0 + nl;
-      if constexpr (EPI) {
+      if constexpr (MODE == kGated) {
+        store_gated(p, ep, m, n, g & 1, m < p.M && nl < nrows, sum);
+        continue;
+      }
+      if (m >= p.M || nl >= nrows) continue;
+      if constexpr (MODE == kEpilogue) {
         store_finished(p, ep, m, n, nrows - nl, sum);
         continue;
       }
@@ -472,7 +534,7 @@ struct SharedCfg {
   static_assert((S - 2) * CPW <= 63, "vmcnt range");
 };
 
-template <int RC, bool EPI>
+template <int RC, Mode MODE>
 __global__ __launch_bounds__(kWaves * 64) void few_rows_shared_kernel(FewArgs p, Epilogue ep) {
 #if defined(__HIP_DEVICE_COMPILE__)
   using C = SharedCfg<RC>;
@@ -491,8 +553,10 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_shared_kernel(FewArgs p,
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   const int g = lane >> 4, l16 = lane & 15;
-  const int64_t row0 = (int64_t)blockIdx.x * C::R;
-  const int nrows = (int)((p.N - row0) < C::R ? (p.N - row0) : C::R);  // >= 1
+  // rows of W, or columns of the gated product
+  constexpr int OWN = MODE == kGated ? C::R / 2 : C::R;
+  const int64_t row0 = (int64_t)blockIdx.x * OWN;
+  const int nrows = (int)((p.N - row0) < OWN ? (p.N - row0) : OWN);  // >= 1
   const int KB = (int)(p.K / 128);
 
   // copies: slot s of this wave is block b = 4 s + wave; blocks [0, RC) are
@@ -510,8 +574,10 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_shared_kernel(FewArgs p,
     is_w[sl] = b < RC;
     if (b < RC) {
       const int r = 8 * b + (lane >> 3);
-      const int rr = r < nrows ? r : nrows - 1;
-      voff[sl] = (uint32_t)rr * (uint32_t)p.ldb + (uint32_t)(((lane & 7) ^ lds_swizzle(r)) * 16);
+      const int own = own_row<MODE>(r);
+      uint32_t rr = own < nrows ? own : nrows - 1;
+      if (MODE == kGated && (r & 4)) rr += (uint32_t)p.N;
+      voff[sl] = rr * (uint32_t)p.ldb + (uint32_t)(((lane & 7) ^ lds_swizzle(r)) * 16);
       ldsoff[sl] = b * 1024;
     } else {
       const int r = 8 * (b - RC) + (lane >> 3);
@@ -552,13 +618,16 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_shared_kernel(FewArgs p,
   asm volatile("" : "+v"(f_lo), "+v"(f_hi), "+v"(a_lo), "+v"(a_hi));
   const int64_t NB = (p.N + 127) / 128;
   const int64_t nb_lo = row0 / 128;
-  int64_t nb_hi = (row0 + C::R - 1) / 128;
+  int64_t nb_hi = (row0 + OWN - 1) / 128;
   nb_hi = nb_hi < NB ? nb_hi : NB - 1;
   bool use_hi[RT];
 #pragma unroll
-  for (int i = 0; i < RT; ++i) use_hi[i] = (row0 + 16 * i + 4 * g) / 128 != nb_lo;
+  for (int i = 0; i < RT; ++i)
+    use_hi[i] = (row0 + own_row<MODE>(16 * i + 4 * g)) / 128 != nb_lo;
   const float* sw_lo = p.sb + nb_lo * KB;
   const float* sw_hi = p.sb + nb_hi * KB;
+  // gated: floats from the gate's block scales to the up projection's
+  const int64_t up_scales = p.N / 128 * KB;
 
   v4f acc[RT];
 #pragma unroll
@@ -575,7 +644,12 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_shared_kernel(FewArgs p,
     gemm::barrier_after_vmcnt<(S - 2) * C::CPW>();
     uint8_t* const nxt = stages[(U + S - 1) % S];
     const uint8_t* st = stages[U];
-    const float swl = scalar_ld(sw_lo + t), swh = scalar_ld(sw_hi + t);
+    float swl = scalar_ld(sw_lo + t), swh = scalar_ld(sw_hi + t);
+    if constexpr (MODE == kGated) {
+      const float ul = scalar_ld(sw_lo + up_scales + t), uh = scalar_ld(sw_hi + up_scales + t);
+      swl = g & 1 ? ul : swl;
+      swh = g & 1 ? uh : swh;
+    }
     const v8i af = gemm::load_frag(st, a_lo, a_hi, 0);
     const float fa = reinterpret_cast<const float*>(st + C::SC_OFF)[ar];
     v4f prev;
@@ -613,7 +687,13 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_shared_kernel(FewArgs p,
 
   // --- store: wave w holds C[16 w + l16][row0 + 16 i + 4 g + r] ---
   const int64_t m = ar;
-  if (m < p.M) {
+  if constexpr (MODE == kGated) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int nl = own_row<MODE>(16 * i + 4 * g);
+      store_gated(p, ep, m, row0 + nl, g & 1, m < p.M && nl < nrows, acc[i]);
+    }
+  } else if (m < p.M) {
     const bool vec = p.ldc % 4 == 0 &&
                      reinterpret_cast<uintptr_t>(p.c) % (p.out_bf16 ? 8 : 16) == 0;
 #pragma unroll
@@ -622,7 +702,7 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_shared_kernel(FewArgs p,
       if (nl >= nrows) continue;
       const int64_t n = row0 + nl;
       const v4f sum = acc[i];
-      if constexpr (EPI) {
+      if constexpr (MODE == kEpilogue) {
         store_finished(p, ep, m, n, nrows - nl, sum);
         continue;
       }
@@ -649,37 +729,69 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_shared_kernel(FewArgs p,
 }
 
 // Weight rows per workgroup (RC 8-row copies): the fewest that put the
-// whole N on at most one workgroup per compute unit, from a fixed set.
-template <int MT, bool FUSED>
-hipError_t launch_mt(const FewArgs& p, const Epilogue* e, int cus, hipStream_t stream) {
-  const int64_t per = (p.N + cus - 1) / cus;
+// whole W on at most one workgroup per compute unit, from a fixed set.
+template <class F>
+hipError_t with_rows(const FewArgs& p, Mode mode, int cus, F&& f) {
+  const int64_t rows = mode == kGated ? 2 * p.N : p.N;
+  const int64_t per = (rows + cus - 1) / cus;
   auto go = [&](auto RC_) {
     constexpr int RC = decltype(RC_)::value;
-    const int64_t blocks = (p.N + 8 * RC - 1) / (8 * RC);
+    const int64_t blocks = (rows + 8 * RC - 1) / (8 * RC);
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)blocks), block(kWaves * 64);
-    if (e) return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, true>, grid, block, stream, p, *e);
-    return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, false>, grid, block, stream, p,
-                         Epilogue{});
+    return f(RC_, dim3((unsigned)blocks));
   };
   if (per <= 8) return go(std::integral_constant<int, 1>{});
   if (per <= 24) return go(std::integral_constant<int, 3>{});
   return go(std::integral_constant<int, 9>{});
 }
 
-hipError_t launch_shared(const FewArgs& p, const Epilogue* e, int cus, hipStream_t stream) {
-  const int64_t per = (p.N + cus - 1) / cus;
-  auto go = [&](auto RC_) {
+template <int MT, bool FUSED>
+hipError_t launch_mt(const FewArgs& p, Mode mode, const Epilogue& e, int cus, hipStream_t stream) {
+  return with_rows(p, mode, cus, [&](auto RC_, dim3 grid) {
     constexpr int RC = decltype(RC_)::value;
-    const int64_t blocks = (p.N + 8 * RC - 1) / (8 * RC);
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)blocks), block(kWaves * 64);
-    if (e) return launch_kernel(few_rows_shared_kernel<RC, true>, grid, block, stream, p, *e);
-    return launch_kernel(few_rows_shared_kernel<RC, false>, grid, block, stream, p, Epilogue{});
-  };
-  if (per <= 8) return go(std::integral_constant<int, 1>{});
-  if (per <= 24) return go(std::integral_constant<int, 3>{});
-  return go(std::integral_constant<int, 9>{});
+    const dim3 block(kWaves * 64);
+    switch (mode) {
+      case kGated:
+        return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kGated>, grid, block, stream, p,
+                             e);
+      case kEpilogue:
+        return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kEpilogue>, grid, block, stream,
+                             p, e);
+      default:
+        return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kStore>, grid, block, stream, p,
+                             e);
+    }
+  });
+}
+
+hipError_t launch_shared(const FewArgs& p, Mode mode, const Epilogue& e, int cus,
+                         hipStream_t stream) {
+  return with_rows(p, mode, cus, [&](auto RC_, dim3 grid) {
+    constexpr int RC = decltype(RC_)::value;
+    const dim3 block(kWaves * 64);
+    switch (mode) {
+      case kGated:
+        return launch_kernel(few_rows_shared_kernel<RC, kGated>, grid, block, stream, p, e);
+      case kEpilogue:
+        return launch_kernel(few_rows_shared_kernel<RC, kEpilogue>, grid, block, stream, p, e);
+      default:
+        return launch_kernel(few_rows_shared_kernel<RC, kStore>, grid, block, stream, p, e);
+    }
+  });
+}
+
+hipError_t launch_few_rows(const FewArgs& p, bool fused, Mode mode, const Epilogue& e,
+                           hipStream_t stream) {
+  const int cus = gemm::device_cus();
+  if (cus <= 0) return hipErrorInvalidDevice;
+  if (fused) {
+    if (p.M > kFewRowsFused) return hipErrorInvalidValue;
+    return launch_mt<1, true>(p, mode, e, cus, stream);
+  }
+  if (p.M <= 16) return launch_mt<1, false>(p, mode, e, cus, stream);
+  if (p.M <= 32) return launch_mt<2, false>(p, mode, e, cus, stream);
+  if (p.M <= kFewRows) return launch_shared(p, mode, e, cus, stream);
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
@@ -689,17 +801,23 @@ hipError_t launch_few_rows_gemm(const void* a, int64_t lda, float* sa, int64_t l
                                 int64_t ldc, bool out_bf16, int64_t M, int64_t N, int64_t K,
                                 hipStream_t stream, const Epilogue* epilogue) {
   const FewArgs p{a, lda, sa, ldsa, b, ldb, sb, c, ldc, M, N, K, out_bf16 ? 1 : 0};
-  const int cus = gemm::device_cus();
-  if (cus <= 0) return hipErrorInvalidDevice;
   if (epilogue && !out_bf16) return hipErrorInvalidValue;
-  if (fused) {
-    if (M > kFewRowsFused) return hipErrorInvalidValue;
-    return launch_mt<1, true>(p, epilogue, cus, stream);
-  }
-  if (M <= 16) return launch_mt<1, false>(p, epilogue, cus, stream);
-  if (M <= 32) return launch_mt<2, false>(p, epilogue, cus, stream);
-  if (M <= kFewRows) return launch_shared(p, epilogue, cus, stream);
-  return hipErrorInvalidValue;
+  return launch_few_rows(p, fused, epilogue ? kEpilogue : kStore, epilogue ? *epilogue : Epilogue{},
+                         stream);
+}
+
+// The copies address a workgroup's gate and up rows from its first gate row.
+bool few_rows_gated_fits(int64_t N, int64_t ldb) {
+  return (N + 64) * ldb <= int64_t(0xFFFFFFFF);
+}
+
+hipError_t launch_few_rows_gated(const void* a, int64_t lda, float* sa, int64_t ldsa, bool fused,
+                                 const uint8_t* b, int64_t ldb, const float* sb, void* c,
+                                 int64_t ldc, bool out_bf16, int64_t M, int64_t N, int64_t K,
+                                 const Gate& gate, hipStream_t stream) {
+  const FewArgs p{a, lda, sa, ldsa, b, ldb, sb, c, ldc, M, N, K, out_bf16 ? 1 : 0};
+  return launch_few_rows(p, fused, kGated,
+                         Epilogue{nullptr, nullptr, 0, gate.z, gate.ldz, gate.act}, stream);
 }
 
 }  // namespace fp8bs

@@ -63,6 +63,9 @@ struct Cfg {
   static constexpr int SB_COUNT = (BN + 127) / 128;
   // B scales per 128x128 block (false) or per row and K group (RowScaledB)
   static constexpr bool ROWB = false;
+  // columns of C per tile (half of the tile's B rows with GatedB)
+  static constexpr bool GATED = false;
+  static constexpr int BNO = BN;
   // block-scaled B: the staged scales are the promotion factors
   // S_A(row) * S_W(block) for each of the tile's SB_COUNT weight blocks
   static constexpr bool PREMUL = true;
@@ -106,6 +109,25 @@ struct RowScaledB : C {
   static constexpr int SREG = (SCALE_ITEMS + C::THREADS - 1) / C::THREADS;
   static constexpr int SCALE_FLOATS = SREG * C::THREADS;
   static constexpr int LOADS = C::TILE_LOADS + SREG;
+  static_assert(LOADS <= 63, "vmcnt range");
+};
+
+// The same tile configuration for the gated product, whose B holds 2N rows:
+// the gate's, then the up projection's.  A tile's first BN/2 B rows are BN/2
+// columns' gate rows, the others the same columns' up rows, so that one half of
+// the waves along N forms the gate and the other half the up projection, each
+// with one weight block, as in the plain product.  N is a multiple of 128.
+template <class C>
+struct GatedB : C {
+  static constexpr bool GATED = true;
+  static constexpr int BNO = C::BN / 2;
+  // factor items: the gate's weight block, then the up projection's
+  static constexpr int SB_COUNT = 2;
+  static constexpr int SCALE_ITEMS = 2 * C::BM;
+  static constexpr int SREG = (SCALE_ITEMS + C::THREADS - 1) / C::THREADS;
+  static constexpr int SCALE_FLOATS = SREG * C::THREADS;
+  static constexpr int LOADS = C::TILE_LOADS + 2 * SREG;
+  static_assert(C::WN % 2 == 0 && BNO <= 128, "a half's columns share one weight block");
   static_assert(LOADS <= 63, "vmcnt range");
 };
 
@@ -158,13 +180,13 @@ __device__ __forceinline__ int64_t xcd_remap(int64_t bid, int64_t T) {
 template <class C>
 __device__ __forceinline__ void raster(const GemmArgs& p, int64_t i, int64_t MT, int64_t& tm,
                                        int64_t& col0) {
-  const int64_t NT = (p.N + C::BN - 1) / C::BN;
+  const int64_t NT = (p.N + C::BNO - 1) / C::BNO;
   const int64_t per_group = (int64_t)C::GROUP_M * NT;
   const int64_t first_m = (i / per_group) * C::GROUP_M;
   const int64_t gsz = (MT - first_m) < C::GROUP_M ? (MT - first_m) : C::GROUP_M;
   const int64_t in_grp = i % per_group;
   tm = first_m + in_grp % gsz;
-  col0 = (in_grp / gsz) * C::BN;
+  col0 = (in_grp / gsz) * C::BNO;
 }
 
 template <class C>
@@ -249,7 +271,7 @@ __device__ __forceinline__ int64_t grouped_row_tiles(const GemmArgs& p) {
 template <class C>
 __device__ __forceinline__ void grouped_tile(const GemmArgs& p, int64_t i, int64_t MT,
                                              TileCoords& t) {
-  const int64_t NB = (p.N + 127) / 128;
+  const int64_t NB = (p.N + 127) / 128 * (C::GATED ? 2 : 1);
   const int lane = threadIdx.x & 63;
   int64_t tm;
   raster<C>(p, i, MT, tm, t.col0);
@@ -316,7 +338,8 @@ __device__ __forceinline__ void make_plan(const GemmArgs& p, const TileCoords& t
       // 16 f + l of a wave's block holds tile column FN l + f, so the lane
       // that produces MFMA column l of fragment f holds, over f, FN
       // consecutive output columns (one vector store per output row)
-      const int rb = r - C::BM, wb = rb / C::TN, rw = rb % C::TN;
+      const int rb = r - C::BM, rw = rb % C::TN;
+      const int wb = rb / C::TN % (C::GATED ? C::WN / 2 : C::WN);
       const int col = wb * C::TN + C::FN * (rw % 16) + rw / 16;
       const int rr = col < rows_b ? col : rows_b - 1;
       lp.tile[j] = (uint32_t)rr * (uint32_t)p.ldb + chunk * 16;
@@ -333,7 +356,7 @@ __device__ __forceinline__ void make_plan(const GemmArgs& p, const TileCoords& t
       int nb = item / C::BM;
       nb = nb < C::SB_COUNT ? nb : C::SB_COUNT - 1;
       lp.scale[s] = row < rows_a ? row : rows_a - 1;
-      lp.scaleb[s] = (int)((nb < nbl ? nb : nbl) * p.sb_ld);
+      lp.scaleb[s] = (int)((C::GATED ? nb * NB : nb < nbl ? nb : nbl) * p.sb_ld);
     } else if (item < C::BM) {
       lp.scale[s] = item < rows_a ? item : rows_a - 1;
     } else {
@@ -349,6 +372,7 @@ __device__ __forceinline__ void make_plan(const GemmArgs& p, const TileCoords& t
 // rows past the edge are clamped to the last valid row.
 struct Rsrc {
   __amdgpu_buffer_rsrc_t a, b;
+  __amdgpu_buffer_rsrc_t up;  // GatedB: the up projection's rows
 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base) {
@@ -363,6 +387,7 @@ __device__ __forceinline__ Rsrc make_rsrc_set(const GemmArgs& p, const TileCoord
   Rsrc r;
   r.a = make_rsrc(p.a + t.row0 * p.lda + t.kb0 * 128);
   r.b = make_rsrc(t.b + t.col0 * p.ldb + t.kb0 * 128);
+  if constexpr (C::GATED) r.up = make_rsrc(t.b + (p.N + t.col0) * p.ldb + t.kb0 * 128);
   return r;
 }
 
@@ -374,7 +399,8 @@ __device__ __forceinline__ void issue_copy(const GemmArgs& p, const Rsrc& rs,
                                            int wave, int idx) {
   (void)p;
   const int rbase = (wave * C::TILE_LOADS + idx) * 8;
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rbase < C::BM ? rs.a : rs.b,
+  const bool up = C::GATED && rbase >= C::BM + C::BN / 2;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rbase < C::BM ? rs.a : up ? rs.up : rs.b,
                                            (lds_void*)(st + rbase * 128), 16, lp.tile[idx],
                                            (int)(kb * 128), 0, 0);
 }
@@ -445,7 +471,8 @@ __device__ __forceinline__ FragOffs frag_offsets(int wm, int wn, int lane) {
   f.a_hi = C::A_OFF + (wm * C::TM + l16) * 128 + (slot0 ^ 1) * 16;
   f.b_lo = C::B_OFF + (wn * C::TN + l16) * 128 + slot0 * 16;
   f.b_hi = C::B_OFF + (wn * C::TN + l16) * 128 + (slot0 ^ 1) * 16;
-  f.sa = wm * C::TM + 4 * (lane >> 4) + (C::PREMUL ? (wn * C::TN) / 128 * C::BM : 0);
+  const int block = C::GATED ? wn / (C::WN / 2) : wn * C::TN / 128;
+  f.sa = wm * C::TM + 4 * (lane >> 4) + (C::PREMUL ? block * C::BM : 0);
   // the lane's FN output columns are consecutive (permuted B staging)
   f.sbc = C::BM + wn * C::TN + C::FN * l16;
   asm volatile("" : "+v"(f.a_lo), "+v"(f.a_hi), "+v"(f.b_lo), "+v"(f.b_hi), "+v"(f.sa));
@@ -754,7 +781,8 @@ struct NoEpilogue {
 
 // ep.load<C>(p, t, wm, wn, lane, early) may load operands of its own before the
 // K loop; ep.apply<C>(p, t, acc, wm, wn, lane, early) may change a wave's
-// finished sums before they are stored.
+// finished sums before they are stored.  With GatedB, ep.finish<C, OUT>(p, t,
+// acc, wm, wn, lane, L) takes the sums and stores all there is.
 template <class C, int OUT, class E = NoEpilogue>
 __device__ __forceinline__ void block_gemm_body(const GemmArgs& p, const TileCoords& t,
                                                 const LdsSet& L, const E& ep = E()) {
@@ -875,11 +903,15 @@ __device__ __forceinline__ void block_gemm_body(const GemmArgs& p, const TileCoo
     }
   }
 
-  ep.template apply<C>(p, t, acc, wm, wn, lane, early);
-  if constexpr (OUT == kOutE4M3) {
-    store_tile_e4m3<C>(p, t, acc, wm, wn, lane, L.red, L.rcp);
+  if constexpr (C::GATED) {
+    ep.template finish<C, OUT>(p, t, acc, wm, wn, lane, L);
   } else {
-    store_tile<C, OUT, E::kStream>(p, t, acc, wm, wn, lane);
+    ep.template apply<C>(p, t, acc, wm, wn, lane, early);
+    if constexpr (OUT == kOutE4M3) {
+      store_tile_e4m3<C>(p, t, acc, wm, wn, lane, L.red, L.rcp);
+    } else {
+      store_tile<C, OUT, E::kStream>(p, t, acc, wm, wn, lane);
+    }
   }
 }
 
@@ -933,7 +965,7 @@ __device__ __forceinline__ void block_gemm_tile(const GemmArgs& p, int64_t full,
   if constexpr (SCHED == kGroupRows) {
     (void)full;
     const int64_t MT = grouped_row_tiles<C>(p);
-    const int64_t T = MT * ((p.N + C::BN - 1) / C::BN);
+    const int64_t T = MT * ((p.N + C::BNO - 1) / C::BNO);
     if (bid >= T) return;  // whole workgroup: past the last real tile
     // tiles dealt round-robin over the XCDs (not in contiguous runs): the
     // groups' short last tile-rows and the raster's end then spread evenly
@@ -1019,7 +1051,7 @@ inline int device_cus() {
 // large.
 template <class C, int SCHED, class TAIL>
 int64_t grid_size(const GemmArgs& args, int64_t& full) {
-  const int64_t NT = (args.N + C::BN - 1) / C::BN;
+  const int64_t NT = (args.N + C::BNO - 1) / C::BNO;
   int64_t MT = (args.M + C::BM - 1) / C::BM;
   // grouped rows: every non-empty group adds at most one partial tile-row,
   // and every tile-row holds at least one row

@@ -143,4 +143,97 @@ hipError_t launch_xent_backward(const uint16_t* x, int64_t ldx, const uint16_t* 
                                 int64_t lddw, int64_t M, int64_t V, int64_t K, void* workspace,
                                 hipStream_t stream);
 
+// Root-mean-square norm: h = RN_bf16(x + residual), y = h rstd weight, in E4M3
+// codes per 1x128 tile (q, s) and / or bf16 (y).  residual, h, y, rstd and the
+// pair q, s may be null.  K is a multiple of 128, at most kMaxNormK.
+constexpr int64_t kMaxNormK = 32768;
+struct NormArgs {
+  const uint16_t* x;
+  int64_t ldx;
+  const uint16_t* residual;
+  int64_t ldr;
+  const float* weight;
+  float eps;
+  uint16_t* h;
+  int64_t ldh;
+  uint16_t* y;
+  int64_t ldy;
+  float* rstd;
+  uint8_t* q;
+  int64_t ldq;
+  float* s;
+  int64_t lds;
+  int64_t M, K;
+};
+hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t stream);
+
+// Its backward pass: dx (with dh added, if given) and the sums dg for the
+// weight.  workspace: rmsnorm_backward_workspace bytes; M may be 0.
+struct NormGradArgs {
+  const uint16_t* dy;
+  int64_t lddy;
+  const uint16_t* h;
+  int64_t ldh;
+  const float* rstd;
+  const float* weight;
+  const uint16_t* dh;
+  int64_t lddh;
+  uint16_t* dx;
+  int64_t lddx;
+  float* part;  // set by the launcher
+  int64_t M, K;
+};
+size_t rmsnorm_backward_workspace(int64_t M, int64_t K);
+hipError_t launch_rmsnorm_backward(NormGradArgs a, float* dg, void* workspace,
+                                   hipStream_t stream);
+
+// Gated product: the weight's first N rows are the gate's, the next N the up
+// projection's; y = act(gate) up, with both sums kept in bf16 [M][2N] if z.
+// N (the output's columns) is a multiple of 128.
+struct Gate {
+  uint16_t* z;  // [M][ldz]
+  int64_t ldz;
+  int act;
+};
+hipError_t launch_block_gemm_gated(const GemmArgs& args, const Gate& gate, OutKind out,
+                                   hipStream_t stream);
+hipError_t launch_grouped_gemm_gated(const GemmArgs& args, const Gate& gate, OutKind out,
+                                     hipStream_t stream);
+// Few rows (M <= kFewRows, fused as launch_few_rows_gemm); fp32 or bf16 output.
+// False where the weight's rows are too far apart for its 32-bit offsets.
+bool few_rows_gated_fits(int64_t N, int64_t ldb);
+hipError_t launch_few_rows_gated(const void* a, int64_t lda, float* sa, int64_t ldsa, bool fused,
+                                 const uint8_t* b, int64_t ldb, const float* sb, void* c,
+                                 int64_t ldc, bool out_bf16, int64_t M, int64_t N, int64_t K,
+                                 const Gate& gate, hipStream_t stream);
+// fp32 [M][N] -> E4M3 codes and scales per 1x128 tile.
+hipError_t launch_quant_f32(const float* x, int64_t M, int64_t N, uint8_t* q, int64_t ldq,
+                            float* s, int64_t lds, hipStream_t stream);
+
+// Backward of the gated product up to the operands of its backward GEMMs: from
+// dy bf16 [M][N] and z bf16 [M][2N] (gate, up), dz = (dy up act'(gate) |
+// dy act(gate)) as codes per 1x128 tile (q, s) and, rows zero-padded to a
+// multiple of 128, per 128 rows and transposed (qt, st); with yt also the
+// product y = act(gate) up, transposed in the same way (yt, syt).
+struct GatedGradArgs {
+  const uint16_t* dy;
+  int64_t lddy;
+  const uint16_t* z;
+  int64_t ldz;
+  int64_t M, N;
+  uint8_t* q;
+  int64_t ldq;
+  float* s;
+  int64_t lds;
+  uint8_t* qt;
+  int64_t ldqt;
+  float* st;
+  int64_t ldst;
+  uint8_t* yt;
+  int64_t ldyt;
+  float* syt;
+  int64_t ldsyt;
+};
+hipError_t launch_gated_backward(const GatedGradArgs& a, int act, hipStream_t stream);
+
 }  // namespace fp8bs

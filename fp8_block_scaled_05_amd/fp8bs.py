@@ -19,7 +19,7 @@ OK, ERR_NULL, ERR_SHAPE, ERR_LAYOUT, ERR_DTYPE, ERR_WORKSPACE, ERR_HIP = range(7
 OUT_F32, OUT_BF16 = 0, 1
 A_E4M3, A_BF16 = 0, 1
 OP_QUANT_ACT, OP_QUANT_W, OP_GEMM_E4M3, OP_GEMM_BF16, OP_GROUPED_GEMM, OP_XENT, \
-    OP_XENT_BACKWARD, OP_EPILOGUE_BACKWARD = range(8)
+    OP_XENT_BACKWARD, OP_EPILOGUE_BACKWARD, OP_GEMM_GATED_E4M3, OP_RMSNORM_BACKWARD = range(10)
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}  # FP8BS_ACT_*
 NOALLOC_SCRATCH_BYTES = 8 * 1024 * 1024  # FP8BS_NOALLOC_SCRATCH_BYTES
 DELAY_TILE, DELAY_TENSOR = 0, 1
@@ -39,6 +39,14 @@ EXPORTS = (
     "fp8_block_gemm_epilogue",
     "fp8_block_gemm_epilogue_e4m3_out",
     "fp8_quant_epilogue_backward",
+    "fp8_block_gemm_gated",
+    "fp8_block_gemm_gated_e4m3_out",
+    "fp8_block_grouped_gemm_gated",
+    "fp8_block_grouped_gemm_gated_e4m3_out",
+    "fp8_quant_gated_backward",
+    "fp8_quant_rmsnorm",
+    "bf16_rmsnorm",
+    "bf16_rmsnorm_backward",
     "fp8_block_gemm_rowscaled",
     "fp8_block_kgrouped_gemm_rowscaled",
     "bf16_linear_xent",
@@ -51,6 +59,7 @@ EXPORTS = (
 _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
+_f32 = ctypes.c_float
 _sz = ctypes.c_size_t
 
 
@@ -92,6 +101,22 @@ _SIGNATURES = {
                                           _p, _i64, _i64, _i64, _i64, _p, _sz, _p], _int),
     "fp8_quant_epilogue_backward": ([_p, _i64, _p, _i64, _int, _i64, _i64, _p, _i64, _p, _i64, _p,
                                      _i64, _p, _i64, _p, _p, _sz, _p], _int),
+    "fp8_block_gemm_gated": ([_int, _p, _i64, _p, _i64, _p, _i64, _p, _int, _p, _i64, _p, _i64, _i64,
+                              _i64, _i64, _p, _sz, _p], _int),
+    "fp8_block_gemm_gated_e4m3_out": ([_int, _p, _i64, _p, _i64, _p, _i64, _p, _int, _p, _i64, _p,
+                                       _i64, _p, _i64, _i64, _i64, _i64, _p, _sz, _p], _int),
+    "fp8_block_grouped_gemm_gated": ([_p, _i64, _p, _i64, _p, _i64, _i64, _p, _int, _p, _i64, _p,
+                                      _i64, _p, _i64, _i64, _i64, _i64, _p], _int),
+    "fp8_block_grouped_gemm_gated_e4m3_out": ([_p, _i64, _p, _i64, _p, _i64, _i64, _p, _int, _p,
+                                               _i64, _p, _i64, _p, _i64, _p, _i64, _i64, _i64,
+                                               _i64, _p], _int),
+    "fp8_quant_gated_backward": ([_p, _i64, _p, _i64, _int, _i64, _i64, _p, _i64, _p, _i64, _p,
+                                  _i64, _p, _i64, _p, _i64, _p, _i64, _p], _int),
+    "fp8_quant_rmsnorm": ([_p, _i64, _p, _i64, _p, _f32, _p, _i64, _p, _i64, _p, _p, _i64, _p,
+                           _i64, _i64, _i64, _p], _int),
+    "bf16_rmsnorm": ([_p, _i64, _p, _i64, _p, _f32, _p, _i64, _p, _p, _i64, _i64, _i64, _p], _int),
+    "bf16_rmsnorm_backward": ([_p, _i64, _p, _i64, _p, _p, _p, _i64, _p, _i64, _p, _i64, _i64, _p,
+                               _sz, _p], _int),
     "bf16_linear_xent": ([_p, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _i64, _i64, _p, _sz, _p],
                          _int),
     "bf16_linear_xent_backward": ([_p, _i64, _p, _i64, _p, _i64, _p, _p, _p, _i64, _p, _i64, _i64,
@@ -741,6 +766,234 @@ def fp8_quant_epilogue_backward(dy, z, act="none", q=None, s=None, qt=None, st=N
             _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(dy)),
             "fp8_quant_epilogue_backward")
     return q, s, qt, st, dbias
+
+
+def _gated_columns(rows, where):
+    """Columns of the gated product's output, from its weight's rows."""
+    if rows % 256 != 0:
+        raise ValueError(f"{where}: b has {rows} rows, gate and up need a multiple of 128 each")
+    return rows // 2
+
+
+def fp8_block_gemm_gated(a, sa, b, sb, act="silu", z=None, out=None, workspace=None):
+    """Gated product of a feed-forward block: with ``b`` [2N][K] the gate's rows,
+    then the up projection's, returns act(A . Wg^T) * (A . Wu^T) in bf16 [M][N].
+
+    ``a``, ``sa`` as ``fp8_block_gemm``; ``act`` as ``fp8_block_gemm_epilogue``;
+    ``z`` an optional bf16 [M][2N] output that receives gate and up, what the
+    backward pass needs (``fp8_quant_gated_backward``).  N is a multiple of 128.
+    """
+    a_kind, M, N2, K, lda, ldsa, ldb = _dense_operands("fp8_block_gemm_gated", a, sa, b, sb)
+    N = _gated_columns(N2, "fp8_block_gemm_gated")
+    act = _act_id(act)
+    ldz = _mat(z, "z", M, N2, torch.bfloat16)
+    _mat(out, "out", M, N, torch.bfloat16)
+    _need_device(a, sa, b, sb, z, out, workspace)
+    if out is None:
+        out = torch.empty(M, N, dtype=torch.bfloat16, device=a.device)
+    workspace, ws_bytes = _workspace(a_kind, M, N, K, workspace, a.device)
+    with _on(a.device):
+        _check(lib.fp8_block_gemm_gated(a_kind, _ptr(a), lda, _ptr(sa), ldsa, _ptr(b), ldb,
+                                        _ptr(sb), act, _ptr(z), ldz, _ptr(out), _ld(out), M, N, K,
+                                        _ptr(workspace), ws_bytes, _stream(a)),
+               "fp8_block_gemm_gated")
+    return out
+
+
+def fp8_block_gemm_gated_e4m3_out(a, sa, b, sb, act="silu", z=None, qc=None, sc=None,
+                                  workspace=None):
+    """As ``fp8_block_gemm_gated``, with the result quantized per 1x128 tile
+    along N: returns ``(qc, sc)`` as ``fp8_block_gemm_e4m3_out``."""
+    a_kind, M, N2, K, lda, ldsa, ldb = _dense_operands("fp8_block_gemm_gated_e4m3_out", a, sa, b,
+                                                       sb)
+    N = _gated_columns(N2, "fp8_block_gemm_gated_e4m3_out")
+    act = _act_id(act)
+    ldz = _mat(z, "z", M, N2, torch.bfloat16)
+    _e4m3_check(M, N, qc, sc)
+    _need_device(a, sa, b, sb, z, qc, sc, workspace)
+    qc, sc = _e4m3_outputs(M, N, qc, sc, a.device)
+    if workspace is None and (a_kind == A_BF16 or M <= 64):
+        workspace = torch.empty(workspace_bytes(OP_GEMM_GATED_E4M3, M, N, K), dtype=torch.uint8,
+                                device=a.device)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    with _on(a.device):
+        _check(lib.fp8_block_gemm_gated_e4m3_out(
+            a_kind, _ptr(a), lda, _ptr(sa), ldsa, _ptr(b), ldb, _ptr(sb), act, _ptr(z), ldz,
+            _ptr(qc), _ld(qc), _ptr(sc), _ld(sc), M, N, K, _ptr(workspace), ws_bytes, _stream(a)),
+            "fp8_block_gemm_gated_e4m3_out")
+    return qc, sc
+
+
+def fp8_block_grouped_gemm_gated(a, sa, b, sb, group_offsets, act="silu", z=None, out=None):
+    """``fp8_block_gemm_gated`` of every expert's rows: operands as
+    ``fp8_block_grouped_gemm`` with ``b`` uint8 [G][2N][K] and ``sb`` fp32
+    [G][2N/128][K/128]; returns bf16 [M_total][N]."""
+    M, G, N2, K = _grouped_operands("fp8_block_grouped_gemm_gated", a, sa, b, sb, group_offsets)
+    N = _gated_columns(N2, "fp8_block_grouped_gemm_gated")
+    act = _act_id(act)
+    ldz = _mat(z, "z", M, N2, torch.bfloat16)
+    _mat(out, "out", M, N, torch.bfloat16)
+    _need_device(a, sa, b, sb, group_offsets, z, out)
+    if out is None:
+        out = torch.empty(M, N, dtype=torch.bfloat16, device=a.device)
+    with _on(a.device):
+        _check(lib.fp8_block_grouped_gemm_gated(
+            _ptr(a), _ld(a), _ptr(sa), _ld(sa), _ptr(b), b.stride(1), b.stride(0), _ptr(sb), act,
+            _ptr(z), ldz, _ptr(out), _ld(out), _ptr(group_offsets), G, M, N, K, _stream(a)),
+            "fp8_block_grouped_gemm_gated")
+    return out
+
+
+def fp8_block_grouped_gemm_gated_e4m3_out(a, sa, b, sb, group_offsets, act="silu", z=None,
+                                          qc=None, sc=None):
+    """As ``fp8_block_grouped_gemm_gated``, with the result quantized per 1x128
+    tile along N: returns ``(qc, sc)`` as ``fp8_block_gemm_e4m3_out``."""
+    M, G, N2, K = _grouped_operands("fp8_block_grouped_gemm_gated_e4m3_out", a, sa, b, sb,
+                                    group_offsets)
+    N = _gated_columns(N2, "fp8_block_grouped_gemm_gated_e4m3_out")
+    act = _act_id(act)
+    ldz = _mat(z, "z", M, N2, torch.bfloat16)
+    _e4m3_check(M, N, qc, sc)
+    _need_device(a, sa, b, sb, group_offsets, z, qc, sc)
+    qc, sc = _e4m3_outputs(M, N, qc, sc, a.device)
+    with _on(a.device):
+        _check(lib.fp8_block_grouped_gemm_gated_e4m3_out(
+            _ptr(a), _ld(a), _ptr(sa), _ld(sa), _ptr(b), b.stride(1), b.stride(0), _ptr(sb), act,
+            _ptr(z), ldz, _ptr(qc), _ld(qc), _ptr(sc), _ld(sc), _ptr(group_offsets), G, M, N, K,
+            _stream(a)), "fp8_block_grouped_gemm_gated_e4m3_out")
+    return qc, sc
+
+
+def fp8_quant_gated_backward(dy, z, act="silu", q=None, s=None, qt=None, st=None, yt=None,
+                             syt=None, product=True):
+    """Backward of the gated product up to the backward GEMMs' operands: from bf16
+    ``dy`` [M][N] and the kept ``z`` [M][2N] (gate, up), dz = (dy up act'(gate) |
+    dy act(gate)) as
+
+    ``(q, s)``: E4M3 codes [M][2N], scales [2N/128][M], the (a, sa) of the data
+    gradient (contraction 2N); ``(qt, st)``: codes [2N][Mp], scales [Mp/128][2N],
+    Mp = M rounded up to 128 (zero padding), the (a, sa) of the weight gradient;
+    and y = act(gate) up again as ``(yt, syt)``: codes [N][Mp], scales
+    [Mp/128][N], the (b, sb) of the down projection's weight gradient (None both
+    where ``product`` is false).  Returns ``(q, s, qt, st, yt, syt)``.
+    """
+    act_id = _act_id(act)
+    _mat(dy, "dy", 0, 0, torch.bfloat16)
+    M, N = dy.shape
+    if N % 128 != 0:
+        raise ValueError(f"fp8_quant_gated_backward: N = {N} must be a multiple of 128")
+    if not product and (yt is not None or syt is not None):
+        raise ValueError("yt and syt are outputs of product=True")
+    Mp = (M + 127) // 128 * 128
+    _mat(z, "z", M, 2 * N, torch.bfloat16)
+    _mat(q, "q", M, 2 * N, torch.uint8)
+    _mat(s, "s", N // 64, M, torch.float32)
+    _mat(qt, "qt", 2 * N, Mp, torch.uint8)
+    _mat(st, "st", Mp // 128, 2 * N, torch.float32)
+    _mat(yt, "yt", N, Mp, torch.uint8)
+    _mat(syt, "syt", Mp // 128, N, torch.float32)
+    _need_device(dy, z, q, s, qt, st, yt, syt)
+    u8, f32, dev = torch.uint8, torch.float32, dy.device
+    q = torch.empty(M, 2 * N, dtype=u8, device=dev) if q is None else q
+    s = torch.empty(N // 64, M, dtype=f32, device=dev) if s is None else s
+    qt = torch.empty(2 * N, Mp, dtype=u8, device=dev) if qt is None else qt
+    st = torch.empty(Mp // 128, 2 * N, dtype=f32, device=dev) if st is None else st
+    if product:
+        yt = torch.empty(N, Mp, dtype=u8, device=dev) if yt is None else yt
+        syt = torch.empty(Mp // 128, N, dtype=f32, device=dev) if syt is None else syt
+    with _on(dev):
+        _check(lib.fp8_quant_gated_backward(
+            _ptr(dy), _rowmajor(dy, "dy") if M else N, _ptr(z),
+            _rowmajor(z, "z") if M else 2 * N, act_id, M, N, _ptr(q), _ld(q), _ptr(s), _ld(s),
+            _ptr(qt), _ld(qt), _ptr(st), _ld(st), _ptr(yt), _ld(yt) if product else 0, _ptr(syt),
+            _ld(syt) if product else 0, _stream(dy)), "fp8_quant_gated_backward")
+    return q, s, qt, st, yt, syt
+
+
+def _norm_operands(where, x, weight, residual, h, y, rstd):
+    """Sizes and leading dimensions (of x, residual, h, y) of a norm's call after
+    checking its operand tensors."""
+    ldx = _mat(x, "x", 0, 0, torch.bfloat16)
+    M, K = x.shape
+    _k_of(K, where)
+    _vec(weight, "weight", K, torch.float32)
+    ldr = _mat(residual, "residual", M, K, torch.bfloat16)
+    ldh = _mat(h, "h", M, K, torch.bfloat16)
+    ldy = _mat(y, "y", M, K, torch.bfloat16)
+    _vec(rstd, "rstd", M, torch.float32)
+    return M, K, ldx, ldr, ldh, ldy
+
+
+def fp8_quant_rmsnorm(x, weight, eps=1e-6, residual=None, h=None, y=None, rstd=None, q=None,
+                      s=None):
+    """Root-mean-square norm with E4M3 output: h = x + residual (rounded to bf16),
+    y = h * rstd * weight with rstd = 1 / sqrt(mean(h^2) + eps); returns ``(q,
+    s)``, the codes and scales of y as ``fp8_quant_act_1x128`` lays them out.
+
+    bf16 ``x`` and ``residual`` [M][K], fp32 ``weight`` [K].  Optional outputs:
+    ``h`` bf16 [M][K] (may be ``x`` or ``residual`` itself), ``y`` bf16 [M][K],
+    ``rstd`` fp32 [M]; the backward pass (``bf16_rmsnorm_backward``) needs h and
+    rstd.  K is at most 32768.
+    """
+    M, K, ldx, ldr, ldh, ldy = _norm_operands("fp8_quant_rmsnorm", x, weight, residual, h, y, rstd)
+    _mat(q, "q", M, K, torch.uint8)
+    _mat(s, "s", K // 128, M, torch.float32)
+    _need_device(x, weight, residual, h, y, rstd, q, s)
+    if q is None:
+        q = torch.empty(M, K, dtype=torch.uint8, device=x.device)
+    if s is None:
+        s = torch.empty(K // 128, M, dtype=torch.float32, device=x.device)
+    with _on(x.device):
+        _check(lib.fp8_quant_rmsnorm(_ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), eps, _ptr(h),
+                                     ldh, _ptr(y), ldy, _ptr(rstd), _ptr(q), _ld(q), _ptr(s),
+                                     _ld(s), M, K, _stream(x)), "fp8_quant_rmsnorm")
+    return q, s
+
+
+def bf16_rmsnorm(x, weight, eps=1e-6, residual=None, h=None, rstd=None, y=None):
+    """As ``fp8_quant_rmsnorm``, with y in bf16 [M][K] alone; returns ``y``."""
+    M, K, ldx, ldr, ldh, ldy = _norm_operands("bf16_rmsnorm", x, weight, residual, h, y, rstd)
+    _need_device(x, weight, residual, h, rstd, y)
+    if y is None:
+        y = torch.empty(M, K, dtype=torch.bfloat16, device=x.device)
+        ldy = K
+    with _on(x.device):
+        _check(lib.bf16_rmsnorm(_ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), eps, _ptr(h), ldh,
+                                _ptr(rstd), _ptr(y), ldy, M, K, _stream(x)), "bf16_rmsnorm")
+    return y
+
+
+def bf16_rmsnorm_backward(dy, h, rstd, weight, dh=None, dx=None, dweight=None, workspace=None):
+    """Gradients of ``fp8_quant_rmsnorm`` and ``bf16_rmsnorm``: from bf16 ``dy``
+    [M][K] (of y), ``h`` and ``rstd`` as the forward call left them and the
+    optional bf16 ``dh`` [M][K] (the gradient that reaches h along the residual)
+    to ``(dx, dweight)``: bf16 [M][K], the gradient of x and of the residual
+    (``dx`` may be ``dy`` or ``dh`` itself), and fp32 [K]."""
+    lddy = _mat(dy, "dy", 0, 0, torch.bfloat16)
+    M, K = dy.shape
+    _k_of(K, "bf16_rmsnorm_backward")
+    ldh = _mat(h, "h", M, K, torch.bfloat16)
+    _vec(rstd, "rstd", M, torch.float32)
+    _vec(weight, "weight", K, torch.float32)
+    lddh = _mat(dh, "dh", M, K, torch.bfloat16)
+    lddx = _mat(dx, "dx", M, K, torch.bfloat16)
+    _vec(dweight, "dweight", K, torch.float32)
+    _need_device(dy, h, rstd, weight, dh, dx, dweight, workspace)
+    dev = dy.device
+    if dx is None:
+        dx = torch.empty(M, K, dtype=torch.bfloat16, device=dev)
+        lddx = K
+    if dweight is None:
+        dweight = torch.empty(K, dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(workspace_bytes(OP_RMSNORM_BACKWARD, M, 0, K), dtype=torch.uint8,
+                                device=dev)
+    with _on(dev):
+        _check(lib.bf16_rmsnorm_backward(
+            _ptr(dy), lddy, _ptr(h), ldh, _ptr(rstd), _ptr(weight), _ptr(dh), lddh, _ptr(dx), lddx,
+            _ptr(dweight), M, K, _ptr(workspace), workspace.numel() * workspace.element_size(),
+            _stream(dy)), "bf16_rmsnorm_backward")
+    return dx, dweight
 
 
 def _head_operands(where, x, w, target):

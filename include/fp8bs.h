@@ -87,10 +87,12 @@ enum {
   FP8BS_OP_GROUPED_GEMM = 4,
   FP8BS_OP_XENT = 5,
   FP8BS_OP_XENT_BACKWARD = 6,
-  FP8BS_OP_EPILOGUE_BACKWARD = 7
+  FP8BS_OP_EPILOGUE_BACKWARD = 7,
+  FP8BS_OP_GEMM_GATED_E4M3 = 8,
+  FP8BS_OP_RMSNORM_BACKWARD = 9
 };
 
-/* act of a linear layer's epilogue. */
+/* act of a linear layer's epilogue and of the gated product. */
 enum {
   FP8BS_ACT_NONE = 0,
   FP8BS_ACT_RELU = 1, /* max(z, 0)                                     */
@@ -405,6 +407,158 @@ int fp8_quant_epilogue_backward(const uint16_t* dy, int64_t lddy,
                                 int64_t ldqt, float* st, int64_t ldst,
                                 float* dbias, void* workspace,
                                 size_t workspace_bytes, void* stream);
+/*
+ * Gated product of a feed-forward block, both projections in one GEMM: with
+ * W's rows 0 .. N-1 the gate's and N .. 2N-1 the up projection's,
+ *   gate = A . Wg^T,  up = A . Wu^T,  y = act(gate) * up,
+ * the sums as fp8_block_gemm's, y formed from them in FP32 and rounded once.
+ * Pages: as fp8_block_gemm.
+ *
+ *   a_kind, a, sa  as fp8_block_gemm.
+ *   b, sb   E4M3 codes [2N][ldb] and block scales [2N/128][K/128]
+ *           (fp8_quant_w_128x128 of the stacked weight).
+ *   act     FP8BS_ACT_* (FP8BS_ACT_NONE: the plain product gate * up).
+ *   z       [out] optional: bf16 [M][ldz], ldz >= 2N, gate in columns
+ *           0 .. N-1, up in N .. 2N-1: what fp8_quant_gated_backward needs.
+ *   c       [out] y in bf16 [M][ldc].  N must be a multiple of 128 (the next
+ *           product's K; gate and up share no block of scales).
+ *   workspace  bf16 A: fp8bs_workspace_bytes(FP8BS_OP_GEMM_BF16, M, N, K, 0);
+ *              not used otherwise.
+ * Errors: as fp8_block_gemm; N not a multiple of 128 -> ERR_SHAPE; unknown
+ *         act -> ERR_DTYPE; ldz < 2N -> ERR_LAYOUT.
+ */
+int fp8_block_gemm_gated(int a_kind, const void* a, int64_t lda, float* sa,
+                         int64_t ldsa, const uint8_t* b, int64_t ldb,
+                         const float* sb, int act, uint16_t* z, int64_t ldz,
+                         uint16_t* c, int64_t ldc, int64_t M, int64_t N,
+                         int64_t K, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/*
+ * fp8_block_gemm_gated with y quantized per 1x128 tile along N, the down
+ * projection's input (qc, sc) as fp8_block_gemm_e4m3_out.
+ *   workspace  fp8bs_workspace_bytes(FP8BS_OP_GEMM_GATED_E4M3, M, N, K, 0);
+ *              needed for a bf16 A and for M <= 64 (y in FP32 before its
+ *              codes), may be NULL otherwise.
+ */
+int fp8_block_gemm_gated_e4m3_out(int a_kind, const void* a, int64_t lda,
+                                  float* sa, int64_t ldsa, const uint8_t* b,
+                                  int64_t ldb, const float* sb, int act,
+                                  uint16_t* z, int64_t ldz, uint8_t* qc,
+                                  int64_t ldqc, float* sc, int64_t ldsc,
+                                  int64_t M, int64_t N, int64_t K,
+                                  void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/*
+ * The gated product of every expert's rows, fp8_block_gemm_gated by the
+ * schedule of fp8_block_grouped_gemm.
+ *   b, sb   expert g's [2N][ldb] codes at b + g*b_group_stride, its scales at
+ *           sb + g*(2N/128)*(K/128).
+ *   z, c    rows as A's; rows of no group are not written.
+ * Errors: as fp8_block_grouped_gemm and fp8_block_gemm_gated;
+ *         b_group_stride < (2N-1)*ldb + K -> ERR_LAYOUT.
+ */
+int fp8_block_grouped_gemm_gated(const uint8_t* a, int64_t lda,
+                                 const float* sa, int64_t ldsa,
+                                 const uint8_t* b, int64_t ldb,
+                                 int64_t b_group_stride, const float* sb,
+                                 int act, uint16_t* z, int64_t ldz,
+                                 uint16_t* c, int64_t ldc,
+                                 const int32_t* group_offsets, int64_t G,
+                                 int64_t M_total, int64_t N, int64_t K,
+                                 void* stream);
+int fp8_block_grouped_gemm_gated_e4m3_out(
+    const uint8_t* a, int64_t lda, const float* sa, int64_t ldsa,
+    const uint8_t* b, int64_t ldb, int64_t b_group_stride, const float* sb,
+    int act, uint16_t* z, int64_t ldz, uint8_t* qc, int64_t ldqc, float* sc,
+    int64_t ldsc, const int32_t* group_offsets, int64_t G, int64_t M_total,
+    int64_t N, int64_t K, void* stream);
+
+/*
+ * Backward of the gated product up to the operands of its backward GEMMs, in
+ * one pass: with dy the gradient of y and z = (gate | up) as kept,
+ *   dgate = dy up act'(gate),  dup = dy act(gate),  dz = (dgate | dup)
+ * in FP32, quantized by the online rule both ways round.
+ * Pages: as fp8_quant_act_1x128 and fp8_quant_act_128x1_t.
+ *
+ *   dy      [in]  bf16 [M][lddy], N columns.
+ *   z       [in]  bf16 [M][ldz], 2N columns.
+ *   q, s    [out] dz [M][ldq], 2N columns, s(m, j) at s[j*lds + m] for the 2N/128
+ *                 tiles of a row: the (a, sa) of dX = dz . W, a GEMM with
+ *                 contraction length 2N (b, sb from fp8_quant_w_128x128_t).
+ *   qt, st  [out] dz^T [2N][ldqt], ldqt >= Mp = M rounded up to 128 (the rows
+ *                 past M count as zeros), st(n, mb) at st[mb*ldst + n]: the
+ *                 (a, sa) of dW = dz^T . X.
+ *   yt, syt [out] y^T [N][ldyt], ldyt >= Mp, syt(n, mb) at syt[mb*ldsyt + n],
+ *                 y = act(gate) * up of the kept values in FP32: the (b, sb) of
+ *                 the down projection's weight gradient.  Both NULL: not formed.
+ * N is a multiple of 128.  M == 0 launches nothing.
+ * Errors: N not a multiple of 128 -> ERR_SHAPE; unknown act -> ERR_DTYPE; one
+ *         of yt and syt -> ERR_NULL; otherwise as the two quantizers.
+ */
+int fp8_quant_gated_backward(const uint16_t* dy, int64_t lddy,
+                             const uint16_t* z, int64_t ldz, int act,
+                             int64_t M, int64_t N, uint8_t* q, int64_t ldq,
+                             float* s, int64_t lds, uint8_t* qt, int64_t ldqt,
+                             float* st, int64_t ldst, uint8_t* yt,
+                             int64_t ldyt, float* syt, int64_t ldsyt,
+                             void* stream);
+
+/*
+ * Root-mean-square norm with the residual's addition and E4M3 output:
+ *   h = RN_bf16(x + residual),  rstd = 1 / sqrt(mean_k h^2 + eps),
+ *   y = h rstd weight,
+ * the FP32 y quantized per 1x128 tile as fp8_quant_act_1x128 does (its sums
+ * and y are FP32; finite rows whose squares leave FP32 are summed scaled).
+ * Pages: as fp8_quant_act_1x128.
+ *
+ *   x       [in]  bf16 [M][ldx].
+ *   residual [in] optional, bf16 [M][ldr]; NULL: h = x.
+ *   weight  [in]  fp32 [K], 16-byte aligned.
+ *   eps     in [2^-100, 3.4e38].
+ *   h       [out] optional, bf16 [M][ldh].  May be x or residual itself (same
+ *                 pointer and leading dimension).
+ *   y       [out] optional, bf16 [M][ldy].
+ *   rstd    [out] optional, fp32 [M].
+ *   q, s    [out] codes [M][ldq] and scales s(m, kb) at s[kb*lds + m].
+ * K is at most 32768.  M == 0 launches nothing.
+ * Errors: as fp8_quant_act_1x128; K above 32768 or eps outside its range ->
+ *         ERR_SHAPE.
+ */
+int fp8_quant_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* residual,
+                      int64_t ldr, const float* weight, float eps, uint16_t* h,
+                      int64_t ldh, uint16_t* y, int64_t ldy, float* rstd,
+                      uint8_t* q, int64_t ldq, float* s, int64_t lds,
+                      int64_t M, int64_t K, void* stream);
+
+/* fp8_quant_rmsnorm with y in bf16 alone (the norm before the bf16 head). */
+int bf16_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* residual,
+                 int64_t ldr, const float* weight, float eps, uint16_t* h,
+                 int64_t ldh, float* rstd, uint16_t* y, int64_t ldy, int64_t M,
+                 int64_t K, void* stream);
+
+/*
+ * Backward of both: with n = h rstd, u = weight dy and c = mean_k(u n),
+ *   dx = rstd (u - n c) + dh,  dweight = sum over the rows of dy n.
+ *   dy      [in]  bf16 [M][lddy], gradient of y.
+ *   h, rstd [in]  as the forward call left them.
+ *   dh      [in]  optional, bf16 [M][lddh]: the gradient that reaches h along
+ *                 the residual.
+ *   dx      [out] bf16 [M][lddx], gradient of x and of residual.  May be dy or
+ *                 dh itself (same pointer and leading dimension).
+ *   dweight [out] fp32 [K], overwritten (zeros for M == 0).  Its sums are
+ *                 always taken in the same order.
+ *   workspace  fp8bs_workspace_bytes(FP8BS_OP_RMSNORM_BACKWARD, M, 0, K, 0)
+ *              bytes (at most 1024 K), 256-byte aligned.
+ * Errors: as fp8_quant_rmsnorm; workspace -> ERR_WORKSPACE.
+ */
+int bf16_rmsnorm_backward(const uint16_t* dy, int64_t lddy, const uint16_t* h,
+                          int64_t ldh, const float* rstd, const float* weight,
+                          const uint16_t* dh, int64_t lddh, uint16_t* dx,
+                          int64_t lddx, float* dweight, int64_t M, int64_t K,
+                          void* workspace, size_t workspace_bytes,
+                          void* stream);
 /*
  * Block-scaled FP8 GEMM with one scale per row and 128-K group on both
  * operands:  C[m][n] = sum_kb sa(m,kb) * sb(n,kb) * P(m,n,kb), P the FP8 x FP8
