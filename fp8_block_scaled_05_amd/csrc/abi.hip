@@ -55,6 +55,11 @@ bool norm_sizes_ok(int64_t M, int64_t K) {
   return M >= 0 && K > 0 && K % kTile == 0 && K <= fp8bs::kMaxNormK;
 }
 
+// The gated product addresses a tile's gate and up rows from one base.
+bool gated_b_ok(int64_t N, int64_t K, int64_t ldb) {
+  return operand_ld_ok(ldb, K) && 2 * N <= int64_t(0xFFFFFFFF) / ldb;
+}
+
 // The gated product's FP32 result for few rows, before its E4M3 codes.
 size_t gated_y_bytes(int64_t M, int64_t N) { return round256(size_t(M) * size_t(N) * 4); }
 
@@ -312,15 +317,15 @@ int gated_gemm_impl(int a_kind, const void* a, int64_t lda, float* sa, int64_t l
   if (M == 0 || N == 0) return FP8BS_OK;
   const bool bf16_a = a_kind == FP8BS_A_BF16;
   if (!a || !b || !sb || !c || (!bf16_a && !sa) || (e4m3 && !sc)) return FP8BS_ERR_NULL;
-  if (!operand_ld_ok(lda, K) || !operand_ld_ok(ldb, K) || (sa && ldsa < M)) return FP8BS_ERR_LAYOUT;
+  if (!operand_ld_ok(lda, K) || !gated_b_ok(N, K, ldb) || (sa && ldsa < M)) return FP8BS_ERR_LAYOUT;
   if (!aligned(a, 16) || !aligned(b, 16) || !aligned(sb, 4) || (sa && !aligned(sa, 4)))
     return FP8BS_ERR_LAYOUT;
   if (z && (ldz < 2 * N || !aligned(z, 2))) return FP8BS_ERR_LAYOUT;
   if (e4m3 ? !ld_ok(ldc, N) || ldsc < M || !aligned(c, 16) || !aligned(sc, 4)
            : ldc < N || !aligned(c, 2))
     return FP8BS_ERR_LAYOUT;
-  const bool few = M <= fp8bs::kFewRows && fp8bs::few_rows_gated_fits(N, ldb);
-  if (bf16_a || (e4m3 && M <= fp8bs::kFewRows)) {
+  const bool few = M <= fp8bs::kFewRows;
+  if (bf16_a || (e4m3 && few)) {
     const int op = e4m3 ? FP8BS_OP_GEMM_GATED_E4M3 : FP8BS_OP_GEMM_BF16;
     if (!workspace || workspace_bytes < fp8bs_workspace_bytes(op, M, N, K, 0))
       return FP8BS_ERR_WORKSPACE;
@@ -386,7 +391,7 @@ int grouped_gated_impl(const uint8_t* a, int64_t lda, const float* sa, int64_t l
     return FP8BS_ERR_SHAPE;
   if (M_total == 0 || N == 0) return FP8BS_OK;
   if (!a || !sa || !b || !sb || !c || !group_offsets || (e4m3 && !sc)) return FP8BS_ERR_NULL;
-  if (!operand_ld_ok(lda, K) || !operand_ld_ok(ldb, K) || ldsa < M_total) return FP8BS_ERR_LAYOUT;
+  if (!operand_ld_ok(lda, K) || !gated_b_ok(N, K, ldb) || ldsa < M_total) return FP8BS_ERR_LAYOUT;
   if (b_group_stride % 16 != 0 || b_group_stride < (2 * N - 1) * ldb + K) return FP8BS_ERR_LAYOUT;
   if (!aligned(a, 16) || !aligned(b, 16) || !aligned(sa, 4) || !aligned(sb, 4) ||
       !aligned(group_offsets, 4))

@@ -806,11 +806,6 @@ hipError_t launch_few_rows_gemm(const void* a, int64_t lda, float* sa, int64_t l
                          stream);
 }
 
-// The copies address a workgroup's gate and up rows from its first gate row.
-bool few_rows_gated_fits(int64_t N, int64_t ldb) {
-  return (N + 64) * ldb <= int64_t(0xFFFFFFFF);
-}
-
 hipError_t launch_few_rows_gated(const void* a, int64_t lda, float* sa, int64_t ldsa, bool fused,
                                  const uint8_t* b, int64_t ldb, const float* sb, void* c,
                                  int64_t ldc, bool out_bf16, int64_t M, int64_t N, int64_t K,

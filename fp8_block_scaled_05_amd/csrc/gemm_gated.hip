@@ -35,10 +35,12 @@ struct GateEpilogue {
   template <class C, int OUT>
   __device__ __forceinline__ void finish(const GemmArgs& p, const gemm::TileCoords& t,
                                          v4f (&acc)[C::FM][C::FN], int wm, int wn, int lane,
-                                         const gemm::LdsSet& L) const {
+                                         uint8_t* st0, uint8_t* st1, float* red,
+                                         float* rcp) const {
     constexpr int HW = C::WN / 2;
     constexpr int CHUNK = C::FM * C::FN * 512;     // bytes a wave gives away
-    constexpr int FIT = C::STAGE_BYTES / CHUNK;  // chunks in a stage
+    // chunks that use a stage; a pair's are in one
+    constexpr int FIT = C::STAGE_BYTES / CHUNK / C::WN * C::WN;
     static_assert(C::FN % 2 == 0, "two columns per LDS access");
     static_assert(2 * FIT >= C::NWAVES, "the chunks fit two stages");
     const int wave = wm * C::WN + wn;
@@ -51,37 +53,50 @@ struct GateEpilogue {
       tz.c = e.z + half * p.N;
       gemm::store_tile<C, kOutBF16, true>(pz, tz, acc, wm, wc, lane);
     }
-    auto chunk = [&](int w) {
-      return reinterpret_cast<v4f*>(w < FIT ? L.st[0] + w * CHUNK : L.st[1] + (w - FIT) * CHUNK);
-    };
-    __syncthreads();  // every wave has read its last operands
-    v4f* const out = chunk(wave);
-#pragma unroll
-    for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-      for (int j = 0; j < C::FN; j += 2) {
-        const v4f a = acc[i][j], b = acc[i][j + 1];
-        out[(i * (C::FN / 2) + j / 2) * 64 + lane] =
-            half ? v4f{a[0], a[1], b[0], b[1]} : v4f{a[2], a[3], b[2], b[3]};
-      }
-    __syncthreads();
-    const v4f* const in = chunk(wave ^ HW);
-    v2f y[C::FM][C::FN];  // first the gate, then act(gate) up
-    v2f up[C::FM][C::FN];
-#pragma unroll
-    for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-      for (int j = 0; j < C::FN; j += 2) {
-        const v4f o = in[(i * (C::FN / 2) + j / 2) * 64 + lane];
-#pragma unroll
-        for (int d = 0; d < 2; ++d) {
-          const v4f a = acc[i][j + d];
-          const v2f mine = half ? v2f{a[2], a[3]} : v2f{a[0], a[1]};
-          const v2f theirs = v2f{o[2 * d], o[2 * d + 1]};
-          y[i][j + d] = half ? theirs : mine;
-          up[i][j + d] = half ? mine : theirs;
+    // f(the stage that holds the chunks of this wave and of its pair, its index there)
+    auto chunks = [&](auto&& f) {
+      if constexpr (FIT >= C::NWAVES) {
+        f(st0, wave);
+      } else {
+        if (wave < FIT) {
+          f(st0, wave);
+        } else {
+          f(st1, wave - FIT);
         }
       }
+    };
+    __syncthreads();  // every wave has read its last operands
+    chunks([&](uint8_t* st, int w) {
+      v4f* const out = reinterpret_cast<v4f*>(st + w * CHUNK) + lane;
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; j += 2) {
+          const v4f a = acc[i][j], b = acc[i][j + 1];
+          out[(i * (C::FN / 2) + j / 2) * 64] =
+              half ? v4f{a[0], a[1], b[0], b[1]} : v4f{a[2], a[3], b[2], b[3]};
+        }
+    });
+    __syncthreads();
+    v2f y[C::FM][C::FN];  // first the gate, then act(gate) up
+    v2f up[C::FM][C::FN];
+    chunks([&](uint8_t* st, int w) {
+      const v4f* const in = reinterpret_cast<const v4f*>(st + (w ^ HW) * CHUNK) + lane;
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; j += 2) {
+          const v4f o = in[(i * (C::FN / 2) + j / 2) * 64];
+#pragma unroll
+          for (int d = 0; d < 2; ++d) {
+            const v4f a = acc[i][j + d];
+            const v2f mine = half ? v2f{a[2], a[3]} : v2f{a[0], a[1]};
+            const v2f theirs = v2f{o[2 * d], o[2 * d + 1]};
+            y[i][j + d] = half ? theirs : mine;
+            up[i][j + d] = half ? mine : theirs;
+          }
+        }
+    });
     with_activation(e.act, [&](auto act) {
 #pragma unroll
       for (int i = 0; i < C::FM; ++i)
@@ -101,7 +116,7 @@ struct GateEpilogue {
     const int row0 = wm * C::TM + 4 * (lane >> 4) + 2 * half;
     const int64_t col = t.col0 + wc * C::TN + C::FN * l16;
     if constexpr (OUT == kOutE4M3) {
-      store_codes<C>(p, t, y, row0, wc, col, l16, L.red, L.rcp);
+      store_codes<C>(p, t, y, row0, wc, col, l16, red, rcp);
     } else {
       store_bf16<C>(p, t, y, row0, col);
     }

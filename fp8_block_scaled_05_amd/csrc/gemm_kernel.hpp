@@ -341,8 +341,10 @@ __device__ __forceinline__ void make_plan(const GemmArgs& p, const TileCoords& t
       const int rb = r - C::BM, rw = rb % C::TN;
       const int wb = rb / C::TN % (C::GATED ? C::WN / 2 : C::WN);
       const int col = wb * C::TN + C::FN * (rw % 16) + rw / 16;
-      const int rr = col < rows_b ? col : rows_b - 1;
-      lp.tile[j] = (uint32_t)rr * (uint32_t)p.ldb + chunk * 16;
+      uint32_t rr = col < rows_b ? col : rows_b - 1;
+      // the up rows, N further (all of W lies within 32-bit offsets)
+      if (C::GATED && rb >= C::BN / 2) rr += (uint32_t)p.N;
+      lp.tile[j] = rr * (uint32_t)p.ldb + chunk * 16;
     }
   }
 #pragma unroll
@@ -372,7 +374,6 @@ __device__ __forceinline__ void make_plan(const GemmArgs& p, const TileCoords& t
 // rows past the edge are clamped to the last valid row.
 struct Rsrc {
   __amdgpu_buffer_rsrc_t a, b;
-  __amdgpu_buffer_rsrc_t up;  // GatedB: the up projection's rows
 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base) {
@@ -387,7 +388,6 @@ __device__ __forceinline__ Rsrc make_rsrc_set(const GemmArgs& p, const TileCoord
   Rsrc r;
   r.a = make_rsrc(p.a + t.row0 * p.lda + t.kb0 * 128);
   r.b = make_rsrc(t.b + t.col0 * p.ldb + t.kb0 * 128);
-  if constexpr (C::GATED) r.up = make_rsrc(t.b + (p.N + t.col0) * p.ldb + t.kb0 * 128);
   return r;
 }
 
@@ -399,8 +399,7 @@ __device__ __forceinline__ void issue_copy(const GemmArgs& p, const Rsrc& rs,
                                            int wave, int idx) {
   (void)p;
   const int rbase = (wave * C::TILE_LOADS + idx) * 8;
-  const bool up = C::GATED && rbase >= C::BM + C::BN / 2;
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rbase < C::BM ? rs.a : up ? rs.up : rs.b,
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rbase < C::BM ? rs.a : rs.b,
                                            (lds_void*)(st + rbase * 128), 16, lp.tile[idx],
                                            (int)(kb * 128), 0, 0);
 }
@@ -782,7 +781,7 @@ struct NoEpilogue {
 // ep.load<C>(p, t, wm, wn, lane, early) may load operands of its own before the
 // K loop; ep.apply<C>(p, t, acc, wm, wn, lane, early) may change a wave's
 // finished sums before they are stored.  With GatedB, ep.finish<C, OUT>(p, t,
-// acc, wm, wn, lane, L) takes the sums and stores all there is.
+// acc, wm, wn, lane, LDS) takes the sums and stores all there is.
 template <class C, int OUT, class E = NoEpilogue>
 __device__ __forceinline__ void block_gemm_body(const GemmArgs& p, const TileCoords& t,
                                                 const LdsSet& L, const E& ep = E()) {
@@ -904,7 +903,7 @@ __device__ __forceinline__ void block_gemm_body(const GemmArgs& p, const TileCoo
   }
 
   if constexpr (C::GATED) {
-    ep.template finish<C, OUT>(p, t, acc, wm, wn, lane, L);
+    ep.template finish<C, OUT>(p, t, acc, wm, wn, lane, L.st[0], L.st[1], L.red, L.rcp);
   } else {
     ep.template apply<C>(p, t, acc, wm, wn, lane, early);
     if constexpr (OUT == kOutE4M3) {

@@ -189,7 +189,8 @@ hipError_t launch_rmsnorm_backward(NormGradArgs a, float* dg, void* workspace,
 
 // Gated product: the weight's first N rows are the gate's, the next N the up
 // projection's; y = act(gate) up, with both sums kept in bf16 [M][2N] if z.
-// N (the output's columns) is a multiple of 128.
+// N (the output's columns) is a multiple of 128, and W (2 N ldb bytes) lies within
+// 32-bit offsets.
 struct Gate {
   uint16_t* z;  // [M][ldz]
   int64_t ldz;
@@ -200,8 +201,6 @@ hipError_t launch_block_gemm_gated(const GemmArgs& args, const Gate& gate, OutKi
 hipError_t launch_grouped_gemm_gated(const GemmArgs& args, const Gate& gate, OutKind out,
                                      hipStream_t stream);
 // Few rows (M <= kFewRows, fused as launch_few_rows_gemm); fp32 or bf16 output.
-// False where the weight's rows are too far apart for its 32-bit offsets.
-bool few_rows_gated_fits(int64_t N, int64_t ldb);
 hipError_t launch_few_rows_gated(const void* a, int64_t lda, float* sa, int64_t ldsa, bool fused,
                                  const uint8_t* b, int64_t ldb, const float* sb, void* c,
                                  int64_t ldc, bool out_bf16, int64_t M, int64_t N, int64_t K,

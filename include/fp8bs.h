@@ -425,7 +425,8 @@ int fp8_quant_epilogue_backward(const uint16_t* dy, int64_t lddy,
  *   workspace  bf16 A: fp8bs_workspace_bytes(FP8BS_OP_GEMM_BF16, M, N, K, 0);
  *              not used otherwise.
  * Errors: as fp8_block_gemm; N not a multiple of 128 -> ERR_SHAPE; unknown
- *         act -> ERR_DTYPE; ldz < 2N -> ERR_LAYOUT.
+ *         act -> ERR_DTYPE; ldz < 2N, or 2N*ldb of 2^32 or more (the copies
+ *         use 32-bit byte offsets) -> ERR_LAYOUT.
  */
 int fp8_block_gemm_gated(int a_kind, const void* a, int64_t lda, float* sa,
                          int64_t ldsa, const uint8_t* b, int64_t ldb,
