@@ -35,9 +35,11 @@ DEVICE_FLAGS = [
 
 # Per-source additions.  Kernels of one wave per SIMD, where the compiler would
 # put MFMA results in accumulation registers and copy each one out before its
-# FP32 promotion (the few-row FP8 kernels) or in and out of every k-step (the
-# cross entropy's small tiles); this option keeps them in VGPRs.
+# FP32 promotion (the few-row FP8 kernels, the gated product's small tiles) or in
+# and out of every k-step (the cross entropy's small tiles); this option keeps them
+# in VGPRs.
 EXTRA_FLAGS = {"gemm_few_rows.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+               "gemm_gated.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                "xent.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 

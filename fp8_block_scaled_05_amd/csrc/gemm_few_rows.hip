@@ -53,8 +53,30 @@ constexpr int kWaves = 4;
 constexpr int kStages = 4;
 
 // What a kernel does with its finished sums: store them, apply a linear layer's
-// epilogue, or multiply gate and up sums.
-enum Mode { kStore, kEpilogue, kGated };
+// epilogue, or multiply gate and up sums, formed by the FP8 instruction (bf16
+// output) or from exact products (FP32 output, see gemm::Exact; the weight's
+// stream hides the widening).
+enum Mode { kStore, kEpilogue, kGated, kGatedExact };
+constexpr bool is_gated(Mode m) { return m == kGated || m == kGatedExact; }
+
+// A 16x16 tile's products over one K group.
+template <bool EXACT>
+__device__ __forceinline__ v4f group_product(const v8i& w, const v8i& a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  v4f c = {0.f, 0.f, 0.f, 0.f};
+  if constexpr (EXACT) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      c = __builtin_amdgcn_mfma_f32_16x16x32_f16(gemm::widen8(w[2 * q], w[2 * q + 1]),
+                                                 gemm::widen8(a[2 * q], a[2 * q + 1]), c, 0, 0, 0);
+    return c;
+  } else {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 0, 0, 0, 0, 0, 0);
+  }
+#else
+  return v4f{};
+#endif
+}
 
 // Gated product: a workgroup's R rows of W are 4 RC columns' gate and up rows,
 // four of the one and four of the other in turn, so that lane groups g and g ^ 1
@@ -62,7 +84,7 @@ enum Mode { kStore, kEpilogue, kGated };
 // workgroup's first (gate) row, that LDS row r holds; up rows lie N further.
 template <Mode MODE>
 __device__ __forceinline__ int own_row(int r) {
-  return MODE == kGated ? 4 * (r >> 3) + (r & 3) : r;
+  return is_gated(MODE) ? 4 * (r >> 3) + (r & 3) : r;
 }
 
 template <int RC, int MT, bool FUSED>
@@ -248,7 +270,7 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_kteam_kernel(FewArgs p, 
   const int lane = threadIdx.x & 63;
   const int g = lane >> 4, l16 = lane & 15;
   // rows of W, or columns of the gated product
-  constexpr int OWN = MODE == kGated ? C::R / 2 : C::R;
+  constexpr int OWN = is_gated(MODE) ? C::R / 2 : C::R;
   const int64_t row0 = (int64_t)blockIdx.x * OWN;
   const int nrows = (int)((p.N - row0) < OWN ? (p.N - row0) : OWN);  // >= 1
   const int64_t KB = p.K / 128;
@@ -273,7 +295,7 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_kteam_kernel(FewArgs p, 
       const int r = 8 * c + (lane >> 3);
       const int own = own_row<MODE>(r);
       uint32_t rr = own < nrows ? own : nrows - 1;
-      if (MODE == kGated && (r & 4)) rr += (uint32_t)p.N;
+      if (is_gated(MODE) && (r & 4)) rr += (uint32_t)p.N;
       voff[c] = rr * (uint32_t)p.ldb + (uint32_t)(((lane & 7) ^ lds_swizzle(r)) * 16);
     }
     // W fragment reads: row 16 i + l16, K chunks 2g and 2g + 1
@@ -360,7 +382,7 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_kteam_kernel(FewArgs p, 
       wait_vmcnt<C::ADIST * RC + (C::ADIST - 1) * C::NA>();
       const int kb = kb_of(t);
       float swl = scalar_ld(sw_lo + kb), swh = scalar_ld(sw_hi + kb);
-      if constexpr (MODE == kGated) {
+      if constexpr (is_gated(MODE)) {
         const float ul = scalar_ld(sw_lo + up_scales + kb), uh = scalar_ld(sw_hi + up_scales + kb);
         swl = g & 1 ? ul : swl;
         swh = g & 1 ? uh : swh;
@@ -396,8 +418,7 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_kteam_kernel(FewArgs p, 
         for (int i = 0; i <= RT; ++i) {
           v4f cur;
           if (i < RT) {
-            cur = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                wf[i], af, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+            cur = group_product<MODE == kGatedExact>(wf[i], af);
             if (j == MT - 1) issue_w(t + 3, stages[(U + 3) % kStages], i * PW, (i + 1) * PW);
           }
           if (i > 0) {
@@ -475,7 +496,7 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_kteam_kernel(FewArgs p, 
       // first of the lane's 4 output columns
       const int nl = own_row<MODE>(16 * i + 4 * g);
       const int64_t n = row0 + nl;
-      if constexpr (MODE == kGated) {
+      if constexpr (is_gated(MODE)) {
         store_gated(p, ep, m, n, g & 1, m < p.M && nl < nrows, sum);
         continue;
       }
@@ -554,7 +575,7 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_shared_kernel(FewArgs p,
   const int lane = threadIdx.x & 63;
   const int g = lane >> 4, l16 = lane & 15;
   // rows of W, or columns of the gated product
-  constexpr int OWN = MODE == kGated ? C::R / 2 : C::R;
+  constexpr int OWN = is_gated(MODE) ? C::R / 2 : C::R;
   const int64_t row0 = (int64_t)blockIdx.x * OWN;
   const int nrows = (int)((p.N - row0) < OWN ? (p.N - row0) : OWN);  // >= 1
   const int KB = (int)(p.K / 128);
@@ -576,7 +597,7 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_shared_kernel(FewArgs p,
       const int r = 8 * b + (lane >> 3);
       const int own = own_row<MODE>(r);
       uint32_t rr = own < nrows ? own : nrows - 1;
-      if (MODE == kGated && (r & 4)) rr += (uint32_t)p.N;
+      if (is_gated(MODE) && (r & 4)) rr += (uint32_t)p.N;
       voff[sl] = rr * (uint32_t)p.ldb + (uint32_t)(((lane & 7) ^ lds_swizzle(r)) * 16);
       ldsoff[sl] = b * 1024;
     } else {
@@ -645,7 +666,7 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_shared_kernel(FewArgs p,
     uint8_t* const nxt = stages[(U + S - 1) % S];
     const uint8_t* st = stages[U];
     float swl = scalar_ld(sw_lo + t), swh = scalar_ld(sw_hi + t);
-    if constexpr (MODE == kGated) {
+    if constexpr (is_gated(MODE)) {
       const float ul = scalar_ld(sw_lo + up_scales + t), uh = scalar_ld(sw_hi + up_scales + t);
       swl = g & 1 ? ul : swl;
       swh = g & 1 ? uh : swh;
@@ -658,8 +679,7 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_shared_kernel(FewArgs p,
       v4f cur;
       if (i < RT) {
         const v8i wf = gemm::load_frag(st, f_lo, f_hi, i * 2048);
-        cur = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, af, v4f{0.f, 0.f, 0.f, 0.f},
-                                                               0, 0, 0, 0, 0, 0);
+        cur = group_product<MODE == kGatedExact>(wf, af);
         __builtin_amdgcn_sched_barrier(0);
         issue(t + S - 1, nxt, i * PR, (i + 1) * PR);
         __builtin_amdgcn_sched_barrier(0);
@@ -687,7 +707,7 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_shared_kernel(FewArgs p,
 
   // --- store: wave w holds C[16 w + l16][row0 + 16 i + 4 g + r] ---
   const int64_t m = ar;
-  if constexpr (MODE == kGated) {
+  if constexpr (is_gated(MODE)) {
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       const int nl = own_row<MODE>(16 * i + 4 * g);
@@ -732,7 +752,7 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_shared_kernel(FewArgs p,
 // whole W on at most one workgroup per compute unit, from a fixed set.
 template <class F>
 hipError_t with_rows(const FewArgs& p, Mode mode, int cus, F&& f) {
-  const int64_t rows = mode == kGated ? 2 * p.N : p.N;
+  const int64_t rows = is_gated(mode) ? 2 * p.N : p.N;
   const int64_t per = (rows + cus - 1) / cus;
   auto go = [&](auto RC_) {
     constexpr int RC = decltype(RC_)::value;
@@ -754,6 +774,9 @@ hipError_t launch_mt(const FewArgs& p, Mode mode, const Epilogue& e, int cus, hi
       case kGated:
         return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kGated>, grid, block, stream, p,
                              e);
+      case kGatedExact:
+        return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kGatedExact>, grid, block,
+                             stream, p, e);
       case kEpilogue:
         return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kEpilogue>, grid, block, stream,
                              p, e);
@@ -772,6 +795,8 @@ hipError_t launch_shared(const FewArgs& p, Mode mode, const Epilogue& e, int cus
     switch (mode) {
       case kGated:
         return launch_kernel(few_rows_shared_kernel<RC, kGated>, grid, block, stream, p, e);
+      case kGatedExact:
+        return launch_kernel(few_rows_shared_kernel<RC, kGatedExact>, grid, block, stream, p, e);
       case kEpilogue:
         return launch_kernel(few_rows_shared_kernel<RC, kEpilogue>, grid, block, stream, p, e);
       default:
@@ -811,7 +836,7 @@ hipError_t launch_few_rows_gated(const void* a, int64_t lda, float* sa, int64_t 
                                  int64_t ldc, bool out_bf16, int64_t M, int64_t N, int64_t K,
                                  const Gate& gate, hipStream_t stream) {
   const FewArgs p{a, lda, sa, ldsa, b, ldb, sb, c, ldc, M, N, K, out_bf16 ? 1 : 0};
-  return launch_few_rows(p, fused, kGated,
+  return launch_few_rows(p, fused, out_bf16 ? kGated : kGatedExact,
                          Epilogue{nullptr, nullptr, 0, gate.z, gate.ldz, gate.act}, stream);
 }
 

@@ -203,29 +203,31 @@ __global__ __launch_bounds__(C::THREADS) void gated_kernel(GemmArgs p, int64_t f
   gemm::block_gemm_tile<C, TAIL, SCHED, OUT>(p, full, ep);
 }
 
-template <class C0, int SCHED, class TAIL0 = C0>
-hipError_t launch_tiles(const GemmArgs& a, const GateEpilogue& ep, OutKind out,
-                        hipStream_t stream) {
-  using C = gemm::GatedB<C0>;
-  using TAIL = gemm::GatedB<TAIL0>;
+// OUT: bf16 from the FP8 instruction's sums, whose error lies far below bf16's
+// rounding, or E4M3 from exact products, whose FP32 scales show it (see
+// gemm::Exact).
+template <class C0, int SCHED, int OUT, class TAIL0 = C0>
+hipError_t launch_tiles(const GemmArgs& a, const GateEpilogue& ep, hipStream_t stream) {
+  using CG = gemm::GatedB<C0>;
+  using TG = gemm::GatedB<TAIL0>;
+  using C = typename std::conditional<OUT == kOutE4M3, gemm::Exact<CG>, CG>::type;
+  using TAIL = typename std::conditional<OUT == kOutE4M3, gemm::Exact<TG>, TG>::type;
   int64_t full = 0;
   const int64_t blocks = gemm::grid_size<C, SCHED, TAIL>(a, full);
   if (blocks == 0) return hipSuccess;
   if (blocks < 0) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)blocks), block(C::THREADS);
-  if constexpr (C::BNO == 128) {
-    if (out == kOutE4M3)
-      return launch_kernel(gated_kernel<C, TAIL, SCHED, kOutE4M3>, grid, block, stream, a, full,
-                           ep);
-  }
-  if (out == kOutBF16)
-    return launch_kernel(gated_kernel<C, TAIL, SCHED, kOutBF16>, grid, block, stream, a, full, ep);
-  return hipErrorInvalidConfiguration;
+  return launch_kernel(gated_kernel<C, TAIL, SCHED, OUT>, grid, block, stream, a, full, ep);
 }
 
-// An E4M3 output needs 128 columns of y, 256 rows of W, per tile: 64 rows of A
-// where the card is not filled otherwise, in three LDS stages.
-using Rows64Wide = gemm::Cfg<64, 256, 1, 4, 3, 1>;
+// An E4M3 output needs 128 columns of y, 256 rows of W, per tile.
+using Exact128 = gemm::Cfg<128, 256, 2, 4, 3, 4>;
+using Exact128Tail = gemm::Cfg<64, 256, 2, 4, 3, 4>;
+using Exact64 = gemm::Cfg<64, 256, 1, 4, 3, 1>;
+using Exact32 = gemm::Cfg<32, 256, 1, 4, 3, 1>;
+// bf16 outputs of few tiles, as the epilogue's
+using SmallCfg = gemm::Cfg<64, 64, 2, 2, 4, 1>;
+using TinyCfg = gemm::Cfg<32, 64, 2, 2, 4, 1>;
 
 // fp32 [M][N] -> codes and scales, 16 lanes per 1x128 tile.
 __global__ __launch_bounds__(256) void quant_f32_kernel(const float* x, int64_t M, int64_t N,
@@ -262,24 +264,64 @@ hipError_t launch_quant_f32(const float* x, int64_t M, int64_t N, uint8_t* q, in
                        ldq, s, lds);
 }
 
+// Tiles by their number, as the epilogue's.  us, rows of 32 / 64 / 128 for E4M3 and
+// 32x64 / 64x64 / 128x256 / 256x256 for bf16:
+//    100 x  2048 x 2048    17.3   22.5   29.1      7.9    8.6   16.7   26.1
+//    333 x  2048 x 2048    18.6   22.8   29.2     16.3   13.2   16.8   27.0
+//    700 x  2048 x 2048    33.8   23.4   29.5     28.9   18.8   19.5   27.5
+//   1000 x  2048 x 7168    95.2   65.5   85.3    129.2   70.4   54.1   74.6
+//    128 x 18432 x 7168   168.0  128.2   86.5    143.7   83.8   80.2   89.1
+//   1500 x  2048 x 7168   135.0  121.9   86.0    185.7  102.6   55.1   74.9
 hipError_t launch_block_gemm_gated(const GemmArgs& args, const Gate& gate, OutKind out,
                                    hipStream_t stream) {
   const GateEpilogue ep{gate};
-  GemmArgs whole = args;  // the tiles' estimate counts W's rows
-  whole.N = 2 * args.N;
-  switch (gemm::pick_tiles(whole)) {
-    case gemm::Tiles::kSmall: return launch_tiles<Rows64Wide, gemm::kDense>(args, ep, out, stream);
-    case gemm::Tiles::kHalf:
-      return launch_tiles<gemm::LargeTail, gemm::kDense>(args, ep, out, stream);
-    default:
-      return launch_tiles<gemm::LargeCfg, gemm::kDense, gemm::LargeTail>(args, ep, out, stream);
+  const int64_t cus = gemm::device_cus() > 0 ? gemm::device_cus() : 256;
+  if (out == kOutE4M3) {
+    const int64_t tiles = (args.M + 63) / 64 * (args.N / 128);
+    if (2 * tiles <= cus) return launch_tiles<Exact32, gemm::kDense, kOutE4M3>(args, ep, stream);
+    if (tiles <= cus) return launch_tiles<Exact64, gemm::kDense, kOutE4M3>(args, ep, stream);
+    return launch_tiles<Exact128, gemm::kDense, kOutE4M3, Exact128Tail>(args, ep, stream);
   }
+  const int64_t tiles = (args.M + 63) / 64 * (args.N / 32);
+  if (2 * tiles <= cus) return launch_tiles<TinyCfg, gemm::kDense, kOutBF16>(args, ep, stream);
+  if (tiles <= 3 * cus) return launch_tiles<SmallCfg, gemm::kDense, kOutBF16>(args, ep, stream);
+  GemmArgs whole = args;  // the estimate counts W's rows
+  whole.N = 2 * args.N;
+  if (gemm::pick_tiles(whole) == gemm::Tiles::kLarge)
+    return launch_tiles<gemm::LargeCfg, gemm::kDense, kOutBF16, gemm::LargeTail>(args, ep, stream);
+  return launch_tiles<gemm::LargeTail, gemm::kDense, kOutBF16>(args, ep, stream);
 }
 
+// The groups' rows are known on the device alone: the rules go by the most
+// tile-rows that M rows of G groups can fill.  us, 32x64 / 64x64 / 128x256 /
+// 256x256 for bf16 and rows of 32 / 64 / 128 for E4M3:
+//   G 8  M  333 N  512 K 2048    8.6    9.7   17.9   18.2     17.7   22.3   30.4
+//   G 4  M  200 N 2048 K 2048   11.0   12.2   20.5   21.0     18.3   23.7   31.0
+//   G 16 M 2000 N  512 K 2048   19.8   19.2   21.2   29.4     34.2   25.0   31.0
+//   G 32 M  256 N 2048 K 7168  161.9  158.0  185.2  185.3    211.5  166.5  165.1
+//   G 32 M 1000 N 2048 K 7168  188.8  176.6  258.1  201.9    192.1  203.1  214.9
+//   G 8  M 3000 N 1024 K 4096   66.0   55.7   39.4   50.1    108.6   76.9   56.8
+// Few rows to a group (the weights' stream) take 64x64 tiles whatever their number.
 hipError_t launch_grouped_gemm_gated(const GemmArgs& args, const Gate& gate, OutKind out,
                                      hipStream_t stream) {
-  return launch_tiles<gemm::LargeCfg, gemm::kGroupRows, gemm::LargeTail>(args, GateEpilogue{gate},
-                                                                         out, stream);
+  const GateEpilogue ep{gate};
+  const int64_t cus = gemm::device_cus() > 0 ? gemm::device_cus() : 256;
+  const int64_t groups = args.G < args.M ? args.G : args.M;
+  const int64_t rows = args.M / 64 + groups;  // tile-rows of 64
+  if (out == kOutE4M3) {
+    const int64_t tiles = rows * (args.N / 128);
+    if (2 * tiles <= cus) return launch_tiles<Exact32, gemm::kGroupRows, kOutE4M3>(args, ep, stream);
+    if (tiles <= cus) return launch_tiles<Exact64, gemm::kGroupRows, kOutE4M3>(args, ep, stream);
+    return launch_tiles<Exact128, gemm::kGroupRows, kOutE4M3, Exact128Tail>(args, ep, stream);
+  }
+  const int64_t tiles = rows * (args.N / 32);
+  if (tiles <= 2 * cus) return launch_tiles<TinyCfg, gemm::kGroupRows, kOutBF16>(args, ep, stream);
+  if (tiles <= 3 * cus || args.M <= 32 * args.G)
+    return launch_tiles<SmallCfg, gemm::kGroupRows, kOutBF16>(args, ep, stream);
+  if ((args.M / 256 + groups) * (args.N / 128) <= cus)
+    return launch_tiles<gemm::LargeTail, gemm::kGroupRows, kOutBF16>(args, ep, stream);
+  return launch_tiles<gemm::LargeCfg, gemm::kGroupRows, kOutBF16, gemm::LargeTail>(args, ep,
+                                                                                   stream);
 }
 
 }  // namespace fp8bs

@@ -66,6 +66,8 @@ struct Cfg {
   // columns of C per tile (half of the tile's B rows with GatedB)
   static constexpr bool GATED = false;
   static constexpr int BNO = BN;
+  // matrix products on f16 (see Exact)
+  static constexpr bool EXACT = false;
   // block-scaled B: the staged scales are the promotion factors
   // S_A(row) * S_W(block) for each of the tile's SB_COUNT weight blocks
   static constexpr bool PREMUL = true;
@@ -129,6 +131,16 @@ struct GatedB : C {
   static constexpr int LOADS = C::TILE_LOADS + 2 * SREG;
   static_assert(C::WN % 2 == 0 && BNO <= 128, "a half's columns share one weight block");
   static_assert(LOADS <= 63, "vmcnt range");
+};
+
+// The same tile configuration with exact products: the FP8 matrix instruction
+// aligns every 8 products of a lane to their largest and drops what lies 2^-13
+// below it (measured), which leaves 1.5e-5 of the sums' size; here the codes are
+// widened to f16 (exact) in registers and take four f16 instructions of 32 K each,
+// which round like FP32 sums but run at half the rate.
+template <class C>
+struct Exact : C {
+  static constexpr bool EXACT = true;
 };
 
 // s_waitcnt vmcnt(N) with the other counters left alone (gfx9 encoding).
@@ -582,6 +594,113 @@ __device__ __forceinline__ void compute_stage(const uint8_t* st, const float* sc
     for (int j = 0; j < C::FN; ++j) asm volatile("" : "+v"(acc[i][j]));
 }
 
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// Eight E4M3 codes (two dwords) as f16, exact.
+__device__ __forceinline__ f16x8 widen8(int lo, int hi) {
+  const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
+  const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+  const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
+  const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+  return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// What a step of the exact product hands to the next one: the widened operands of
+// its first row of tiles, the last pair of tiles, still to be promoted, and its
+// row's factors.
+template <class C>
+struct ExactState {
+  f16x8 a[4], b[C::FN][4];
+  v8i raw_b[2];    // of the last two B operands, still to be widened
+  v4f part[2];
+  float4 w, wn;    // factors of the row before and of the first row
+};
+
+// One K group with exact products (block-scaled B).  Quarter q of a lane's 32 K
+// bytes is the operand of instruction q, on both sides.  The wave's B operands
+// stay widened for the step; a row's A operands are widened while the last pair of
+// tiles of the row before uses theirs, quarter by quarter into the same registers,
+// and the next group's operands likewise around the last row, ahead of which the
+// waves meet (`meet`): all of this group's operands are in registers then and the
+// next group's copies have landed, so that no wave waits for LDS at a step's
+// start.  The promotion of a pair follows while the next one's two chains of four
+// instructions run.
+//
+// Bound by instruction issue: widening, promotions and matrix instructions share
+// it (4.5 VALU instructions per matrix one, 3.3 of them the widening's and the
+// promotions'; matrix cores busy 0.53).  Tiles of 256x256 widen less per product
+// but do not fit the registers (1.75 against 2.35 ms for 4096 x 36864 x 7168);
+// two stages in place of three take 1.96.
+template <class C, class Copy, class Meet>
+__device__ __forceinline__ void compute_step_exact(const uint8_t* st, const float* sc,
+                                                   const uint8_t* st_next, const float* sc_next,
+                                                   const FragOffs& fo, ExactState<C>& s,
+                                                   v4f (&acc)[C::FM][C::FN], Copy&& issue_copy_n,
+                                                   Meet&& meet) {
+  static_assert(C::PREMUL && C::FM >= 2 && C::FN == 4, "block-scaled B, four tiles to a row");
+  constexpr int NP = 2 * C::FM;  // pairs of tiles
+  constexpr int PER_ROW = (C::TILE_LOADS + C::FM - 2) / (C::FM - 1);
+  v8i raw_a, raw_b[4];
+  raw_b[2] = s.raw_b[0];
+  raw_b[3] = s.raw_b[1];
+  v4f part[2][2];
+  part[1][0] = s.part[0];
+  part[1][1] = s.part[1];
+  static_for<0, NP>([&](auto t_) {
+    constexpr int t = decltype(t_)::value, i = t / 2, h = t % 2;
+    constexpr bool last = i == C::FM - 1;
+    if constexpr (h == 0 && last) meet();
+    if constexpr (h == 0)
+      raw_a = load_frag(last ? st_next : st, fo.a_lo, fo.a_hi, last ? 0 : 16 * (i + 1) * 128);
+    if constexpr (last) {
+      raw_b[2 * h] = load_frag(st_next, fo.b_lo, fo.b_hi, 16 * 2 * h * 128);
+      raw_b[2 * h + 1] = load_frag(st_next, fo.b_lo, fo.b_hi, 16 * (2 * h + 1) * 128);
+    }
+    static_for<0, 4>([&](auto q_) {
+      constexpr int q = decltype(q_)::value;
+#pragma unroll
+      for (int d = 0; d < 2; ++d)
+        part[t & 1][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+            s.a[q], s.b[2 * h + d][q], q == 0 ? v4f{0.f, 0.f, 0.f, 0.f} : part[t & 1][d], 0, 0, 0);
+      // two of the eight promotions of the pair before
+      constexpr int u = (t + NP - 1) % NP, ui = u / 2, uj = 2 * (u % 2) + q / 2, r = 2 * (q & 1);
+      const float f0 = r == 0 ? s.w.x : s.w.z, f1 = r == 0 ? s.w.y : s.w.w;
+      const v4f& pp = part[(t + 1) & 1][q / 2];
+      acc[ui][uj][r] = __builtin_fmaf(pp[r], f0, acc[ui][uj][r]);
+      acc[ui][uj][r + 1] = __builtin_fmaf(pp[r + 1], f1, acc[ui][uj][r + 1]);
+      // operands of the next row or group
+      if (t == 0) {
+        s.b[2][q] = widen8(raw_b[2][2 * q], raw_b[2][2 * q + 1]);
+        s.b[3][q] = widen8(raw_b[3][2 * q], raw_b[3][2 * q + 1]);
+      }
+      if (last && h == 1) {
+        s.b[0][q] = widen8(raw_b[0][2 * q], raw_b[0][2 * q + 1]);
+        s.b[1][q] = widen8(raw_b[1][2 * q], raw_b[1][2 * q + 1]);
+      }
+      if (h == 1) s.a[q] = widen8(raw_a[2 * q], raw_a[2 * q + 1]);
+      __builtin_amdgcn_sched_barrier(0);  // LDS reads stay ahead of their use
+    });
+    if (h == 0) {
+      // the row before is promoted: this row's factors, and the next one's
+      s.w = s.wn;
+      s.wn = *reinterpret_cast<const float4*>(last ? sc_next + fo.sa : sc + fo.sa + 16 * (i + 1));
+    }
+    if (h == 1 && !last) {
+#pragma unroll
+      for (int c = i * PER_ROW; c < (i + 1) * PER_ROW && c < C::TILE_LOADS; ++c) issue_copy_n(c);
+    }
+  });
+  s.raw_b[0] = raw_b[2];
+  s.raw_b[1] = raw_b[3];
+  s.part[0] = part[1][0];
+  s.part[1] = part[1][1];
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) asm volatile("" : "+v"(acc[i][j]));
+}
+
 // The LDS arrays of the kernel: one per pipeline stage for the tiles and one
 // per stage for the scales (distinct objects, so that the compiler can tell
 // the stages apart when it tracks copies in flight).
@@ -764,46 +883,12 @@ __device__ __forceinline__ void store_tile_e4m3(const GemmArgs& p, const TileCoo
   }
 }
 
-// Epilogue of the plain product: the FP32 sums are stored as they are.
-struct NoEpilogue {
-  static constexpr bool kStream = false;  // see store_tile
-  template <class C>
-  struct Early {};
-  template <class C>
-  __device__ __forceinline__ void load(const GemmArgs&, const TileCoords&, int, int, int,
-                                       Early<C>&) const {}
-  template <class C>
-  __device__ __forceinline__ void apply(const GemmArgs&, const TileCoords&,
-                                        v4f (&)[C::FM][C::FN], int, int, int,
-                                        const Early<C>&) const {}
-};
-
-// ep.load<C>(p, t, wm, wn, lane, early) may load operands of its own before the
-// K loop; ep.apply<C>(p, t, acc, wm, wn, lane, early) may change a wave's
-// finished sums before they are stored.  With GatedB, ep.finish<C, OUT>(p, t,
-// acc, wm, wn, lane, LDS) takes the sums and stores all there is.
-template <class C, int OUT, class E = NoEpilogue>
-__device__ __forceinline__ void block_gemm_body(const GemmArgs& p, const TileCoords& t,
-                                                const LdsSet& L, const E& ep = E()) {
-  // wave index in an SGPR so that per-wave values stay scalar
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  const int wm = wave / C::WN, wn = wave % C::WN;
+// The K loop of a tile.
+template <class C>
+__device__ __forceinline__ void k_loop(const GemmArgs& p, const TileCoords& t, const LdsSet& L,
+                                       const LoadPlan<C>& lp, const FragOffs& fo, const Rsrc& rs,
+                                       int wave, v4f (&acc)[C::FM][C::FN]) {
   const int64_t KB = t.KB;
-
-  LoadPlan<C> lp;
-  make_plan<C>(p, t, wave, lane, lp);
-  const FragOffs fo = frag_offsets<C>(wm, wn, lane);
-  const Rsrc rs = make_rsrc_set<C>(p, t);
-  typename E::template Early<C> early;
-  ep.template load<C>(p, t, wm, wn, lane, early);
-
-  v4f acc[C::FM][C::FN];
-#pragma unroll
-  for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-    for (int j = 0; j < C::FN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-
   // Pipeline: group g lives in LDS stage g % STAGES.  Step kb waits for this
   // wave's copies of group kb (leaving the copies of later groups in flight),
   // meets the other waves at a barrier (so every copy of group kb is visible
@@ -901,7 +986,129 @@ __device__ __forceinline__ void block_gemm_body(const GemmArgs& p, const TileCoo
       retire_scales(u % C::STAGES, sv, SLEAD == 0 ? refill : k + 1 < KB);
     }
   }
+}
 
+// The K loop with exact products: three LDS stages, group g in stage g % 3.  In
+// the step of group k the copies of group k + 2 are issued into the stage of group
+// k - 1, which every wave has left when it meets the others in step k - 1; they
+// land before the meeting of step k + 1.  Past the last group the copies repeat
+// it, into stages that nobody uses, so that all wait counts are constants.
+template <class C>
+__device__ __forceinline__ void exact_k_loop(const GemmArgs& p, const TileCoords& t,
+                                             const LdsSet& L, const LoadPlan<C>& lp,
+                                             const FragOffs& fo, const Rsrc& rs, int wave,
+                                             v4f (&acc)[C::FM][C::FN]) {
+  static_assert(C::STAGES == 3, "three stages");
+  const int64_t KB = t.KB;
+  auto group = [&](int64_t g) { return g < KB ? g : KB - 1; };
+  ScaleRegs<C> ahead;  // scales of the group after the next one
+  {
+    ScaleRegs<C> sv;
+    load_scales<C>(p, t, lp, 0, sv);
+    issue_stage<C>(p, rs, lp, 0, L.st[0], wave);
+    store_scales<C>(L.sc[0], sv);
+    load_scales<C>(p, t, lp, group(1), ahead);
+    issue_stage<C>(p, rs, lp, group(1), L.st[1], wave);
+  }
+  barrier_after_vmcnt<C::LOADS>();
+  ExactState<C> s;
+  {
+    const v8i ra = load_frag(L.st[0], fo.a_lo, fo.a_hi, 0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) s.a[q] = widen8(ra[2 * q], ra[2 * q + 1]);
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+      const v8i rb = load_frag(L.st[0], fo.b_lo, fo.b_hi, 16 * j * 128);
+      if (j >= 2) s.raw_b[j - 2] = rb;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) s.b[j][q] = widen8(rb[2 * q], rb[2 * q + 1]);
+    }
+    s.part[0] = s.part[1] = v4f{0.f, 0.f, 0.f, 0.f};
+    s.w = float4{0.f, 0.f, 0.f, 0.f};
+    s.wn = *reinterpret_cast<const float4*>(L.sc[0] + fo.sa);
+  }
+  auto step = [&](int64_t k, auto U_) {
+    constexpr int U = decltype(U_)::value, N1 = (U + 1) % 3, N2 = (U + 2) % 3;
+    ScaleRegs<C> sv;
+    const int64_t kn = group(k + 2);
+    load_scales<C>(p, t, lp, kn, sv);
+    // keep the scale loads ahead of this step's tile copies (in-order
+    // completion then lets their wait leave the tile copies in flight)
+    __builtin_amdgcn_sched_barrier(0);
+    compute_step_exact<C>(
+        L.st[U], L.sc[U], L.st[N1], L.sc[N1], fo, s, acc,
+        [&](int c) { issue_copy<C>(p, rs, lp, kn, L.st[N2], wave, c); },
+        [&] {
+          store_scales<C>(L.sc[N1], ahead);
+          barrier_after_vmcnt<C::LOADS>();
+        });
+    ahead = sv;
+  };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  int64_t k = 0;
+  for (; k + 3 <= KB; k += 3) {
+    step(k, I0{});
+    step(k + 1, I1{});
+    step(k + 2, I2{});
+  }
+  if (k < KB) step(k, I0{});
+  if (k + 1 < KB) step(k + 1, I1{});
+  // the last pair's promotion; the repeated copies land before LDS is used again
+  const float f[4] = {s.w.x, s.w.y, s.w.z, s.w.w};
+#pragma unroll
+  for (int d = 0; d < 2; ++d)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      acc[C::FM - 1][2 + d][r] = __builtin_fmaf(s.part[d][r], f[r], acc[C::FM - 1][2 + d][r]);
+  wait_vmcnt<0>();
+}
+
+// Epilogue of the plain product: the FP32 sums are stored as they are.
+struct NoEpilogue {
+  static constexpr bool kStream = false;  // see store_tile
+  template <class C>
+  struct Early {};
+  template <class C>
+  __device__ __forceinline__ void load(const GemmArgs&, const TileCoords&, int, int, int,
+                                       Early<C>&) const {}
+  template <class C>
+  __device__ __forceinline__ void apply(const GemmArgs&, const TileCoords&,
+                                        v4f (&)[C::FM][C::FN], int, int, int,
+                                        const Early<C>&) const {}
+};
+
+// ep.load<C>(p, t, wm, wn, lane, early) may load operands of its own before the
+// K loop; ep.apply<C>(p, t, acc, wm, wn, lane, early) may change a wave's
+// finished sums before they are stored.  With GatedB, ep.finish<C, OUT>(p, t,
+// acc, wm, wn, lane, LDS) takes the sums and stores all there is.
+template <class C, int OUT, class E = NoEpilogue>
+__device__ __forceinline__ void block_gemm_body(const GemmArgs& p, const TileCoords& t,
+                                                const LdsSet& L, const E& ep = E()) {
+  // wave index in an SGPR so that per-wave values stay scalar
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  const int wm = wave / C::WN, wn = wave % C::WN;
+
+  LoadPlan<C> lp;
+  make_plan<C>(p, t, wave, lane, lp);
+  const FragOffs fo = frag_offsets<C>(wm, wn, lane);
+  const Rsrc rs = make_rsrc_set<C>(p, t);
+  typename E::template Early<C> early;
+  ep.template load<C>(p, t, wm, wn, lane, early);
+
+  v4f acc[C::FM][C::FN];
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  if constexpr (C::EXACT) {
+    exact_k_loop<C>(p, t, L, lp, fo, rs, wave, acc);
+  } else {
+    k_loop<C>(p, t, L, lp, fo, rs, wave, acc);
+  }
   if constexpr (C::GATED) {
     ep.template finish<C, OUT>(p, t, acc, wm, wn, lane, L.st[0], L.st[1], L.red, L.rcp);
   } else {
