@@ -328,6 +328,10 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_kteam_kernel(FewArgs p, 
     const int last_kb = wave + kWaves * (T - 1);
     auto kb_of = [&](int t) -> int { return t < T ? wave + kWaves * t : last_kb; };
 
+    // The gated product of up to 16 rows reads its weight past the caches: it is
+    // read once, and in a model's step the next layer's weights follow.  One row of
+    // 18432 x 7168 after others' weights 51.5 -> 46.8 us, sixteen 52.1 -> 50.8.
+    constexpr int kPolicy = is_gated(MODE) && MT == 1 ? 2 : 0;
     // copies [c0, c1) of group t into stage st
     auto issue_w = [&](int t, uint8_t* st, int c0, int c1) {
       const int kb = kb_of(t);
@@ -336,7 +340,7 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_kteam_kernel(FewArgs p, 
         if (c < c0 || c >= c1) continue;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
             wrs, (gemm::lds_void*)(st + wave * C::WAVE_BYTES + c * 1024), 16, voff[c], kb * 128,
-            0, 0);
+            0, kPolicy);
       }
     };
     // A values of group t for tile j of A into `ar`
@@ -749,7 +753,11 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_shared_kernel(FewArgs p,
 }
 
 // Weight rows per workgroup (RC 8-row copies): the fewest that put the
-// whole W on at most one workgroup per compute unit, from a fixed set.
+// whole W on at most one workgroup per compute unit, from a fixed set.  us for the
+// gated product of one row with RC 1 / 2 / 3 / 4 / 9:
+//   4096 x 7168   26.2  16.4  17.5  13.8  17.9
+//   2048 x 7168   15.0  11.1  11.4  11.6  16.2
+//   4096 x 2048    9.5   7.3   7.9   6.4   8.1
 template <class F>
 hipError_t with_rows(const FewArgs& p, Mode mode, int cus, F&& f) {
   const int64_t rows = is_gated(mode) ? 2 * p.N : p.N;
@@ -761,7 +769,9 @@ hipError_t with_rows(const FewArgs& p, Mode mode, int cus, F&& f) {
     return f(RC_, dim3((unsigned)blocks));
   };
   if (per <= 8) return go(std::integral_constant<int, 1>{});
+  if (is_gated(mode) && per <= 16) return go(std::integral_constant<int, 2>{});
   if (per <= 24) return go(std::integral_constant<int, 3>{});
+  if (is_gated(mode) && per <= 32) return go(std::integral_constant<int, 4>{});
   return go(std::integral_constant<int, 9>{});
 }
 
@@ -769,6 +779,8 @@ template <int MT, bool FUSED>
 hipError_t launch_mt(const FewArgs& p, Mode mode, const Epilogue& e, int cus, hipStream_t stream) {
   return with_rows(p, mode, cus, [&](auto RC_, dim3 grid) {
     constexpr int RC = decltype(RC_)::value;
+    constexpr Mode kPlain = RC % 2 ? kStore : kGated;  // RC of 2 and 4: gated only
+    constexpr Mode kLinear = RC % 2 ? kEpilogue : kGated;
     const dim3 block(kWaves * 64);
     switch (mode) {
       case kGated:
@@ -778,10 +790,10 @@ hipError_t launch_mt(const FewArgs& p, Mode mode, const Epilogue& e, int cus, hi
         return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kGatedExact>, grid, block,
                              stream, p, e);
       case kEpilogue:
-        return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kEpilogue>, grid, block, stream,
+        return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kLinear>, grid, block, stream,
                              p, e);
       default:
-        return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kStore>, grid, block, stream, p,
+        return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kPlain>, grid, block, stream, p,
                              e);
     }
   });
@@ -791,6 +803,8 @@ hipError_t launch_shared(const FewArgs& p, Mode mode, const Epilogue& e, int cus
                          hipStream_t stream) {
   return with_rows(p, mode, cus, [&](auto RC_, dim3 grid) {
     constexpr int RC = decltype(RC_)::value;
+    constexpr Mode kPlain = RC % 2 ? kStore : kGated;  // RC of 2 and 4: gated only
+    constexpr Mode kLinear = RC % 2 ? kEpilogue : kGated;
     const dim3 block(kWaves * 64);
     switch (mode) {
       case kGated:
@@ -798,9 +812,9 @@ hipError_t launch_shared(const FewArgs& p, Mode mode, const Epilogue& e, int cus
       case kGatedExact:
         return launch_kernel(few_rows_shared_kernel<RC, kGatedExact>, grid, block, stream, p, e);
       case kEpilogue:
-        return launch_kernel(few_rows_shared_kernel<RC, kEpilogue>, grid, block, stream, p, e);
+        return launch_kernel(few_rows_shared_kernel<RC, kLinear>, grid, block, stream, p, e);
       default:
-        return launch_kernel(few_rows_shared_kernel<RC, kStore>, grid, block, stream, p, e);
+        return launch_kernel(few_rows_shared_kernel<RC, kPlain>, grid, block, stream, p, e);
     }
   });
 }
