@@ -12,7 +12,11 @@
 // read once and nothing but codes and scales is written.  A thread holds 8
 // values of each of 4 rows (16 lanes span a row): row maxima are a 16-lane
 // reduction, column maxima go over the thread's rows, its wave's row groups and
-// the waves.  The codes are transposed through LDS, 128x128 bytes at a time.
+// the waves.  The codes are transposed through LDS, all three blocks between the
+// same barriers.  4096 x 18432, silu: 166 us, 5.0 TB/s beside a plain copy's 5.2
+// (842 MB, each input read once; 184 with the blocks dealt round-robin over the
+// XCDs, 170 with the column codes left to the caches).  333 x 2048: 11 us, launch
+// and latency.
 
 #include "epilogue.hpp"
 #include "transpose.hpp"
@@ -38,16 +42,20 @@ __device__ __forceinline__ u32x2 codes8(const float (&v)[8], const float (&r)[8]
 }
 
 constexpr int kThreads = 512;
+constexpr int kWaves = kThreads / 64;
 constexpr int kRows = 4;     // rows per thread, 32 apart
 constexpr int kPitch = 132;  // LDS row pitch of the staged codes (bytes)
 
-// The 128x128 block v (kRows rows of 8 columns per thread) as codes per column,
-// transposed to qt[n0 + c][m0 ..], scales to st.  cmax: 8 x 128 floats, rcp: 128,
-// tile: 128 * kPitch bytes, all free on entry and on return.
-__device__ __forceinline__ void store_columns(const float (&v)[kRows][8], uint8_t* qt, int64_t ldqt,
-                                              float* st, float (*cmax)[128], float* rcp,
-                                              uint8_t* tile) {
-  const int lane = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+// One 128x128 block on its way to codes per column, transposed.
+struct Columns {
+  float cmax[kWaves][128];
+  float rcp[128];
+  uint8_t tile[128 * kPitch];
+};
+
+// Column maxima of the block v (kRows rows of 8 columns per thread) by waves.
+__device__ __forceinline__ void column_maxima(const float (&v)[kRows][8], Columns& L) {
+  const int lane = threadIdx.x & 15;
   float cm[8];
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
@@ -59,42 +67,50 @@ __device__ __forceinline__ void store_columns(const float (&v)[kRows][8], uint8_
   }
   if ((threadIdx.x & 63) < 16) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) cmax[threadIdx.x >> 6][lane * 8 + c] = cm[c];
+    for (int c = 0; c < 8; ++c) L.cmax[threadIdx.x >> 6][lane * 8 + c] = cm[c];
   }
-  __syncthreads();
-  if (threadIdx.x < 128) {
-    float m = 0.0f;
+}
+
+// Scale and reciprocal of column c.
+__device__ __forceinline__ void column_scale(int c, Columns& L, float* st) {
+  float m = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kThreads / 64; ++w) m = fmaxf(m, cmax[w][threadIdx.x]);
-    float s, r;
-    group_scale(m, s, r);
-    rcp[threadIdx.x] = r;
-    st[threadIdx.x] = s;
-  }
-  __syncthreads();
+  for (int w = 0; w < kWaves; ++w) m = fmaxf(m, L.cmax[w][c]);
+  float s, r;
+  group_scale(m, s, r);
+  L.rcp[c] = r;
+  st[c] = s;
+}
+
+__device__ __forceinline__ void stage_codes(const float (&v)[kRows][8], Columns& L) {
+  const int lane = threadIdx.x & 15, r0 = threadIdx.x >> 4;
   float r[8];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) r[c] = rcp[lane * 8 + c];
+  for (int c = 0; c < 8; ++c) r[c] = L.rcp[lane * 8 + c];
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const u32x2 w = codes8(v[i], r);
-    uint32_t* const dst = reinterpret_cast<uint32_t*>(tile + (r0 + 32 * i) * kPitch + lane * 8);
+    uint32_t* const dst = reinterpret_cast<uint32_t*>(L.tile + (r0 + 32 * i) * kPitch + lane * 8);
     dst[0] = w.x;
     dst[1] = w.y;
   }
-  __syncthreads();
-  // 16 consecutive threads cover the 128 rows of one output row (whole lines)
-  const int m0 = lane * 8, c0 = r0 * 4;
+}
+
+// The staged codes to qt[c][0 .. 127]: 16 consecutive threads cover the 128 rows
+// of one output row (whole lines).
+__device__ __forceinline__ void store_columns(const Columns& L, uint8_t* qt, int64_t ldqt) {
+  const int m0 = (threadIdx.x & 15) * 8, c0 = (threadIdx.x >> 4) * 4;
   uint32_t in[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    in[i] = *reinterpret_cast<const uint32_t*>(tile + (m0 + i) * kPitch + c0);
+    in[i] = *reinterpret_cast<const uint32_t*>(L.tile + (m0 + i) * kPitch + c0);
   u32x2 out[4];
   transpose8x4(in, out);
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
-    *reinterpret_cast<u32x2*>(qt + (int64_t)(c0 + c) * ldqt + m0) = out[c];
-  __syncthreads();
+  for (int c = 0; c < 4; ++c) {
+    __builtin_nontemporal_store(out[c],
+                                reinterpret_cast<u32x2*>(qt + (int64_t)(c0 + c) * ldqt + m0));
+  }
 }
 
 // The block's rows as codes per 1x128 tile (rows past M are not stored).
@@ -120,11 +136,13 @@ __device__ __forceinline__ void store_rows(const float (&v)[kRows][8], int64_t r
 
 template <int ACT>
 __global__ __launch_bounds__(kThreads) void gated_backward_kernel(GatedGradArgs a) {
-  __shared__ float cmax[kThreads / 64][128];
-  __shared__ float rcp[128];
-  __shared__ __attribute__((aligned(16))) uint8_t tile[128 * kPitch];
+  __shared__ __attribute__((aligned(16))) Columns L[3];  // dgate, dup, y
   const int64_t NB = a.N / 128;
-  const int64_t nb = blockIdx.x % NB, mb = blockIdx.x / NB;
+  // each XCD a contiguous run of blocks (workgroup b runs on XCD b mod 8), so that
+  // neighbouring stretches of a row of dy and z come through one L2
+  const int64_t x = blockIdx.x % 8, n = gridDim.x / 8, r8 = gridDim.x % 8;
+  const int64_t block = x * n + (x < r8 ? x : r8) + blockIdx.x / 8;
+  const int64_t nb = block % NB, mb = block / NB;
   const int lane = threadIdx.x & 15;
   const int64_t row0 = mb * 128 + (threadIdx.x >> 4), col = nb * 128 + lane * 8;
   float dg[kRows][8], du[kRows][8], y[kRows][8];
@@ -155,12 +173,27 @@ __global__ __launch_bounds__(kThreads) void gated_backward_kernel(GatedGradArgs 
   }
   store_rows(dg, row0, a.M, a.q + nb * 128, a.ldq, a.s + nb * a.lds);
   store_rows(du, row0, a.M, a.q + a.N + nb * 128, a.ldq, a.s + (NB + nb) * a.lds);
+  column_maxima(dg, L[0]);
+  column_maxima(du, L[1]);
+  if (a.yt) column_maxima(y, L[2]);
+  __syncthreads();
   const int64_t n0 = nb * 128, m0 = mb * 128;
-  store_columns(dg, a.qt + n0 * a.ldqt + m0, a.ldqt, a.st + mb * a.ldst + n0, cmax, rcp, tile);
-  store_columns(du, a.qt + (a.N + n0) * a.ldqt + m0, a.ldqt, a.st + mb * a.ldst + a.N + n0, cmax,
-                rcp, tile);
-  if (a.yt)
-    store_columns(y, a.yt + n0 * a.ldyt + m0, a.ldyt, a.syt + mb * a.ldsyt + n0, cmax, rcp, tile);
+  const int c = threadIdx.x & 127;
+  if (threadIdx.x < 128) {
+    column_scale(c, L[0], a.st + mb * a.ldst + n0);
+  } else if (threadIdx.x < 256) {
+    column_scale(c, L[1], a.st + mb * a.ldst + a.N + n0);
+  } else if (threadIdx.x < 384 && a.yt) {
+    column_scale(c, L[2], a.syt + mb * a.ldsyt + n0);
+  }
+  __syncthreads();
+  stage_codes(dg, L[0]);
+  stage_codes(du, L[1]);
+  if (a.yt) stage_codes(y, L[2]);
+  __syncthreads();
+  store_columns(L[0], a.qt + n0 * a.ldqt + m0, a.ldqt);
+  store_columns(L[1], a.qt + (a.N + n0) * a.ldqt + m0, a.ldqt);
+  if (a.yt) store_columns(L[2], a.yt + n0 * a.ldyt + m0, a.ldyt);
 }
 
 }  // namespace

@@ -30,17 +30,28 @@ __device__ __forceinline__ float sum_wave64(float v) {
 }
 
 // Sum over the threads of a row (blockDim.x, whole waves); every thread
-// receives it, always in the same order.  `red`: 16 floats that no wave of the
-// row still reads from an earlier call.
+// receives it, always in the same order.  `red`: 16 floats, shared by the
+// workgroup's rows, that no wave still reads from an earlier call.
 __device__ __forceinline__ float sum_row(float v, float* red) {
   v = sum_wave64(v);
   const int waves = (int)blockDim.x >> 6;
-  if (waves == 1) return v;
+  if (waves == 1) return v;  // rows of one wave: nobody waits
+  red += (int)threadIdx.y * waves;
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
   float s = 0.0f;
   for (int w = 0; w < waves; ++w) s += red[w];
   return s;
+}
+
+// 16 or 8 bytes to p; STREAM: past the caches' retention.
+template <bool STREAM, class T>
+__device__ __forceinline__ void store_vec(T v, void* p) {
+  if constexpr (STREAM) {
+    __builtin_nontemporal_store(v, static_cast<T*>(p));
+  } else {
+    *static_cast<T*>(p) = v;
+  }
 }
 
 __device__ __forceinline__ void unpack8(const u32x4 v, float (&f)[8]) {
@@ -67,7 +78,7 @@ __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
 // this scale, whose square takes no bit from a sum that large.
 constexpr float kTiny = 0x1p-80f;
 
-template <int V>
+template <int V, bool STREAM>
 __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a) {
   __shared__ float red[2][16];
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
@@ -75,12 +86,16 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a) {
   const int T = (int)blockDim.x;
   const int K = (int)a.K;
   u32x4 h[V];
+  // the weight is on its way during the sum, where registers allow
+  constexpr bool EARLY = V <= 2;
+  float g[EARLY ? V : 1][8];
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int col = (i * T + (int)threadIdx.x) * 8;
     h[i] = u32x4{0u, 0u, 0u, 0u};
     if (col >= K) continue;
+    if constexpr (EARLY) load8(a.weight + col, g[i]);
     h[i] = *reinterpret_cast<const u32x4*>(a.x + row * a.ldx + col);
     if (a.residual) {
       const u32x4 r = *reinterpret_cast<const u32x4*>(a.residual + row * a.ldr + col);
@@ -91,7 +106,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a) {
       for (int e = 0; e < 8; ++e) f[e] += fr[e];
       h[i] = pack8(f);
     }
-    if (a.h) *reinterpret_cast<u32x4*>(a.h + row * a.ldh + col) = h[i];
+    if (a.h) store_vec<STREAM>(h[i], a.h + row * a.ldh + col);
     float f[8];
     unpack8(h[i], f);
 #pragma unroll
@@ -116,12 +131,12 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a) {
   for (int i = 0; i < V; ++i) {
     const int col = (i * T + (int)threadIdx.x) * 8;
     if (col >= K) continue;
-    float f[8], g[8];
+    float f[8];
     unpack8(h[i], f);
-    load8(a.weight + col, g);
+    if constexpr (!EARLY) load8(a.weight + col, g[0]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = f[e] * rstd * g[e];
-    if (a.y) *reinterpret_cast<u32x4*>(a.y + row * a.ldy + col) = pack8(f);
+    for (int e = 0; e < 8; ++e) f[e] = f[e] * rstd * g[EARLY ? i : 0][e];
+    if (a.y) store_vec<STREAM>(pack8(f), a.y + row * a.ldy + col);
     if (a.q) {
       float m = 0.0f;
 #pragma unroll
@@ -132,50 +147,68 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a) {
       lo = cvt2_e4m3<true>(f[2] * r, f[3] * r, lo);
       uint32_t hi = cvt2_e4m3<false>(f[4] * r, f[5] * r, 0u);
       hi = cvt2_e4m3<true>(f[6] * r, f[7] * r, hi);
-      *reinterpret_cast<u32x2*>(a.q + row * a.ldq + col) = u32x2{lo, hi};
+      store_vec<STREAM>(u32x2{lo, hi}, a.q + row * a.ldq + col);
       if ((threadIdx.x & 15) == 0) a.s[(int64_t)(col / 128) * a.lds + row] = s;
     }
   }
 }
 
-// Rows b, b + blocks, ... of one workgroup; its sums for dg go to part[b].
-template <int V>
+// R rows at a time (blockDim.y), workgroup b the groups b, b + blocks, ... of
+// them; its sums for dg go to part[b].
+template <int V, bool STREAM>
 __global__ __launch_bounds__(1024) void rmsnorm_backward_kernel(NormGradArgs a) {
   __shared__ float red[2][16];
-  __shared__ float fold[64 * 8 * 4];  // rows of one wave: the other rows' sums
+  __shared__ __attribute__((aligned(16))) float fold[V > 2 ? 4 : 512 * 8 * V];
   const int T = (int)blockDim.x, K = (int)a.K, R = (int)blockDim.y;
-  float g[V][8], dg[V][8];
+  // the weight stays in registers where they allow it
+  constexpr bool KEEP = V <= 2;
+  float g[KEEP ? V : 1][8], dg[V][8];
+  auto weight = [&](int i) -> const float (&)[8] {
+    if constexpr (!KEEP) load8(a.weight + (i * T + (int)threadIdx.x) * 8, g[0]);
+    return g[KEEP ? i : 0];
+  };
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int col = (i * T + (int)threadIdx.x) * 8;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dg[i][e] = g[i][e] = 0.0f;
-    if (col < K) load8(a.weight + col, g[i]);
+    for (int e = 0; e < 8; ++e) dg[i][e] = g[KEEP ? i : 0][e] = 0.0f;
+    if constexpr (KEEP) {
+      if (col < K) load8(a.weight + col, g[i]);
+    }
   }
+  auto load = [&](const uint16_t* p) {
+    const u32x4* v = reinterpret_cast<const u32x4*>(p);
+    return STREAM ? __builtin_nontemporal_load(v) : *v;
+  };
   int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * R + threadIdx.y; row < a.M;
-       row += (int64_t)gridDim.x * R, turn ^= 1) {
+  // all rows of a group go through the same number of turns: they may meet
+  for (int64_t first = (int64_t)blockIdx.x * R; first < a.M;
+       first += (int64_t)gridDim.x * R, turn ^= 1) {
+    const int64_t row = first + threadIdx.y;
+    const bool live = row < a.M;
     u32x4 y[V], h[V], d[V];
-    const float rstd = a.rstd[row];
+    const float rstd = live ? a.rstd[row] : 0.0f;
     float c = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int col = (i * T + (int)threadIdx.x) * 8;
       y[i] = h[i] = d[i] = u32x4{0u, 0u, 0u, 0u};
-      if (col >= K) continue;
-      y[i] = *reinterpret_cast<const u32x4*>(a.dy + row * a.lddy + col);
-      h[i] = *reinterpret_cast<const u32x4*>(a.h + row * a.ldh + col);
-      if (a.dh) d[i] = *reinterpret_cast<const u32x4*>(a.dh + row * a.lddh + col);
+      if (col >= K || !live) continue;
+      y[i] = load(a.dy + row * a.lddy + col);
+      h[i] = load(a.h + row * a.ldh + col);
+      if (a.dh) d[i] = load(a.dh + row * a.lddh + col);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
+      if ((i * T + (int)threadIdx.x) * 8 >= K) continue;
       float fy[8], fh[8];
       unpack8(y[i], fy);
       unpack8(h[i], fh);
+      const float (&w)[8] = weight(i);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float n = fh[e] * rstd;
-        c = __builtin_fmaf(fy[e] * g[i][e], n, c);
+        c = __builtin_fmaf(fy[e] * w[e], n, c);
         dg[i][e] = __builtin_fmaf(fy[e], n, dg[i][e]);
       }
     }
@@ -183,27 +216,41 @@ __global__ __launch_bounds__(1024) void rmsnorm_backward_kernel(NormGradArgs a) 
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int col = (i * T + (int)threadIdx.x) * 8;
-      if (col >= K) continue;
+      if (col >= K || !live) continue;
       float fy[8], fh[8], fd[8];
       unpack8(y[i], fy);
       unpack8(h[i], fh);
       unpack8(d[i], fd);
+      const float (&w)[8] = weight(i);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        fd[e] = __builtin_fmaf(rstd, fy[e] * g[i][e] - fh[e] * rstd * c, fd[e]);
+        fd[e] = __builtin_fmaf(rstd, fy[e] * w[e] - fh[e] * rstd * c, fd[e]);
       *reinterpret_cast<u32x4*>(a.dx + row * a.lddx + col) = pack8(fd);
     }
   }
-  float* const out = a.part + (int64_t)blockIdx.x * K;
-  if (R > 1) {  // V == 1, T == 64: added up in row order
+  // the rows' sums, halves onto halves
+  if constexpr (V <= 2) {
+    for (int half = R / 2; half > 0; half /= 2) {
+      const int y = (int)threadIdx.y;
+      __syncthreads();
+      if (y >= half && y < 2 * half) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) fold[(threadIdx.y * 8 + e) * 64 + threadIdx.x] = dg[0][e];
-    __syncthreads();
-    if (threadIdx.y != 0) return;
-    for (int r = 1; r < R; ++r)
+        for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) dg[0][e] += fold[(r * 8 + e) * 64 + threadIdx.x];
+          for (int e = 0; e < 8; ++e)
+            fold[((i * 8 + e) * half + y - half) * T + threadIdx.x] = dg[i][e];
+      }
+      __syncthreads();
+      if (y < half) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dg[i][e] += fold[((i * 8 + e) * half + y) * T + threadIdx.x];
+      }
+    }
   }
+  if (threadIdx.y != 0) return;
+  float* const out = a.part + (int64_t)blockIdx.x * K;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int col = (i * T + (int)threadIdx.x) * 8;
@@ -214,24 +261,28 @@ __global__ __launch_bounds__(1024) void rmsnorm_backward_kernel(NormGradArgs a) 
   }
 }
 
-// dg from the workgroups' sums: 64 columns per workgroup, its four waves taking
-// every fourth sum (a fixed order).
-__global__ __launch_bounds__(256) void rmsnorm_weight_kernel(const float* part, int parts,
-                                                             int64_t K, float* dg) {
-  __shared__ float sum[4][64];
+// dg from the workgroups' sums: 64 columns per workgroup, its sixteen waves taking
+// every sixteenth sum, all their loads at once (a fixed order).
+__global__ __launch_bounds__(1024) void rmsnorm_weight_kernel(const float* part, int parts,
+                                                              int64_t K, float* dg) {
+  __shared__ float sum[16][64];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t k = (int64_t)blockIdx.x * 64 + lane;  // K is a multiple of 128
   float s = 0.0f;
-#pragma unroll 8
-  for (int b = wave; b < parts; b += 4) s += part[b * K + k];
+#pragma unroll 16
+  for (int b = wave; b < parts; b += 16) s += part[b * K + k];
   sum[wave][lane] = s;
   __syncthreads();
-  if (wave == 0) dg[k] = (sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]);
+  if (wave != 0) return;
+  s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) s += sum[w][lane];
+  dg[k] = s;
 }
 
 // Threads of a row and loads of 8 values per thread.
 struct RowPlan {
-  int vecs, threads, rows;  // rows: rows per workgroup (of one wave each)
+  int vecs, threads;
 };
 
 RowPlan row_plan(int64_t K) {
@@ -239,28 +290,48 @@ RowPlan row_plan(int64_t K) {
   RowPlan p;
   p.vecs = lanes <= 512 ? 1 : lanes <= 2048 ? 2 : 4;
   p.threads = ((lanes + p.vecs - 1) / p.vecs + 63) / 64 * 64;
-  p.rows = p.threads == 64 ? 4 : 1;
   return p;
 }
 
-// Workgroups of the backward pass, each with its own sums for dg.
+// Workgroups of the backward pass, each with its own sums for dg, at most one per
+// compute unit, and rows that one takes at a time, up to 1024 threads: 16384 x 1024
+// by two waves to a compute unit 79 us, by sixteen 31 (two workgroups each, with
+// twice the sums, 34).  Below 64 workgroups one row at a time; above, few
+// workgroups pay, their sums are read again (333 x 2048 by 167 of them 9.8 us, by
+// 84 8.6; 1531 x 512 by 192 10.1, by 96 8.8).
 constexpr int64_t kNormParts = 256;
+int rows_at_once(int64_t M, int threads) {
+  int r = 1;
+  while (2 * r * threads <= 1024 && r * 64 < M) r *= 2;
+  return r;
+}
 int64_t norm_parts(int64_t M, int64_t K) {
-  const int64_t rows = row_plan(K).rows, blocks = (M + rows - 1) / rows;
+  const int64_t rows = rows_at_once(M, row_plan(K).threads), blocks = (M + rows - 1) / rows;
   return blocks < kNormParts ? blocks : kNormParts;
 }
+
+// Elements from which on outputs are stored, and the backward pass's inputs read,
+// past the caches' retention: 4096 x 7168 forward 46 -> 34 us, backward 51 -> 49.
+constexpr int64_t kStreamFrom = int64_t(1) << 21;
 
 }  // namespace
 
 hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t stream) {
   const RowPlan p = row_plan(a.K);
-  const int64_t blocks = (a.M + p.rows - 1) / p.rows;
+  const int64_t rows = p.threads == 64 ? 4 : 1;  // per workgroup
+  const int64_t blocks = (a.M + rows - 1) / rows;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  const dim3 grid((unsigned)blocks), block((unsigned)p.threads, (unsigned)p.rows);
+  const dim3 grid((unsigned)blocks), block((unsigned)p.threads, (unsigned)rows);
+  const bool stream_out = a.M * a.K >= kStreamFrom;
+  auto go = [&](auto V) {
+    constexpr int v = decltype(V)::value;
+    return stream_out ? launch_kernel(rmsnorm_kernel<v, true>, grid, block, stream, a)
+                      : launch_kernel(rmsnorm_kernel<v, false>, grid, block, stream, a);
+  };
   switch (p.vecs) {
-    case 1: return launch_kernel(rmsnorm_kernel<1>, grid, block, stream, a);
-    case 2: return launch_kernel(rmsnorm_kernel<2>, grid, block, stream, a);
-    default: return launch_kernel(rmsnorm_kernel<4>, grid, block, stream, a);
+    case 1: return go(std::integral_constant<int, 1>{});
+    case 2: return go(std::integral_constant<int, 2>{});
+    default: return go(std::integral_constant<int, 4>{});
   }
 }
 
@@ -274,19 +345,25 @@ hipError_t launch_rmsnorm_backward(NormGradArgs a, float* dg, void* workspace,
   const int64_t parts = norm_parts(a.M, a.K);
   // one workgroup: its sums are dg
   a.part = parts == 1 ? dg : static_cast<float*>(workspace);
-  const dim3 block((unsigned)p.threads, (unsigned)p.rows);
+  const dim3 block((unsigned)p.threads, (unsigned)rows_at_once(a.M, p.threads));
   hipError_t e = hipSuccess;
   if (parts > 0) {
     const dim3 grid((unsigned)parts);
+    auto go = [&](auto V) {
+      constexpr int v = decltype(V)::value;
+      return a.M * a.K >= kStreamFrom
+                 ? launch_kernel(rmsnorm_backward_kernel<v, true>, grid, block, stream, a)
+                 : launch_kernel(rmsnorm_backward_kernel<v, false>, grid, block, stream, a);
+    };
     switch (p.vecs) {
-      case 1: e = launch_kernel(rmsnorm_backward_kernel<1>, grid, block, stream, a); break;
-      case 2: e = launch_kernel(rmsnorm_backward_kernel<2>, grid, block, stream, a); break;
-      default: e = launch_kernel(rmsnorm_backward_kernel<4>, grid, block, stream, a);
+      case 1: e = go(std::integral_constant<int, 1>{}); break;
+      case 2: e = go(std::integral_constant<int, 2>{}); break;
+      default: e = go(std::integral_constant<int, 4>{});
     }
   }
   if (e != hipSuccess || parts == 1) return e;
   // no rows: dg is zero
-  return launch_kernel(rmsnorm_weight_kernel, dim3((unsigned)(a.K / 64)), dim3(256), stream,
+  return launch_kernel(rmsnorm_weight_kernel, dim3((unsigned)(a.K / 64)), dim3(1024), stream,
                        static_cast<const float*>(workspace), (int)parts, a.K, dg);
 }
 
