@@ -5,16 +5,23 @@ updated weights, on the library's calls:
   up projection's epilogue applies bias and activation, keeps the
   pre-activation and emits the down projection's E4M3 input; the down
   projection's adds bias and residual;
+- or, with ``block="gated"``, pre-norm gated blocks ``y = x + W2 (act(Wg n) *
+  (Wu n))``, ``n = norm(x)``: the norm adds the residual and emits the E4M3 input
+  of the gated product, which keeps gate and up and emits the down projection's;
+  a last norm stands before the head;
 - a bf16 head whose cross entropy never stores the logits, and its gradients;
 - backward: the epilogues' backward emits the E4M3 operands of the FP8 data and
   weight gradients and the bias gradients; the data gradient's own epilogue
-  adds the gradient that came along the residual.
+  adds the gradient that came along the residual.  The gated product's backward
+  emits its operands and the down projection's in one pass, the norm's adds the
+  gradient along the residual.
 
 Embedding, the decoding of the kept activations and the Adam update are plain
 torch.
 
-Usage: ``python -m fp8_block_scaled_05_amd.train_step [--steps 60]`` trains it
-to predict a fixed permutation of the vocabulary and prints the losses.
+Usage: ``python -m fp8_block_scaled_05_amd.train_step [--steps 60] [--block
+gated]`` trains it to predict a fixed permutation of the vocabulary and prints
+the losses.
 """
 
 import argparse
@@ -32,6 +39,7 @@ class Config:
     inner: int = 512
     layers: int = 2
     act: str = "gelu"
+    block: str = "mlp"  # or "gated"
 
 
 def init(cfg, seed=0, device="cuda"):
@@ -43,6 +51,16 @@ def init(cfg, seed=0, device="cuda"):
 
     p = {"embedding": randn(cfg.vocab, cfg.hidden, std=1.0),
          "head": randn(cfg.vocab, cfg.hidden, std=cfg.hidden ** -0.5)}
+    if cfg.block not in ("mlp", "gated"):
+        raise ValueError(f"block must be 'mlp' or 'gated', got {cfg.block!r}")
+    if cfg.block == "gated":
+        for i in range(cfg.layers):
+            p[f"norm{i}"] = torch.ones(cfg.hidden, device=device)
+            # the gate's rows, then the up projection's
+            p[f"up{i}"] = randn(2 * cfg.inner, cfg.hidden, std=cfg.hidden ** -0.5)
+            p[f"down{i}"] = randn(cfg.hidden, cfg.inner, std=cfg.inner ** -0.5)
+        p["norm"] = torch.ones(cfg.hidden, device=device)
+        return p
     for i in range(cfg.layers):
         p[f"up{i}"] = randn(cfg.inner, cfg.hidden, std=cfg.hidden ** -0.5)
         p[f"up_bias{i}"] = torch.zeros(cfg.inner, device=device)
@@ -75,6 +93,8 @@ def loss_and_grads(cfg, p, tokens, target, ignore_index=-100):
     weights (fp32 where the library gives fp32)."""
     bf16 = torch.bfloat16
     x = p["embedding"][tokens].to(bf16)
+    if cfg.block == "gated":
+        return _gated_loss_and_grads(cfg, p, tokens, x, target, ignore_index)
     kept = []
     for i in range(cfg.layers):
         qx, sx = fp8bs.fp8_quant_act_1x128(x)
@@ -87,14 +107,8 @@ def loss_and_grads(cfg, p, tokens, target, ignore_index=-100):
                                           residual=x)
         kept.append((x, z, qh, sh, up, down))
         x = y
-    head = p["head"].to(bf16)
-    loss, lse = fp8bs.bf16_linear_xent(x, head, target, ignore_index)
-    counts = (target != ignore_index) & (target >= 0) & (target < cfg.vocab)
-    count = counts.sum().clamp_min(1).float()
-    dloss = torch.ones_like(loss) / count
-
     grads = {}
-    dy, grads["head"] = fp8bs.bf16_linear_xent_backward(x, head, target, lse, dloss, ignore_index)
+    loss, dy, grads["head"] = _head(cfg, p, x, target, ignore_index)
     for i in reversed(range(cfg.layers)):
         x, z, qh, sh, up, down = kept[i]
         q, s, qt, st, grads[f"down_bias{i}"] = fp8bs.fp8_quant_epilogue_backward(dy, None)
@@ -104,7 +118,55 @@ def loss_and_grads(cfg, p, tokens, target, ignore_index=-100):
         dy = fp8bs.fp8_block_gemm_epilogue(q, s, up[2], up[3], residual=dy)
         grads[f"up{i}"] = _weight_grad(qt, st, x)
     grads["embedding"] = torch.zeros_like(p["embedding"]).index_add_(0, tokens, dy.float())
-    return loss.sum() / count, grads
+    return loss, grads
+
+
+def _head(cfg, p, x, target, ignore_index):
+    """Mean loss, and the gradients of x and of the head's weight."""
+    head = p["head"].to(torch.bfloat16)
+    loss, lse = fp8bs.bf16_linear_xent(x, head, target, ignore_index)
+    counts = (target != ignore_index) & (target >= 0) & (target < cfg.vocab)
+    count = counts.sum().clamp_min(1).float()
+    dloss = torch.ones_like(loss) / count
+    dx, dhead = fp8bs.bf16_linear_xent_backward(x, head, target, lse, dloss, ignore_index)
+    return loss.sum() / count, dx, dhead
+
+
+def _gated_loss_and_grads(cfg, p, tokens, x, target, ignore_index):
+    """loss_and_grads of the pre-norm gated blocks."""
+    M, bf16 = x.shape[0], torch.bfloat16
+
+    def empty(*shape, dtype=bf16):
+        return torch.empty(*shape, dtype=dtype, device=x.device)
+
+    kept, branch = [], None  # of the block before, added by the next norm
+    for i in range(cfg.layers):
+        up = fp8bs.fp8_quant_w_128x128_t(p[f"up{i}"].to(bf16))
+        down = fp8bs.fp8_quant_w_128x128_t(p[f"down{i}"].to(bf16))
+        h, n, rstd = torch.empty_like(x), torch.empty_like(x), empty(M, dtype=torch.float32)
+        q, s = fp8bs.fp8_quant_rmsnorm(x, p[f"norm{i}"], residual=branch, h=h, y=n, rstd=rstd)
+        z = empty(M, 2 * cfg.inner)
+        qy, sy = fp8bs.fp8_block_gemm_gated_e4m3_out(q, s, up[0], up[1], act=cfg.act, z=z)
+        branch = fp8bs.fp8_block_gemm(qy, sy, down[0], down[1])
+        kept.append((h, n, rstd, z, up, down))
+        x = h
+    h, rstd = torch.empty_like(x), empty(M, dtype=torch.float32)
+    y = fp8bs.bf16_rmsnorm(x, p["norm"], residual=branch, h=h, rstd=rstd)
+
+    grads = {}
+    loss, dy, grads["head"] = _head(cfg, p, y, target, ignore_index)
+    dh, grads["norm"] = fp8bs.bf16_rmsnorm_backward(dy, h, rstd, p["norm"])
+    for i in reversed(range(cfg.layers)):
+        h, n, rstd, z, up, down = kept[i]
+        q, s, qt, st, _ = fp8bs.fp8_quant_epilogue_backward(dh, None)
+        dy = fp8bs.fp8_block_gemm(q, s, down[2], down[3])
+        q, s, zt, szt, yt, syt = fp8bs.fp8_quant_gated_backward(dy, z, cfg.act)
+        grads[f"down{i}"] = fp8bs.fp8_block_gemm_rowscaled(qt, st, yt, syt)
+        grads[f"up{i}"] = _weight_grad(zt, szt, n)
+        dn = fp8bs.fp8_block_gemm(q, s, up[2], up[3])
+        dh, grads[f"norm{i}"] = fp8bs.bf16_rmsnorm_backward(dn, h, rstd, p[f"norm{i}"], dh=dh)
+    grads["embedding"] = torch.zeros_like(p["embedding"]).index_add_(0, tokens, dh.float())
+    return loss, grads
 
 
 def update(p, grads, state, lr, betas=(0.9, 0.99), eps=1e-8):
@@ -134,8 +196,9 @@ def main():
     ap.add_argument("--steps", type=int, default=60)
     ap.add_argument("--rows", type=int, default=2000)
     ap.add_argument("--lr", type=float, default=0.01)
+    ap.add_argument("--block", choices=["mlp", "gated"], default="mlp")
     a = ap.parse_args()
-    cfg = Config()
+    cfg = Config(block=a.block, act="gelu" if a.block == "mlp" else "silu")
     p, state = init(cfg), {}
     for step in range(a.steps):
         loss, grads = loss_and_grads(cfg, p, *batch(cfg, a.rows, step))
