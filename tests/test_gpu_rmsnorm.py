@@ -137,6 +137,21 @@ def test_zero_tiny_and_huge_rows(fp8bs, K):
         check_codes(q[m:m + 1], s[:, m:m + 1], wy[m:m + 1])
 
 
+@pytest.mark.parametrize("eps", [1e20, 1e36, 3.4e38])
+def test_large_eps(fp8bs, eps):
+    """An eps that counts beside a mean of squares past FP32's range, and one that
+    leaves it together with the mean."""
+    eps = float(np.float32(eps))
+    x, _, g = inputs(5, 512, 1005)
+    x = (x.float() * torch.tensor([1.0, 1e10, 1e18, 1e19, 1e20], device="cuda")[:, None])
+    x = x.to(torch.bfloat16)
+    y, rstd = torch.empty_like(x), torch.empty(5, device="cuda")
+    q, s = fp8bs.fp8_quant_rmsnorm(x, g, eps, y=y, rstd=rstd)
+    wy, wr = rmsnorm.forward(gu.host_f64(x), gu.host_f64(g), eps)
+    assert np.all(np.abs(gu.host_f64(rstd) - wr) <= 2.0 ** -19 * wr)
+    assert np.all(np.abs(gu.host_f64(y) - wy) <= (2.0 ** -8 + 2 * REL) * np.abs(wy))
+
+
 @pytest.mark.parametrize("M,K", [(1, 7168), (70, 512), (33, 2048)])
 def test_strides_and_untouched_memory(fp8bs, M, K):
     x, r, g = inputs(M, K + 48, 1002)
