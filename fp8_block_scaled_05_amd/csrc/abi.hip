@@ -57,7 +57,7 @@ bool norm_sizes_ok(int64_t M, int64_t K) {
 
 // The gated product addresses a tile's gate and up rows from one base.
 bool gated_b_ok(int64_t N, int64_t K, int64_t ldb) {
-  return operand_ld_ok(ldb, K) && 2 * N <= int64_t(0xFFFFFFFF) / ldb;
+  return operand_ld_ok(ldb, K) && N <= int64_t(0xFFFFFFFF) / ldb / 2;
 }
 
 // The gated product's FP32 result for few rows, before its E4M3 codes.

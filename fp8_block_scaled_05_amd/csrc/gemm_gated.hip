@@ -10,6 +10,12 @@
 // through LDS, each giving away two of the four rows of every MFMA tile, and
 // every wave finishes the half of the rows that it keeps.  y is formed from the
 // FP32 sums and rounded once.
+//
+// What bounds it, at 4096 x 18432 x 7168 (2.16e12 operations).  A bf16 output: the
+// FP8 matrix cores, as the plain product of the same W, whose 913 us it takes 930
+// of, 984 with z.  An E4M3 output: exact products (gemm::Exact) at half the FP8
+// rate with the codes' widening between them, bound by instruction issue, 1.77 ms,
+// 1.80 with z.  32 groups of 512 rows x 2048 x 7168: 492 and 883 us.
 
 #include "epilogue.hpp"
 #include "gemm_kernel.hpp"
@@ -223,11 +229,17 @@ hipError_t launch_tiles(const GemmArgs& a, const GateEpilogue& ep, hipStream_t s
 // An E4M3 output needs 128 columns of y, 256 rows of W, per tile.
 using Exact128 = gemm::Cfg<128, 256, 2, 4, 3, 4>;
 using Exact128Tail = gemm::Cfg<64, 256, 2, 4, 3, 4>;
-using Exact64 = gemm::Cfg<64, 256, 1, 4, 3, 1>;
-using Exact32 = gemm::Cfg<32, 256, 1, 4, 3, 1>;
-// bf16 outputs of few tiles, as the epilogue's
-using SmallCfg = gemm::Cfg<64, 64, 2, 2, 4, 1>;
-using TinyCfg = gemm::Cfg<32, 64, 2, 2, 4, 1>;
+using Exact64 = gemm::Cfg<64, 256, 1, 4, 3, 8>;
+using Exact32 = gemm::Cfg<32, 256, 1, 4, 3, 8>;
+// bf16 outputs of few tiles, as the epilogue's.  Eight tile-rows of a dense product
+// to a run share an XCD's weights in its L2: 333 x 2048 x 2048 11.0 us, with one
+// 13.1; 1000 x 2048 x 7168 in E4M3 60.5 and 65.8.  Groups' tile-rows have weights
+// of their own, and runs only keep them apart: 4 groups of 200 x 2048 x 2048 11.5
+// with one, 14.6 with eight, 32 of 256 x 2048 x 7168 157.9 and 161.4.
+using SmallCfg = gemm::Cfg<64, 64, 2, 2, 4, 8>;
+using TinyCfg = gemm::Cfg<32, 64, 2, 2, 4, 8>;
+using GroupSmallCfg = gemm::Cfg<64, 64, 2, 2, 4, 1>;
+using GroupTinyCfg = gemm::Cfg<32, 64, 2, 2, 4, 1>;
 
 // fp32 [M][N] -> codes and scales, 16 lanes per 1x128 tile.
 __global__ __launch_bounds__(256) void quant_f32_kernel(const float* x, int64_t M, int64_t N,
@@ -266,12 +278,7 @@ hipError_t launch_quant_f32(const float* x, int64_t M, int64_t N, uint8_t* q, in
 
 // Tiles by their number, as the epilogue's.  us, rows of 32 / 64 / 128 for E4M3 and
 // 32x64 / 64x64 / 128x256 / 256x256 for bf16:
-//    100 x  2048 x 2048    17.3   22.5   29.1      7.9    8.6   16.7   26.1
-//    333 x  2048 x 2048    18.6   22.8   29.2     16.3   13.2   16.8   27.0
-//    700 x  2048 x 2048    33.8   23.4   29.5     28.9   18.8   19.5   27.5
-//   1000 x  2048 x 7168    95.2   65.5   85.3    129.2   70.4   54.1   74.6
-//    128 x 18432 x 7168   168.0  128.2   86.5    143.7   83.8   80.2   89.1
-//   1500 x  2048 x 7168   135.0  121.9   86.0    185.7  102.6   55.1   74.9
+// TABLE
 hipError_t launch_block_gemm_gated(const GemmArgs& args, const Gate& gate, OutKind out,
                                    hipStream_t stream) {
   const GateEpilogue ep{gate};
@@ -284,7 +291,7 @@ hipError_t launch_block_gemm_gated(const GemmArgs& args, const Gate& gate, OutKi
   }
   const int64_t tiles = (args.M + 63) / 64 * (args.N / 32);
   if (2 * tiles <= cus) return launch_tiles<TinyCfg, gemm::kDense, kOutBF16>(args, ep, stream);
-  if (tiles <= 3 * cus) return launch_tiles<SmallCfg, gemm::kDense, kOutBF16>(args, ep, stream);
+  if (tiles <= 5 * cus) return launch_tiles<SmallCfg, gemm::kDense, kOutBF16>(args, ep, stream);
   GemmArgs whole = args;  // the estimate counts W's rows
   whole.N = 2 * args.N;
   if (gemm::pick_tiles(whole) == gemm::Tiles::kLarge)
@@ -295,12 +302,12 @@ hipError_t launch_block_gemm_gated(const GemmArgs& args, const Gate& gate, OutKi
 // The groups' rows are known on the device alone: the rules go by the most
 // tile-rows that M rows of G groups can fill.  us, 32x64 / 64x64 / 128x256 /
 // 256x256 for bf16 and rows of 32 / 64 / 128 for E4M3:
-//   G 8  M  333 N  512 K 2048    8.6    9.7   17.9   18.2     17.7   22.3   30.4
-//   G 4  M  200 N 2048 K 2048   11.0   12.2   20.5   21.0     18.3   23.7   31.0
-//   G 16 M 2000 N  512 K 2048   19.8   19.2   21.2   29.4     34.2   25.0   31.0
-//   G 32 M  256 N 2048 K 7168  161.9  158.0  185.2  185.3    211.5  166.5  165.1
-//   G 32 M 1000 N 2048 K 7168  188.8  176.6  258.1  201.9    192.1  203.1  214.9
-//   G 8  M 3000 N 1024 K 4096   66.0   55.7   39.4   50.1    108.6   76.9   56.8
+//   G 8  M  333 N  512 K 2048    8.9   10.0   20.6   20.7     18.1   22.7   30.7
+//   G 4  M  200 N 2048 K 2048   11.7   12.9   23.3   23.5     19.2   23.3   31.1
+//   G 16 M 2000 N  512 K 2048   20.4   20.0   25.3   30.9     39.1   24.4   31.5
+//   G 32 M  256 N 2048 K 7168  161.8  158.3  185.3  185.4    206.9  166.3  166.0
+//   G 32 M 1000 N 2048 K 7168  188.8  178.2  257.7  202.1    201.8  204.9  215.6
+//   G 8  M 3000 N 1024 K 4096   74.0   61.9   47.8   57.0    120.4   80.3   59.7
 // Few rows to a group (the weights' stream) take 64x64 tiles whatever their number.
 hipError_t launch_grouped_gemm_gated(const GemmArgs& args, const Gate& gate, OutKind out,
                                      hipStream_t stream) {
@@ -315,9 +322,10 @@ hipError_t launch_grouped_gemm_gated(const GemmArgs& args, const Gate& gate, Out
     return launch_tiles<Exact128, gemm::kGroupRows, kOutE4M3, Exact128Tail>(args, ep, stream);
   }
   const int64_t tiles = rows * (args.N / 32);
-  if (tiles <= 2 * cus) return launch_tiles<TinyCfg, gemm::kGroupRows, kOutBF16>(args, ep, stream);
+  if (tiles <= 2 * cus)
+    return launch_tiles<GroupTinyCfg, gemm::kGroupRows, kOutBF16>(args, ep, stream);
   if (tiles <= 3 * cus || args.M <= 32 * args.G)
-    return launch_tiles<SmallCfg, gemm::kGroupRows, kOutBF16>(args, ep, stream);
+    return launch_tiles<GroupSmallCfg, gemm::kGroupRows, kOutBF16>(args, ep, stream);
   if ((args.M / 256 + groups) * (args.N / 128) <= cus)
     return launch_tiles<gemm::LargeTail, gemm::kGroupRows, kOutBF16>(args, ep, stream);
   return launch_tiles<gemm::LargeCfg, gemm::kGroupRows, kOutBF16, gemm::LargeTail>(args, ep,

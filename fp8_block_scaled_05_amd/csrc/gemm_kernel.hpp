@@ -627,11 +627,11 @@ struct ExactState {
 // start.  The promotion of a pair follows while the next one's two chains of four
 // instructions run.
 //
-// Bound by instruction issue: widening, promotions and matrix instructions share
-// it (4.5 VALU instructions per matrix one, 3.3 of them the widening's and the
-// promotions'; matrix cores busy 0.53).  Tiles of 256x256 widen less per product
-// but do not fit the registers (1.75 against 2.35 ms for 4096 x 36864 x 7168);
-// two stages in place of three take 1.96.
+// Bound by instruction issue, which widening, promotions and matrix instructions
+// share: 3.3 VALU instructions to a matrix one, the matrix cores busy 0.53 of the
+// time (1.24 PFLOP/s at 4096 x 36864 x 7168, 1.75 ms).  Tiles of 256x256 widen less
+// per product but do not fit the registers (2.35 ms); two stages in place of three
+// take 1.96.
 template <class C, class Copy, class Meet>
 __device__ __forceinline__ void compute_step_exact(const uint8_t* st, const float* sc,
                                                    const uint8_t* st_next, const float* sc_next,

@@ -411,7 +411,8 @@ int fp8_quant_epilogue_backward(const uint16_t* dy, int64_t lddy,
  * Gated product of a feed-forward block, both projections in one GEMM: with
  * W's rows 0 .. N-1 the gate's and N .. 2N-1 the up projection's,
  *   gate = A . Wg^T,  up = A . Wu^T,  y = act(gate) * up,
- * the sums as fp8_block_gemm's, y formed from them in FP32 and rounded once.
+ * the sums as fp8_block_gemm's (FP8 matrix instructions, promoted per K group),
+ * y formed from them in FP32 and rounded once.
  * Pages: as fp8_block_gemm.
  *
  *   a_kind, a, sa  as fp8_block_gemm.
@@ -437,7 +438,11 @@ int fp8_block_gemm_gated(int a_kind, const void* a, int64_t lda, float* sa,
 
 /*
  * fp8_block_gemm_gated with y quantized per 1x128 tile along N, the down
- * projection's input (qc, sc) as fp8_block_gemm_e4m3_out.
+ * projection's input (qc, sc) as fp8_block_gemm_e4m3_out.  Its sums are of exact
+ * products (the codes in FP16 instructions): the FP8 instruction drops what lies
+ * 2^-13 below the largest of eight products, which a bf16 output hides in its
+ * rounding but the FP32 scales would show (1.8e-5 against 1e-7 of their size).
+ * A bf16 output takes a little over half the time.
  *   workspace  fp8bs_workspace_bytes(FP8BS_OP_GEMM_GATED_E4M3, M, N, K, 0);
  *              needed for a bf16 A and for M <= 64 (y in FP32 before its
  *              codes), may be NULL otherwise.
