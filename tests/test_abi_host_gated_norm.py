@@ -32,6 +32,7 @@ def test_gated_gemm():
         assert gemm(**{k: v}) == fp8bs.ERR_LAYOUT, (k, v)
     # W within 32-bit offsets
     assert gemm(N=1 << 20, ldb=2048, ldc=1 << 20) == fp8bs.ERR_LAYOUT
+    assert gemm(N=1 << 62, ldc=1 << 62) == fp8bs.ERR_LAYOUT
     assert gemm(z=P, ldz=255) == fp8bs.ERR_LAYOUT and gemm(z=P + 1, ldz=256) == fp8bs.ERR_LAYOUT
     need = fp8bs.workspace_bytes(fp8bs.OP_GEMM_BF16, 64, 128, 256)
     assert gemm(a_kind=1, sa=0) == fp8bs.ERR_WORKSPACE
