@@ -297,6 +297,41 @@ def test_grouped_bad_offsets_stay_inside(fp8bs):
         assert torch.all(buf[0] == 9) and torch.all(buf[301] == 9)
 
 
+@pytest.mark.parametrize("M", [60, 400, 5000])
+def test_grouped_graph_follows_the_offsets(fp8bs, M):
+    """A captured call takes the offsets that the device holds at its replay."""
+    N, K, G = 256, 384, 5
+    cuts = np.random.default_rng(6)
+    qx, sx, qw, sw, off = experts(fp8bs, [M] + [0] * (G - 1), N, K, 1111)
+    y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    qc, sc = torch.empty(M, N, dtype=torch.uint8, device="cuda"), torch.empty(2, M, device="cuda")
+
+    def step():
+        fp8bs.fp8_block_grouped_gemm_gated(qx, sx, qw, sw, off, out=y)
+        fp8bs.fp8_block_grouped_gemm_gated_e4m3_out(qx, sx, qw, sw, off, qc=qc, sc=sc)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(4):
+        inner = np.sort(cuts.integers(0, M + 1, G - 1))
+        off.copy_(torch.tensor([0, *inner, M], dtype=torch.int32))
+        y.fill_(5.0)
+        sc.fill_(5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (y, qc, sc)]
+        step()
+        assert all(torch.equal(a, b) for a, b in zip(got, (y, qc, sc)))
+    # an expert's rows by themselves (few rows of a dense call are summed in another order)
+    g = int(np.argmax(np.diff([0, *inner, M])))
+    lo, hi = (int(c) for c in [0, *inner, M][g:g + 2])
+    one = torch.tensor([0, hi - lo], dtype=torch.int32, device="cuda")
+    assert same(y[lo:hi], fp8bs.fp8_block_grouped_gemm_gated(
+        qx[lo:hi], sx[:, lo:hi], qw[g:g + 1], sw[g:g + 1], one))
+
+
 def test_graph_and_streams(fp8bs):
     """Captured and replayed between eager calls; calls on two streams at once."""
     M, N, K = 40, 512, 640
