@@ -14,8 +14,9 @@
 // What bounds it, at 4096 x 18432 x 7168 (2.16e12 operations).  A bf16 output: the
 // FP8 matrix cores, as the plain product of the same W, whose 913 us it takes 930
 // of, 984 with z.  An E4M3 output: exact products (gemm::Exact) at half the FP8
-// rate with the codes' widening between them, bound by instruction issue, 1.77 ms,
-// 1.80 with z.  32 groups of 512 rows x 2048 x 7168: 492 and 883 us.
+// rate with the codes' widening between them, bound by instruction issue and board
+// power, 1.77 ms, 1.80 with z (a plain FP16 product of these sizes by the installed
+// BLAS 1.76).  32 groups of 512 rows x 2048 x 7168: 492 and 883 us.
 
 #include "epilogue.hpp"
 #include "gemm_kernel.hpp"
