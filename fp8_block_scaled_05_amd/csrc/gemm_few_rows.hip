@@ -31,7 +31,10 @@
 //   faster, so larger bf16 A is quantized first.
 // - few_rows_shared_kernel (32 < M <= 64, E4M3 A): the four waves share
 //   each K group's stage, which also holds the group's A codes and scales,
-//   and wave w takes A rows 16 w .. 16 w + 15.
+//   and wave w takes A rows 16 w .. 16 w + 15.  Products widened to FP16 (the
+//   gated product's E4M3 output) stay with the first kernel there: a wave of
+//   its own K group widens W once for all rows, where the shared kernel's four
+//   waves would each widen all of it.
 
 // Built with -mllvm -amdgpu-mfma-vgpr-form (build.py): one wave per SIMD may
 // hold 512 registers, and the compiler would otherwise write every MFMA
@@ -98,8 +101,8 @@ struct FewCfg {
   // scale)
   static constexpr int NA = FUSED ? 4 * MT : 3 * MT;
   // A loads in flight ahead of their use: two groups when their registers
-  // are few, one for the bf16 A of four tiles
-  static constexpr int ADIST = (FUSED && MT > 2) ? 1 : 2;
+  // are few, one for four tiles
+  static constexpr int ADIST = MT > 2 ? 1 : 2;
   static_assert(kStages * STAGE_BYTES <= 160 * 1024, "LDS budget");
   static_assert(ADIST * RC + (ADIST - 1) * NA <= 63, "vmcnt range");
 };
@@ -392,6 +395,50 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_kteam_kernel(FewArgs p, 
         swh = g & 1 ? uh : swh;
       }
       const uint8_t* st = stages[U];
+      // copies that go out with a row tile of W
+      constexpr int PW = (RC + RT - 1) / RT;
+      if constexpr (MODE == kGatedExact && MT > 1) {
+        // each operand is widened once: all of A first, W's tiles as they come
+        gemm::f16x8 aw[MT][4];
+        float fa[MT];
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          const ARegs<false>& ar = abuf[Bf][j];
+          fa[j] = ar.s;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            aw[j][q] = gemm::widen8((int)ar.v[q / 2][2 * (q & 1)], (int)ar.v[q / 2][2 * (q & 1) + 1]);
+          issue_a_tile(t + C::ADIST, j, abuf[Bf][j]);
+        }
+        auto promote = [&](const v4f& v, int i, int j) {
+          const float f = fa[j] * (use_hi[i] ? swh : swl);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(v[r], f, acc[i][j][r]);
+        };
+        v8i raw = gemm::load_frag(st, f_lo, f_hi, 0);
+        v4f prev = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          gemm::f16x8 ww[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) ww[q] = gemm::widen8(raw[2 * q], raw[2 * q + 1]);
+          if (i + 1 < RT) raw = gemm::load_frag(st, f_lo, f_hi, (i + 1) * 2048);
+          issue_w(t + 3, stages[(U + 3) % kStages], i * PW, (i + 1) * PW);
+#pragma unroll
+          for (int j = 0; j < MT; ++j) {
+            v4f cur = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              cur = __builtin_amdgcn_mfma_f32_16x16x32_f16(ww[q], aw[j][q], cur, 0, 0, 0);
+            // the promotion follows the next product
+            if (i + j > 0) promote(prev, j > 0 ? i : i - 1, (j + MT - 1) % MT);
+            prev = cur;
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        promote(prev, RT - 1, MT - 1);
+        return;
+      }
       v8i wf[RT];
 #pragma unroll
       for (int i = 0; i < RT; ++i) wf[i] = gemm::load_frag(st, f_lo, f_hi, i * 2048);
@@ -416,7 +463,6 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_kteam_kernel(FewArgs p, 
         // with the last tile of A, the copies of group t + 3 (into the stage
         // read one group ago) are spread over the MFMAs, after every A load
         // of the step as the wait counts assume
-        constexpr int PW = (RC + RT - 1) / RT;
         v4f prev;
 #pragma unroll
         for (int i = 0; i <= RT; ++i) {
@@ -683,7 +729,7 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_shared_kernel(FewArgs p,
       v4f cur;
       if (i < RT) {
         const v8i wf = gemm::load_frag(st, f_lo, f_hi, i * 2048);
-        cur = group_product<MODE == kGatedExact>(wf, af);
+        cur = group_product<false>(wf, af);
         __builtin_amdgcn_sched_barrier(0);
         issue(t + S - 1, nxt, i * PR, (i + 1) * PR);
         __builtin_amdgcn_sched_barrier(0);
@@ -782,19 +828,24 @@ hipError_t launch_mt(const FewArgs& p, Mode mode, const Epilogue& e, int cus, hi
     constexpr Mode kPlain = RC % 2 ? kStore : kGated;  // RC of 2 and 4: gated only
     constexpr Mode kLinear = RC % 2 ? kEpilogue : kGated;
     const dim3 block(kWaves * 64);
-    switch (mode) {
-      case kGated:
-        return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kGated>, grid, block, stream, p,
-                             e);
-      case kGatedExact:
-        return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kGatedExact>, grid, block,
-                             stream, p, e);
-      case kEpilogue:
-        return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kLinear>, grid, block, stream,
-                             p, e);
-      default:
-        return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kPlain>, grid, block, stream, p,
-                             e);
+    if constexpr (MT > 2) {  // exact products only
+      return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kGatedExact>, grid, block, stream,
+                           p, e);
+    } else {
+      switch (mode) {
+        case kGated:
+          return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kGated>, grid, block, stream, p,
+                               e);
+        case kGatedExact:
+          return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kGatedExact>, grid, block,
+                               stream, p, e);
+        case kEpilogue:
+          return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kLinear>, grid, block, stream,
+                               p, e);
+        default:
+          return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kPlain>, grid, block, stream, p,
+                               e);
+      }
     }
   });
 }
@@ -809,8 +860,6 @@ hipError_t launch_shared(const FewArgs& p, Mode mode, const Epilogue& e, int cus
     switch (mode) {
       case kGated:
         return launch_kernel(few_rows_shared_kernel<RC, kGated>, grid, block, stream, p, e);
-      case kGatedExact:
-        return launch_kernel(few_rows_shared_kernel<RC, kGatedExact>, grid, block, stream, p, e);
       case kEpilogue:
         return launch_kernel(few_rows_shared_kernel<RC, kLinear>, grid, block, stream, p, e);
       default:
@@ -829,6 +878,8 @@ hipError_t launch_few_rows(const FewArgs& p, bool fused, Mode mode, const Epilog
   }
   if (p.M <= 16) return launch_mt<1, false>(p, mode, e, cus, stream);
   if (p.M <= 32) return launch_mt<2, false>(p, mode, e, cus, stream);
+  if (p.M <= kFewRows && mode == kGatedExact)
+    return launch_mt<4, false>(p, mode, e, cus, stream);
   if (p.M <= kFewRows) return launch_shared(p, mode, e, cus, stream);
   return hipErrorInvalidValue;
 }
