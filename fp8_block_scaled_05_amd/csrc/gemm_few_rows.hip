@@ -798,73 +798,102 @@ __global__ __launch_bounds__(kWaves * 64) void few_rows_shared_kernel(FewArgs p,
 #endif
 }
 
-// Weight rows per workgroup (RC 8-row copies): the fewest that put the
-// whole W on at most one workgroup per compute unit, from a fixed set.  us for the
-// gated product of one row with RC 1 / 2 / 3 / 4 / 9:
-//   4096 x 7168   26.2  16.4  17.5  13.8  17.9
-//   2048 x 7168   15.0  11.1  11.4  11.6  16.2
-//   4096 x 2048    9.5   7.3   7.9   6.4   8.1
+// f(RC, grid) for RC 8-row copies, 8 RC weight rows, to a workgroup.
+template <int RC, class F>
+hipError_t with_rc(int64_t rows, F&& f) {
+  const int64_t blocks = (rows + 8 * RC - 1) / (8 * RC);
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  return f(std::integral_constant<int, RC>{}, dim3((unsigned)blocks));
+}
+
+// The fewest weight rows per workgroup that put the whole N on at most one
+// workgroup per compute unit, from a fixed set.
 template <class F>
-hipError_t with_rows(const FewArgs& p, Mode mode, int cus, F&& f) {
-  const int64_t rows = is_gated(mode) ? 2 * p.N : p.N;
-  const int64_t per = (rows + cus - 1) / cus;
-  auto go = [&](auto RC_) {
-    constexpr int RC = decltype(RC_)::value;
-    const int64_t blocks = (rows + 8 * RC - 1) / (8 * RC);
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    return f(RC_, dim3((unsigned)blocks));
-  };
-  if (per <= 8) return go(std::integral_constant<int, 1>{});
-  if (is_gated(mode) && per <= 16) return go(std::integral_constant<int, 2>{});
-  if (per <= 24) return go(std::integral_constant<int, 3>{});
-  if (is_gated(mode) && per <= 32) return go(std::integral_constant<int, 4>{});
-  return go(std::integral_constant<int, 9>{});
+hipError_t with_rows(const FewArgs& p, int cus, F&& f) {
+  const int64_t per = (p.N + cus - 1) / cus;
+  if (per <= 8) return with_rc<1>(p.N, f);
+  if (per <= 24) return with_rc<3>(p.N, f);
+  return with_rc<9>(p.N, f);
+}
+
+// The gated product.  Up to 72 weight rows per compute unit: one round of
+// workgroups that share them evenly.  Beyond: of 40 to 72 rows per workgroup those
+// whose rounds, of one workgroup per compute unit, take the fewest rows in turn.  us
+// with 32 / 40 / 48 / 56 / 64 / 72 rows, bf16 output, codes in:
+//    1 x  5120 x 5120    13.4  11.4  11.5  12.0  12.5  13.6
+//   64 x  5120 x 5120    26.1  18.0  18.9  20.1  20.1  22.5
+//    1 x 12288 x 4096    20.4  23.5  21.4  22.0  24.6  26.5
+//   64 x 12288 x 4096    32.2  36.5  28.6  31.3  31.3  35.4
+//   16 x 14336 x 7168    40.8  39.7  43.4  36.9  38.2  41.5
+//    1 x 28672 x 8192    72.2  78.7  77.7  78.4  91.7  91.4
+//   64 x 28672 x 8192   127.0 126.0 117.3 109.3 112.8 121.1
+//    1 x  8192 x 4096    14.2  16.4  18.0  20.2  18.1  16.9
+//   64 x  8192 x 4096    22.5  25.9  27.3  30.0  19.2  20.4
+// In place of one workgroup of 64 rows two of 32 fit a compute unit, and for up to
+// 16 rows of A their two streams are the better.
+template <class F>
+hipError_t with_gated_rows(const FewArgs& p, int cus, F&& f) {
+  const int64_t rows = 2 * p.N, per = (rows + cus - 1) / cus;
+  int64_t rc = (per + 7) / 8;
+  if (rc > 9) {
+    int64_t best = 0;
+    for (int c = 9; c >= 5; --c) {
+      const int64_t in_turn = (per + 8 * c - 1) / (8 * c) * c;
+      if (c == 9 || in_turn < best) best = in_turn, rc = c;
+    }
+  } else if (rc == 8 && p.M <= 16) {
+    rc = 4;
+  }
+  switch (rc) {
+    case 1: return with_rc<1>(rows, f);
+    case 2: return with_rc<2>(rows, f);
+    case 3: return with_rc<3>(rows, f);
+    case 4: return with_rc<4>(rows, f);
+    case 5: return with_rc<5>(rows, f);
+    case 6: return with_rc<6>(rows, f);
+    case 7: return with_rc<7>(rows, f);
+    case 8: return with_rc<8>(rows, f);
+    default: return with_rc<9>(rows, f);
+  }
 }
 
 template <int MT, bool FUSED>
 hipError_t launch_mt(const FewArgs& p, Mode mode, const Epilogue& e, int cus, hipStream_t stream) {
-  return with_rows(p, mode, cus, [&](auto RC_, dim3 grid) {
-    constexpr int RC = decltype(RC_)::value;
-    constexpr Mode kPlain = RC % 2 ? kStore : kGated;  // RC of 2 and 4: gated only
-    constexpr Mode kLinear = RC % 2 ? kEpilogue : kGated;
-    const dim3 block(kWaves * 64);
-    if constexpr (MT > 2) {  // exact products only
+  const dim3 block(kWaves * 64);
+  if (is_gated(mode))
+    return with_gated_rows(p, cus, [&](auto RC_, dim3 grid) {
+      constexpr int RC = decltype(RC_)::value;
+      if (MT <= 2 && mode == kGated)
+        return launch_kernel(few_rows_kteam_kernel<RC, MT <= 2 ? MT : 1, FUSED, kGated>, grid,
+                             block, stream, p, e);
       return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kGatedExact>, grid, block, stream,
                            p, e);
-    } else {
-      switch (mode) {
-        case kGated:
-          return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kGated>, grid, block, stream, p,
-                               e);
-        case kGatedExact:
-          return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kGatedExact>, grid, block,
-                               stream, p, e);
-        case kEpilogue:
-          return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kLinear>, grid, block, stream,
-                               p, e);
-        default:
-          return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kPlain>, grid, block, stream, p,
-                               e);
-      }
-    }
-  });
+    });
+  if constexpr (MT <= 2)
+    return with_rows(p, cus, [&](auto RC_, dim3 grid) {
+      constexpr int RC = decltype(RC_)::value;
+      if (mode == kEpilogue)
+        return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kEpilogue>, grid, block, stream,
+                             p, e);
+      return launch_kernel(few_rows_kteam_kernel<RC, MT, FUSED, kStore>, grid, block, stream, p,
+                           e);
+    });
+  return hipErrorInvalidValue;
 }
 
 hipError_t launch_shared(const FewArgs& p, Mode mode, const Epilogue& e, int cus,
                          hipStream_t stream) {
-  return with_rows(p, mode, cus, [&](auto RC_, dim3 grid) {
+  const dim3 block(kWaves * 64);
+  if (mode == kGated)
+    return with_gated_rows(p, cus, [&](auto RC_, dim3 grid) {
+      return launch_kernel(few_rows_shared_kernel<decltype(RC_)::value, kGated>, grid, block,
+                           stream, p, e);
+    });
+  return with_rows(p, cus, [&](auto RC_, dim3 grid) {
     constexpr int RC = decltype(RC_)::value;
-    constexpr Mode kPlain = RC % 2 ? kStore : kGated;  // RC of 2 and 4: gated only
-    constexpr Mode kLinear = RC % 2 ? kEpilogue : kGated;
-    const dim3 block(kWaves * 64);
-    switch (mode) {
-      case kGated:
-        return launch_kernel(few_rows_shared_kernel<RC, kGated>, grid, block, stream, p, e);
-      case kEpilogue:
-        return launch_kernel(few_rows_shared_kernel<RC, kLinear>, grid, block, stream, p, e);
-      default:
-        return launch_kernel(few_rows_shared_kernel<RC, kPlain>, grid, block, stream, p, e);
-    }
+    if (mode == kEpilogue)
+      return launch_kernel(few_rows_shared_kernel<RC, kEpilogue>, grid, block, stream, p, e);
+    return launch_kernel(few_rows_shared_kernel<RC, kStore>, grid, block, stream, p, e);
   });
 }
 

@@ -105,14 +105,16 @@ def same(a, b):
     return torch.equal(a.view(torch.int16), b.view(torch.int16))
 
 
-# few-row kernels (one, two and shared row tiles; 8, 16, 24, 32 and 72 weight rows
-# per workgroup), ragged rows, odd numbers of 128-column blocks; K of one to seven
+# few-row kernels (one, two, four and shared row tiles; 8 to 72 weight rows per
+# workgroup, in one round of workgroups and two), ragged rows, odd numbers of 128-column blocks; K of one to seven
 # groups (fewer than the stages, every end of their turn)
 SHAPES = [(1, 128, 128), (1, 3456, 256), (3, 384, 1280), (2, 2048, 256), (16, 1152, 512),
           (16, 2816, 384), (16, 4096, 640), (17, 128, 384), (20, 1920, 256), (32, 3456, 128),
           (32, 3968, 256), (33, 896, 256), (50, 2048, 256), (64, 4224, 384), (65, 128, 128),
           (100, 256, 512), (129, 384, 256), (333, 2048, 640), (300, 8192, 256), (1100, 4096, 256),
-          (2100, 3968, 128)]
+          (2100, 3968, 128)] + [(m, n, 256) for m in (1, 16, 20, 33, 64)
+                                for n in (4608, 5248, 6784, 7552, 9088)] + [
+          (2, 12416, 128), (40, 10752, 128), (1, 19456, 128)]
 # tiles: E4M3 of 32, 64 and 128 rows, a last round in halves of 64; bf16 of 32x64,
 # 64x64, 128x256 and 256x256, a last round in halves of 128
 TILES = [(70, 1024, 768), (200, 4096, 896), (700, 2048, 384), (1000, 4096, 256), (1200, 8192, 128),
