@@ -80,6 +80,30 @@ __device__ __forceinline__ uint32_t cvt2_e4m3(float a, float b, uint32_t old) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, (int)old, HI);
 }
 
+// Two values of a group of FP32 results, scaled by its reciprocal, -> two E4M3
+// codes in one half of `old`.  With |x| <= a and r = RN32(448 / a) a finite |x r|
+// is at most 448.0001, which the convert takes to 448, so there is nothing to
+// clamp; a NaN, which the group's maximum leaves out and a clamp would make -448,
+// has the code of NaN, and so has an infinite value (r = 0).
+template <bool HI>
+__device__ __forceinline__ uint32_t codes2(float a, float b, uint32_t old) {
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, (int)old, HI);
+}
+
+// Eight of them, each under a reciprocal of its own (columns) or all under one.
+__device__ __forceinline__ u32x2 codes8(const float (&v)[8], const float (&r)[8]) {
+  uint32_t lo = codes2<false>(v[0] * r[0], v[1] * r[1], 0u);
+  lo = codes2<true>(v[2] * r[2], v[3] * r[3], lo);
+  uint32_t hi = codes2<false>(v[4] * r[4], v[5] * r[5], 0u);
+  hi = codes2<true>(v[6] * r[6], v[7] * r[7], hi);
+  return u32x2{lo, hi};
+}
+
+__device__ __forceinline__ u32x2 codes8(const float (&v)[8], float r) {
+  const float all[8] = {r, r, r, r, r, r, r, r};
+  return codes8(v, all);
+}
+
 // Quantize 8 bf16 values (one u32x4) with reciprocal r -> 8 codes (u32x2).
 __device__ __forceinline__ u32x2 quant8(const u32x4 v, float r) {
   uint32_t lo = cvt2_e4m3<false>(bf16_lo(v.x) * r, bf16_hi(v.x) * r, 0u);

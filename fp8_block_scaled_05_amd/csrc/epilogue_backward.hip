@@ -38,14 +38,6 @@ struct BackwardArgs {
   float* part;  // [ceil(M/128)][N] column sums
 };
 
-// Two values -> two E4M3 codes in one half of `old`.  With |x| <= a and r =
-// RN32(448 / a) a finite |x r| is at most 448.0001, which the convert takes to
-// 448, so there is nothing to clamp.
-template <bool HI>
-__device__ __forceinline__ uint32_t codes2(float a, float b, uint32_t old) {
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, (int)old, HI);
-}
-
 // v of lane i (compile time) of the 16 lanes of this one's row.
 template <int I>
 __device__ __forceinline__ float of_row_lane(float v) {

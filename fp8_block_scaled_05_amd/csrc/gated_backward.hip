@@ -25,22 +25,6 @@ namespace fp8bs {
 
 namespace {
 
-// Two values -> two E4M3 codes in one half of `old`.  With |x| <= a and r =
-// RN32(448 / a) a finite |x r| is at most 448.0001, which the convert takes to
-// 448, so there is nothing to clamp.
-template <bool HI>
-__device__ __forceinline__ uint32_t codes2(float a, float b, uint32_t old) {
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, (int)old, HI);
-}
-
-__device__ __forceinline__ u32x2 codes8(const float (&v)[8], const float (&r)[8]) {
-  uint32_t lo = codes2<false>(v[0] * r[0], v[1] * r[1], 0u);
-  lo = codes2<true>(v[2] * r[2], v[3] * r[3], lo);
-  uint32_t hi = codes2<false>(v[4] * r[4], v[5] * r[5], 0u);
-  hi = codes2<true>(v[6] * r[6], v[7] * r[7], hi);
-  return u32x2{lo, hi};
-}
-
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
 constexpr int kRows = 4;     // rows per thread, 32 apart
@@ -125,8 +109,7 @@ __device__ __forceinline__ void store_rows(const float (&v)[kRows][8], int64_t r
     float sc, r;
     group_scale(max_row16(m), sc, r);
     const int64_t row = row0 + 32 * i;
-    const float rr[8] = {r, r, r, r, r, r, r, r};
-    const u32x2 w = codes8(v[i], rr);
+    const u32x2 w = codes8(v[i], r);
     if (row < M) {
       __builtin_nontemporal_store(w, reinterpret_cast<u32x2*>(q + row * ldq + lane * 8));
       if (lane == 0) s[row] = sc;

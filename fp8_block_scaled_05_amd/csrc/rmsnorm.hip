@@ -150,11 +150,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a) {
       for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
       float s, r;
       group_scale(max_row16(m), s, r);
-      uint32_t lo = cvt2_e4m3<false>(f[0] * r, f[1] * r, 0u);
-      lo = cvt2_e4m3<true>(f[2] * r, f[3] * r, lo);
-      uint32_t hi = cvt2_e4m3<false>(f[4] * r, f[5] * r, 0u);
-      hi = cvt2_e4m3<true>(f[6] * r, f[7] * r, hi);
-      store_vec<STREAM>(u32x2{lo, hi}, a.q + row * a.ldq + col);
+      store_vec<STREAM>(codes8(f, r), a.q + row * a.ldq + col);
       if ((threadIdx.x & 15) == 0) a.s[(int64_t)(col / 128) * a.lds + row] = s;
     }
   }

@@ -935,7 +935,7 @@ def fp8_quant_rmsnorm(x, weight, eps=1e-6, residual=None, h=None, y=None, rstd=N
     bf16 ``x`` and ``residual`` [M][K], fp32 ``weight`` [K].  Optional outputs:
     ``h`` bf16 [M][K] (may be ``x`` or ``residual`` itself), ``y`` bf16 [M][K],
     ``rstd`` fp32 [M]; the backward pass (``bf16_rmsnorm_backward``) needs h and
-    rstd.  K is at most 32768.
+    rstd.  K is at most 32768.  A NaN in y has the code of NaN.
     """
     M, K, ldx, ldr, ldh, ldy = _norm_operands("fp8_quant_rmsnorm", x, weight, residual, h, y, rstd)
     _mat(q, "q", M, K, torch.uint8)

@@ -517,6 +517,9 @@ int fp8_quant_gated_backward(const uint16_t* dy, int64_t lddy,
  *   y = h rstd weight,
  * the FP32 y quantized per 1x128 tile as fp8_quant_act_1x128 does (its sums
  * and y are FP32; finite rows whose squares leave FP32 are summed scaled).
+ * A NaN in y has the code of NaN (0x7F or 0xFF) and stays out of its tile's
+ * maximum: all of a row with a NaN in it, and the infinite element of an h
+ * where x + residual left bf16's range (the rest of that row is 0).
  * Pages: as fp8_quant_act_1x128.
  *
  *   x       [in]  bf16 [M][ldx].
