@@ -159,7 +159,7 @@ struct GateEpilogue {
   }
 
   // As gemm::store_tile_e4m3 for the rows that the wave keeps: a row's 128
-  // columns are those of HW waves.
+  // columns are those of HW waves; a NaN keeps the code of NaN.
   template <class C>
   static __device__ __forceinline__ void store_codes(const GemmArgs& p, const gemm::TileCoords& t,
                                                      const v2f (&y)[C::FM][C::FN], int row0, int wc,
@@ -197,9 +197,9 @@ struct GateEpilogue {
         const int64_t row = t.row0 + row0 + 16 * i + r;
         if (row >= t.row_end) continue;
         const float f = rcp[row0 + 16 * i + r];
-        const uint32_t lo = cvt2_e4m3<false>(y[i][0][r] * f, y[i][1][r] * f, 0u);
+        const uint32_t lo = codes2<false>(y[i][0][r] * f, y[i][1][r] * f, 0u);
         *reinterpret_cast<uint32_t*>(out + row * p.ldc + col) =
-            cvt2_e4m3<true>(y[i][2][r] * f, y[i][3][r] * f, lo);
+            codes2<true>(y[i][2][r] * f, y[i][3][r] * f, lo);
       }
   }
 };
@@ -258,11 +258,7 @@ __global__ __launch_bounds__(256) void quant_f32_kernel(const float* x, int64_t 
   for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
   float sc, r;
   group_scale(max_row16(m), sc, r);
-  uint32_t lo = cvt2_e4m3<false>(v[0] * r, v[1] * r, 0u);
-  lo = cvt2_e4m3<true>(v[2] * r, v[3] * r, lo);
-  uint32_t hi = cvt2_e4m3<false>(v[4] * r, v[5] * r, 0u);
-  hi = cvt2_e4m3<true>(v[6] * r, v[7] * r, hi);
-  *reinterpret_cast<u32x2*>(q + row * ldq + col) = u32x2{lo, hi};
+  *reinterpret_cast<u32x2*>(q + row * ldq + col) = codes8(v, r);
   if ((threadIdx.x & 15) == 0) s[nb * lds + row] = sc;
 }
 

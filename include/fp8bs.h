@@ -442,6 +442,8 @@ int fp8_block_gemm_gated(int a_kind, const void* a, int64_t lda, float* sa,
  * products (the codes in FP16 instructions): the FP8 instruction drops what lies
  * 2^-13 below the largest of eight products, which a bf16 output hides in its
  * rounding but the FP32 scales would show (1.8e-5 against 1e-7 of their size).
+ * A NaN in y has the code of NaN (0x7F or 0xFF) and stays out of its tile's
+ * maximum.
  * A bf16 output takes a little over half the time.
  *   workspace  fp8bs_workspace_bytes(FP8BS_OP_GEMM_GATED_E4M3, M, N, K, 0);
  *              needed for a bf16 A and for M <= 64 (y in FP32 before its
