@@ -319,23 +319,40 @@ constexpr int64_t kStreamFrom = int64_t(1) << 21;
 
 }  // namespace
 
-hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t stream) {
-  const RowPlan p = row_plan(a.K);
+hipError_t launch_rmsnorm(const NormArgs& all, hipStream_t stream) {
+  const RowPlan p = row_plan(all.K);
   const int64_t rows = p.threads == 64 ? 4 : 1;  // per workgroup
-  const int64_t blocks = (a.M + rows - 1) / rows;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  const dim3 grid((unsigned)blocks), block((unsigned)p.threads, (unsigned)rows);
-  const bool stream_out = a.M * a.K >= kStreamFrom;
-  auto go = [&](auto V) {
-    constexpr int v = decltype(V)::value;
-    return stream_out ? launch_kernel(rmsnorm_kernel<v, true>, grid, block, stream, a)
-                      : launch_kernel(rmsnorm_kernel<v, false>, grid, block, stream, a);
-  };
-  switch (p.vecs) {
-    case 1: return go(std::integral_constant<int, 1>{});
-    case 2: return go(std::integral_constant<int, 2>{});
-    default: return go(std::integral_constant<int, 4>{});
+  const dim3 block((unsigned)p.threads, (unsigned)rows);
+  const bool stream_out = all.M * all.K >= kStreamFrom;
+  // a grid has fewer than 2^32 threads: rows past that go in further launches
+  const int64_t most = (int64_t(1) << 31) / p.threads * rows;
+  for (int64_t first = 0; first < all.M; first += most) {
+    NormArgs a = all;
+    a.M = all.M - first < most ? all.M - first : most;
+    a.x += first * a.ldx;
+    if (a.residual) a.residual += first * a.ldr;
+    if (a.h) a.h += first * a.ldh;
+    if (a.y) a.y += first * a.ldy;
+    if (a.rstd) a.rstd += first;
+    if (a.q) {
+      a.q += first * a.ldq;
+      a.s += first;
+    }
+    const dim3 grid((unsigned)((a.M + rows - 1) / rows));
+    auto go = [&](auto V) {
+      constexpr int v = decltype(V)::value;
+      return stream_out ? launch_kernel(rmsnorm_kernel<v, true>, grid, block, stream, a)
+                        : launch_kernel(rmsnorm_kernel<v, false>, grid, block, stream, a);
+    };
+    hipError_t e;
+    switch (p.vecs) {
+      case 1: e = go(std::integral_constant<int, 1>{}); break;
+      case 2: e = go(std::integral_constant<int, 2>{}); break;
+      default: e = go(std::integral_constant<int, 4>{});
+    }
+    if (e != hipSuccess) return e;
   }
+  return hipSuccess;
 }
 
 size_t rmsnorm_backward_workspace(int64_t M, int64_t K) {
