@@ -15,8 +15,10 @@
 // FP8 matrix cores, as the plain product of the same W, whose 913 us it takes 930
 // of, 984 with z.  An E4M3 output: exact products (gemm::Exact) at half the FP8
 // rate with the codes' widening between them, bound by instruction issue and board
-// power, 1.77 ms, 1.80 with z (a plain FP16 product of these sizes by the installed
-// BLAS 1.76).  32 groups of 512 rows x 2048 x 7168: 492 and 883 us.
+// power, 1.75 to 1.90 ms with z by the clock that a card holds, 0.03 less without (a
+// plain FP16 product of these sizes by the installed BLAS 1.76).  32 groups of 512
+// rows x 2048 x 7168: 492 and 883 us.  The 256x256 kernels keep a few registers in
+// scratch (10 dense, 24 grouped), outside their K loop.
 
 #include "epilogue.hpp"
 #include "gemm_kernel.hpp"
@@ -273,9 +275,22 @@ hipError_t launch_quant_f32(const float* x, int64_t M, int64_t N, uint8_t* q, in
                        ldq, s, lds);
 }
 
-// Tiles by their number, as the epilogue's.  us, rows of 32 / 64 / 128 for E4M3 and
-// 32x64 / 64x64 / 128x256 / 256x256 for bf16:
-// TABLE
+// Tiles by their number, as the epilogue's.  us, each call after one with other
+// weights, rows of 32 / 64 / 128 for E4M3 and 32x64 / 64x64 / 128x256 / 256x256 for
+// bf16:
+//    100 x  2048 x 2048     17.0   21.6   29.6      7.8    8.6   19.7   26.7
+//    333 x  2048 x 2048     17.8   22.0   29.6     12.2   11.5   19.7   27.8
+//    512 x  2048 x 2048     18.0   22.1   29.6     15.9   11.8   19.7   27.6
+//    576 x  2048 x 2048     32.0   21.9   29.5     17.6   16.9   19.9   27.6
+//    250 x  2048 x 7168     44.1   58.2   84.2     21.9   18.8   53.7   74.7
+//   1000 x  2048 x 7168     90.5   60.4   84.1     66.7   51.3   54.3   77.8
+//   1100 x  2048 x 7168    125.7  114.3   84.8     76.1   63.3   55.5   78.1
+//   1500 x  2048 x 7168    128.7  120.1   86.2     98.5   76.8   68.4   86.4
+//     70 x 18432 x 7168    100.4  116.7   86.4     86.1   75.8   87.0   96.0
+//    128 x 18432 x 7168    145.8  119.5   89.9    108.8   90.4   90.9   98.3
+//    200 x 18432 x 7168    188.1  174.9  149.8    165.3  125.4  158.7  101.3
+// The bf16 rule loses where 64x64 tiles pass four to a compute unit over a long K
+// (1100 rows).
 hipError_t launch_block_gemm_gated(const GemmArgs& args, const Gate& gate, OutKind out,
                                    hipStream_t stream) {
   const GateEpilogue ep{gate};
@@ -299,13 +314,16 @@ hipError_t launch_block_gemm_gated(const GemmArgs& args, const Gate& gate, OutKi
 // The groups' rows are known on the device alone: the rules go by the most
 // tile-rows that M rows of G groups can fill.  us, 32x64 / 64x64 / 128x256 /
 // 256x256 for bf16 and rows of 32 / 64 / 128 for E4M3:
-//   G 8  M  333 N  512 K 2048    8.9   10.0   20.6   20.7     18.1   22.7   30.7
-//   G 4  M  200 N 2048 K 2048   11.7   12.9   23.3   23.5     19.2   23.3   31.1
-//   G 16 M 2000 N  512 K 2048   20.4   20.0   25.3   30.9     39.1   24.4   31.5
-//   G 32 M  256 N 2048 K 7168  161.8  158.3  185.3  185.4    206.9  166.3  166.0
-//   G 32 M 1000 N 2048 K 7168  188.8  178.2  257.7  202.1    201.8  204.9  215.6
-//   G 8  M 3000 N 1024 K 4096   74.0   61.9   47.8   57.0    120.4   80.3   59.7
-// Few rows to a group (the weights' stream) take 64x64 tiles whatever their number.
+//   G 8  M  333 N  512 K 2048    8.8   10.0   20.7   20.8     18.0   22.7   30.8
+//   G 4  M  200 N 2048 K 2048   12.1   13.4   25.0   25.2     19.4   23.4   31.5
+//   G 16 M 2000 N  512 K 2048   21.2   20.5   27.2   32.6     39.1   24.5   31.5
+//   G 32 M  256 N 2048 K 7168  162.3  158.6  185.4  185.5    207.1  166.2  165.7
+//   G 32 M 1000 N 2048 K 7168  189.3  178.0  258.2  203.2    196.8  205.9  216.2
+//   G 32 M 2048 N 2048 K 7168  265.4  223.8  261.8  268.6    324.7  227.9  235.8
+//   G 8  M 3000 N 1024 K 4096   76.5   64.8   51.9   60.3    122.1   80.5   59.2
+// Few rows to a group (the weights' stream) take 64x64 tiles whatever their number,
+// in bf16 up to 32 rows to a group.  The rules lose at 64 rows to a group (bf16 269
+// us where 224 could be) and, in E4M3, at 32 to 64 (216 where 197, 236 where 228).
 hipError_t launch_grouped_gemm_gated(const GemmArgs& args, const Gate& gate, OutKind out,
                                      hipStream_t stream) {
   const GateEpilogue ep{gate};

@@ -629,10 +629,11 @@ struct ExactState {
 //
 // Bound by instruction issue and board power: 3.3 VALU instructions to a matrix
 // one, the matrix cores busy 0.55 of the time at 2.1 GHz (1.2 PFLOP/s at 4096 x
-// 36864 x 7168, 1.77 ms); the LDS reads, widening, products and promotions alone
-// reach 0.62 at 2.2, busier orders of them hold lower clocks.  Other orders and wave
-// priorities are within 1%.  Tiles of 256x256 widen less per product but do not fit
-// the registers (2.35 ms); two stages in place of three take 1.96.
+// 36864 x 7168, 1.77 ms; up to 1.87 on cards that hold less); the LDS reads,
+// widening, products and promotions alone reach 0.62 at 2.2, busier orders of them
+// hold lower clocks.  Other orders and wave priorities are within 1%.  Tiles of
+// 256x256 widen less per product but do not fit the registers (2.35 ms); two stages
+// in place of three take 1.96.
 template <class C, class Copy, class Meet>
 __device__ __forceinline__ void compute_step_exact(const uint8_t* st, const float* sc,
                                                    const uint8_t* st_next, const float* sc_next,

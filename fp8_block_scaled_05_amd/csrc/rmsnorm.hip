@@ -13,8 +13,10 @@
 //
 // At 4096 x 7168: forward 36 us, 42 with y and rstd (6.2 TB/s of 265 MB; a large
 // copy reaches 5.2), bf16 output alone 19 (its operands lie in the last-level
-// cache), backward 49 (4.8 TB/s of 235 MB).  One row 4 us: a
-// load, a sum over the row's waves and a store in turn.
+// cache), backward 49 (4.8 TB/s of 235 MB).  One row 4 us: a load, a sum over the
+// row's waves and a store in turn.  Rows past 16384 (four loads per thread): forward
+// 5.2 to 5.8 TB/s, backward 3.1 to 3.7, one workgroup to a compute unit with 44 of
+// its registers in scratch (2048 x 32768 167 us; 4096 x 16384 98, 5.5 TB/s).
 
 #include "device.hpp"
 #include "internal.hpp"

@@ -805,7 +805,9 @@ def fp8_block_gemm_gated_e4m3_out(a, sa, b, sb, act="silu", z=None, qc=None, sc=
     """As ``fp8_block_gemm_gated``, with the result quantized per 1x128 tile
     along N: returns ``(qc, sc)`` as ``fp8_block_gemm_e4m3_out``.  The sums are of
     exact products, so that the scales are right to FP32; large products take
-    nearly twice the bf16 output's time."""
+    nearly twice the bf16 output's time, and past 16 rows that output and
+    ``fp8_quant_act_1x128`` are together mostly the faster way to an operand whose y
+    is rounded to bf16 in between.  A NaN in y has the code of NaN."""
     a_kind, M, N2, K, lda, ldsa, ldb = _dense_operands("fp8_block_gemm_gated_e4m3_out", a, sa, b,
                                                        sb)
     N = _gated_columns(N2, "fp8_block_gemm_gated_e4m3_out")
